@@ -426,3 +426,17 @@ def tl_unscale_norm_noalloc(numel: Sequence[int], accs, S: float, max_norm: floa
                                      ctypes.c_void_p(int(out_addr)), _stream(stream))
     if rc != TL_OK:
         raise TLError("tl_unscale_norm_noalloc", rc, lib.tl_status_string(rc).decode())
+
+
+_LOSSES = ("tl_loss_create", "tl_loss_destroy", "tl_loss_launch_count", "tl_token_logprob", "tl_policy_loss",
+           "tl_preference_loss", "tl_distill_loss", "LossContext", "LOSS_EXPORTED", "tl_logits", "tl_loss_result",
+           "tl_loss_out", "tl_policy_args", "tl_preference_args", "tl_distill_args")
+
+
+def __getattr__(name: str):
+    """The objectives over logits (losses.py) import torch, which the optimizer step's
+    binding does without until a stream is needed: they are loaded when first used."""
+    if name in _LOSSES:
+        from . import losses
+        return getattr(losses, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

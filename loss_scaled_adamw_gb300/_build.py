@@ -1,8 +1,8 @@
 """Build the CUDA library (libtl_gb300.so) in-tree with nvcc for sm_103a.
 
-The translation units (kernels, host C ABI, the allocation-free entry point)
-compile in parallel, then link
-into one shared library with the CUDA runtime linked statically.
+The translation units (kernels, host C ABI, the allocation-free entry point, the
+objectives over logits) compile in parallel, then link into one shared library with
+the CUDA runtime linked statically.
 """
 from __future__ import annotations
 
@@ -14,8 +14,9 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtl_gb300.so")
-SOURCES = ["tl_kernels.cu", "tl_kernels_split.cu", "tl_api.cu", "tl_noalloc.cu"]
-HEADERS = [os.path.join(CSRC, "tl_internal.cuh"), os.path.join(ROOT, "include", "tl.h")]
+SOURCES = ["tl_kernels.cu", "tl_kernels_split.cu", "tl_api.cu", "tl_noalloc.cu", "tl_loss_kernels.cu", "tl_loss_api.cu"]
+HEADERS = [os.path.join(CSRC, "tl_internal.cuh"), os.path.join(CSRC, "tl_loss_internal.cuh"),
+           os.path.join(ROOT, "include", "tl.h"), os.path.join(ROOT, "include", "tl_loss.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-lineinfo", "-O3", "-std=c++17", "-fmad=false", "-Xcompiler", "-fPIC",
                      "-I" + os.path.join(ROOT, "include")]
