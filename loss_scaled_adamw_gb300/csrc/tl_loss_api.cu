@@ -320,7 +320,7 @@ int tl_preference_loss(tl_loss_ctx* ctx, const tl_logits* logits, const tl_prefe
     if ((rc = check_spans(ctx, logits, a, sp)) != TL_OK) return rc;
     if ((rc = run_rows(ctx, kPrefStat, logits->dtype, a, stream)) != TL_OK) return rc;
     if (a.dx == nullptr || a.rows == 0) return TL_OK;
-    cudaError_t e = launch_pref_grad(logits->dtype, a, ctx->sm_count, static_cast<cudaStream_t>(stream));
+    cudaError_t e = launch_pref_grad(logits->dtype, a, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(ctx, e, "preference gradient launch");
     ctx->launches += 1;
     return TL_OK;
@@ -355,7 +355,9 @@ int tl_distill_loss(tl_loss_ctx* ctx, const tl_logits* logits, const tl_distill_
     a.kd_weight = args->kd_weight;
     a.ce_weight = args->ce_weight;
     a.k = args->kd_weight > 0.0f ? args->k : 0;   // without weight the teacher is not read
-    if (a.k > 0) {
+    if (a.k == 0) {
+        a.it = 1.0f;   // the cross-entropy alone is at temperature 1
+    } else {
         a.teacher = args->teacher;
         a.tid = args->teacher_id;
         a.ldt = args->ld_teacher;

@@ -72,6 +72,6 @@ struct LossArgs {
 
 // Launchers (tl_loss_kernels.cu).  dt: element type of the logits.
 cudaError_t launch_loss_rows(int op, int dt, const LossArgs& a, int sm_count, cudaStream_t s);
-cudaError_t launch_pref_grad(int dt, const LossArgs& a, int sm_count, cudaStream_t s);
+cudaError_t launch_pref_grad(int dt, const LossArgs& a, cudaStream_t s);
 
 }  // namespace tl
