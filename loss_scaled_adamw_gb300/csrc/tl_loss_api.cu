@@ -20,6 +20,7 @@ struct tl_loss_ctx {
     RowStat* d_stat = nullptr;     // preference: one per row
     double* d_slots = nullptr;     // 4 sums per row group of a launch
     uint32_t* d_ticket = nullptr;  // row groups that have finished; zero between calls
+    GroupCache cache;
     int64_t launches = 0;
     std::string last_error;
 };
@@ -185,7 +186,7 @@ int check_spans(tl_loss_ctx* ctx, const tl_logits* x, const LossArgs& a, const S
 }
 
 int run_rows(tl_loss_ctx* ctx, int op, int dt, const LossArgs& a, tl_stream stream) {
-    cudaError_t e = launch_loss_rows(op, dt, a, ctx->sm_count, static_cast<cudaStream_t>(stream));
+    cudaError_t e = launch_loss_rows(op, dt, a, ctx->sm_count, ctx->cache, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(ctx, e, "objective launch");
     ctx->launches += 1;
     return TL_OK;

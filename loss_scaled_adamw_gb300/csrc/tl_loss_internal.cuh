@@ -70,8 +70,20 @@ struct LossArgs {
     uint32_t* ticket;
 };
 
+// Row groups that each kernel form can have resident at once on the context's device
+// (asking the runtime for it costs more than a small launch).  A group waits for
+// nothing outside itself, so this sizes the grid and no more.
+struct GroupCache {
+    static constexpr int kEntries = 64;
+    struct Entry {
+        const void* kernel;
+        int threads, cluster, smem, groups;
+    } v[kEntries];
+    int n = 0;
+};
+
 // Launchers (tl_loss_kernels.cu).  dt: element type of the logits.
-cudaError_t launch_loss_rows(int op, int dt, const LossArgs& a, int sm_count, cudaStream_t s);
+cudaError_t launch_loss_rows(int op, int dt, const LossArgs& a, int sm_count, GroupCache& cache, cudaStream_t s);
 cudaError_t launch_pref_grad(int dt, const LossArgs& a, cudaStream_t s);
 
 }  // namespace tl

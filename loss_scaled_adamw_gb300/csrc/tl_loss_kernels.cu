@@ -3,8 +3,6 @@
 // Mathematics.  For one row x of V logits, it = 1 / temperature, M = max x:
 //   S = sum_j exp((x_j - M) it),  lp = (x_y - M) it - log S,  q_j = exp((x_j - M) it) / S,
 //   dL/dx_j = it g (1[j = y] - q_j),  g = dL/dlp.
-// x - M is taken before the multiplication, so logits at the type's lowest value
-// cannot overflow into a wrong finite result.
 #include "tl_loss_internal.cuh"
 #include "tl_internal.cuh"
 
@@ -32,10 +30,26 @@ __device__ __forceinline__ float ex2(float v) {
     return r;
 }
 
-// A part of a row (a warp's elements) has its largest element m and its sum s of
-// exp((x - m) it).  A part without an element above -inf takes 0 in the place of m,
-// so its s is 0 (NaN if it holds a NaN), and parts join without -inf - -inf.
+// Exponents.  exp((x - m) it) is 2^(x c2 - m c2) with c2 = it log2(e): one multiply-add
+// per element once u = m c2 is rounded, and that rounding cancels, since every later use
+// (joining parts, log S, q) takes the same u.  Where u could overflow (|m| from 2^120 on:
+// logits at a type's lowest or highest values) the difference is taken first.
+constexpr float kBig = 1.329227995784916e36f;   // 2^120
+__device__ __forceinline__ bool big(float m) { return !(fabsf(m) < kBig); }
+
+// A part of a row (a thread's or a warp's elements) has its largest element m and its sum
+// s of 2^((x - m) c2).  A part without an element above -inf takes 0 in the place of m, so
+// its s is 0 (NaN if it holds a NaN), and parts join without -inf - -inf.
 __device__ __forceinline__ float part_ref(float m) { return m == kNegInf ? 0.0f : m; }
+// 2^((x - m) c2)
+__device__ __forceinline__ float power(float x, float m, float c2) {
+    return ex2(big(m) ? (x - m) * c2 : __fmaf_rn(x, c2, -(m * c2)));
+}
+// What brings a part's sum from its largest element m to the joined one.
+__device__ __forceinline__ float rescale(float m, float to, float c2) {
+    if (m == kNegInf) return 1.0f;   // an empty part's 0 (or NaN) stays
+    return ex2(big(to) ? (m - to) * c2 : m * c2 - to * c2);
+}
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
@@ -188,22 +202,6 @@ __device__ __forceinline__ float policy_row(const LossArgs& a, float lp, float o
 // 16-byte vectors of logits
 // ---------------------------------------------------------------------------
 
-typedef unsigned long long f2;   // two fp32 lanes of the packed instructions
-__device__ __forceinline__ f2 pk(float lo, float hi) {
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpk(f2 v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
-__device__ __forceinline__ f2 add2(f2 a, f2 b) { f2 r; asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b)); return r; }
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) { f2 r; asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b)); return r; }
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) { f2 r; asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c)); return r; }
-__device__ __forceinline__ f2 ex2x2(f2 v) {
-    float lo, hi;
-    unpk(v, lo, hi);
-    return pk(ex2(lo), ex2(hi));
-}
-
 __device__ __forceinline__ uint4 ld16(const void* p) {
     uint4 v;
     asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
@@ -220,15 +218,11 @@ template <> struct Vec<float> {
     static __device__ __forceinline__ float top(uint4 v) {
         return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
     }
-    static __device__ __forceinline__ void wide(uint4 v, f2 (&f)[2]) {
-        f[0] = pk(__uint_as_float(v.x), __uint_as_float(v.y));
-        f[1] = pk(__uint_as_float(v.z), __uint_as_float(v.w));
+    static __device__ __forceinline__ void wide(uint4 v, float (&f)[4]) {
+        f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y); f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
     }
-    static __device__ __forceinline__ uint4 narrow(const f2 (&f)[2]) {
-        float a, b, c, d;
-        unpk(f[0], a, b);
-        unpk(f[1], c, d);
-        return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
+    static __device__ __forceinline__ uint4 narrow(const float (&f)[4]) {
+        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
     }
 };
 template <> struct Vec<__nv_bfloat16> {
@@ -239,15 +233,20 @@ template <> struct Vec<__nv_bfloat16> {
         const __nv_bfloat162 m = __hmax2(__hmax2(b2(v.x), b2(v.y)), __hmax2(b2(v.z), b2(v.w)));
         return fmaxf(__low2float(m), __high2float(m));
     }
-    static __device__ __forceinline__ f2 one(uint32_t v) { return pk(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)); }
-    static __device__ __forceinline__ void wide(uint4 v, f2 (&f)[4]) { f[0] = one(v.x); f[1] = one(v.y); f[2] = one(v.z); f[3] = one(v.w); }
-    static __device__ __forceinline__ uint32_t back(f2 f) {
-        float lo, hi;
-        unpk(f, lo, hi);
+    static __device__ __forceinline__ void one(uint32_t v, float& lo, float& hi) {
+        lo = __uint_as_float(v << 16);
+        hi = __uint_as_float(v & 0xffff0000u);
+    }
+    static __device__ __forceinline__ void wide(uint4 v, float (&f)[8]) {
+        one(v.x, f[0], f[1]); one(v.y, f[2], f[3]); one(v.z, f[4], f[5]); one(v.w, f[6], f[7]);
+    }
+    static __device__ __forceinline__ uint32_t back(float lo, float hi) {
         const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
         return *reinterpret_cast<const uint32_t*>(&r);
     }
-    static __device__ __forceinline__ uint4 narrow(const f2 (&f)[4]) { return make_uint4(back(f[0]), back(f[1]), back(f[2]), back(f[3])); }
+    static __device__ __forceinline__ uint4 narrow(const float (&f)[8]) {
+        return make_uint4(back(f[0], f[1]), back(f[2], f[3]), back(f[4], f[5]), back(f[6], f[7]));
+    }
 };
 template <> struct Vec<__half> {
     static constexpr int N = 8;
@@ -257,18 +256,21 @@ template <> struct Vec<__half> {
         const __half2 m = __hmax2(__hmax2(h2(v.x), h2(v.y)), __hmax2(h2(v.z), h2(v.w)));
         return fmaxf(__low2float(m), __high2float(m));
     }
-    static __device__ __forceinline__ f2 one(uint32_t v) {
+    static __device__ __forceinline__ void one(uint32_t v, float& lo, float& hi) {
         const float2 w = __half22float2(h2(v));
-        return pk(w.x, w.y);
+        lo = w.x;
+        hi = w.y;
     }
-    static __device__ __forceinline__ void wide(uint4 v, f2 (&f)[4]) { f[0] = one(v.x); f[1] = one(v.y); f[2] = one(v.z); f[3] = one(v.w); }
-    static __device__ __forceinline__ uint32_t back(f2 f) {
-        float lo, hi;
-        unpk(f, lo, hi);
+    static __device__ __forceinline__ void wide(uint4 v, float (&f)[8]) {
+        one(v.x, f[0], f[1]); one(v.y, f[2], f[3]); one(v.z, f[4], f[5]); one(v.w, f[6], f[7]);
+    }
+    static __device__ __forceinline__ uint32_t back(float lo, float hi) {
         const __half2 r = __floats2half2_rn(lo, hi);
         return *reinterpret_cast<const uint32_t*>(&r);
     }
-    static __device__ __forceinline__ uint4 narrow(const f2 (&f)[4]) { return make_uint4(back(f[0]), back(f[1]), back(f[2]), back(f[3])); }
+    static __device__ __forceinline__ uint4 narrow(const float (&f)[8]) {
+        return make_uint4(back(f[0], f[1]), back(f[2], f[3]), back(f[4], f[5]), back(f[6], f[7]));
+    }
 };
 
 // Where a row's elements lie: `head` elements up to the first 16-byte boundary, `body`
@@ -309,7 +311,7 @@ __device__ __forceinline__ bool same_phase(const T* x, const T* dx) {
 // ---------------------------------------------------------------------------
 
 constexpr int kMaxCluster = 8;
-constexpr int kMaxWarps = 16;   // 512 threads
+constexpr int kMaxWarps = 8;   // 256 threads
 
 __device__ __forceinline__ uint32_t cluster_rank() { uint32_t r; asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r)); return r; }
 __device__ __forceinline__ void cluster_barrier() {
@@ -328,50 +330,145 @@ __device__ __forceinline__ float warp_max(float v) {
     return r;
 }
 
-// e^tau of the temperature's exponential for the cross-entropy at temperature 1: tau = 2,
-// 3, 4 by products, else (0) from the logit.
-__device__ __forceinline__ f2 untempered(f2 e, f2 d, int pow) {
-    if (pow == 0) return ex2x2(mul2(d, pk(kLog2e, kLog2e)));
-    f2 r = mul2(e, e);
-    if (pow == 3) r = mul2(r, e);
-    if (pow == 4) r = mul2(r, r);
+// The sum at temperature 1 beside the one at tau (distillation with both terms).  For tau
+// = 2, 3 or 4 (pow) its exponentials are powers of the tempered ones; else (pow = 0) they
+// are taken from the logits.
+__device__ __forceinline__ float untempered(float e, float x, float v, int pow) {
+    if (pow == 0) return ex2(__fmaf_rn(x, kLog2e, -v));
+    float r = e * e;
+    if (pow == 3) r *= e;
+    if (pow == 4) r *= r;
     return r;
 }
+// The exponent's reference at temperature 1 for a largest element m, u = m c2.
+__device__ __forceinline__ float untempered_ref(float m, float u, int pow) { return pow == 0 ? m * kLog2e : u * float(pow); }
+__device__ __forceinline__ float rescale1(float m, float to, float c2, int pow) {
+    if (m == kNegInf) return 1.0f;
+    return ex2(big(to) ? (m - to) * kLog2e : untempered_ref(m, m * c2, pow) - untempered_ref(to, to * c2, pow));
+}
+// The same two exponentials of one element where m may be big.
+__device__ __forceinline__ float power1(float e, float x, float m, float c2, int pow) {
+    return big(m) ? ex2((x - m) * kLog2e) : untempered(e, x, untempered_ref(m, m * c2, pow), pow);
+}
 
-// One row at a time per group of `cluster` CTAs, each holding a contiguous share of the
-// row's vectors in registers (NV per thread): the row is read once.  A warp finds the
-// largest of its elements and their sum, writes both into every CTA of the group
-// (distributed shared memory), and after one barrier every warp joins all parts and
-// goes on to the gradient of the elements that it still holds.  Rows longer than the
-// group's registers run in rounds and are read a second time for the gradient.
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+constexpr int kMaxRingBytes = 220 * 1024;   // dynamic shared memory: tiles and teacher entries
+
+// A tile is kTileVecs vectors per thread, kStages of them are in shared memory.
+constexpr int kTileVecs = 8, kStages = 3;
+constexpr int64_t kRowsInL2 = 48 << 20;
+
+// How a launch lays its rows out: threads per CTA, and CTAs per row (2^clog).
+struct RowShape {
+    int threads, clog;
+};
+
+// One row at a time per group of `cluster` CTAs, each with a contiguous share of the
+// row's vectors.  The share comes through shared memory in tiles, copied asynchronously
+// ST - 1 tiles ahead of their use: while one row is worked on, the next ones are under
+// way.  A thread copies the vectors that it will itself use, so a tile needs no barrier.
+// Every thread keeps a running maximum and sum; the CTA's first warp joins its warps',
+// writes the CTA's part into every CTA of the group (distributed shared memory) and,
+// after one cluster barrier, joins the group's parts and works out the row's loss and
+// gradient factors; after a block barrier all warps write the gradient.  The factors are
+// the first warp's work alone: worked out by all warps they cost as many instructions as
+// the elements themselves.  A share of one tile is still in shared memory then, so the
+// row is read once; longer ones are streamed a second time.
 // DUAL: distillation with both terms at temperatures that differ, two sums per row.
-template <typename T, int OP, int NV, bool DUAL>
-__global__ void __launch_bounds__(512, 2) k_row(const LossArgs a, const int cluster, const int pow) {
-    constexpr int N = Vec<T>::N;
+template <typename T, int OP, int B, bool DUAL>
+__global__ void __launch_bounds__(B, 512 / B) k_row(const LossArgs a, const int clog, const int pow) {
+    constexpr int N = Vec<T>::N, U = 4, tile = B * kTileVecs, ST = kStages;
     constexpr bool kTeach = OP == kDistill;
     constexpr bool kGrad = OP == kPolicy || OP == kDistill;
-    __shared__ float4 parts[2][kMaxCluster * kMaxWarps];          // m, s, s at temperature 1
-    __shared__ float4 tparts[kTeach ? 2 : 1][kMaxWarps];           // teacher: m, sum e, sum e (t - z), bad
-    __shared__ float4 rowin[2];                                  // x_y, old, advantage, ref
-    extern __shared__ float teach[];                             // [2][k + 1] of id, t / tau, x
-    const int B = blockDim.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nw = B >> 5;
-    const int rank = cluster > 1 ? int(cluster_rank()) : 0;
-    const int group = int(blockIdx.x) / cluster, ngroups = int(gridDim.x) / cluster;
+    __shared__ float4 wparts[2][kMaxWarps];           // per warp, by row parity: m, s, s at temperature 1
+    __shared__ float4 tparts[2][kTeach ? kMaxWarps : 1]; // teacher: m, sum e, sum e (t - z), bad
+    __shared__ float4 cparts[2][kMaxCluster];         // per CTA of the group, by row parity
+    __shared__ float4 fac[2];                         // gradient factors of the row, from the first warp
+    extern __shared__ uint4 ring[];                   // [ST][tile] vectors; then [2][3][k] of id, t / tau, x
+    float* const teach = reinterpret_cast<float*>(ring + ST * tile);
+    constexpr int nw = B / 32;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int cluster = 1 << clog, rank = cluster > 1 ? int(cluster_rank()) : 0;
+    const int group = int(blockIdx.x) >> clog, ngroups = int(gridDim.x) >> clog;
+    const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + 16u * uint32_t(tid);
     const float c2 = a.it * kLog2e;
-    const float step = (a.seed ? *a.seed : 1.0f) * a.inv_n;
     const bool kd_on = kTeach && a.k > 0, ce_on = kTeach && a.ce_weight > 0.0f;
     const float kNaN = __int_as_float(0x7fffffff);
+    const float step = (kGrad && a.seed ? *a.seed : 1.0f) * a.inv_n;
     LossSums sum;
     int par = 0;
+
+    // this CTA's share of row r: [lo, hi) of its whole vectors
+    auto share_of = [&](const Row<T>& row, int& lo, int& hi) {
+        const int share = cluster > 1 ? (row.body + cluster - 1) >> clog : row.body;
+        lo = min(row.body, rank * share);
+        hi = min(row.body, lo + share);
+    };
+    // The copies run ahead in the order of their use: the tiles of a row, those of its
+    // second pass where there is one, the next row that is not ignored.
+    const bool twice = kGrad && a.dx != nullptr;   // a share longer than a tile is streamed again
+    int64_t fr = group - ngroups, fynext = a.target && group < a.rows ? a.target[group] : 0;
+    int fcount = 0, fleft = 0, fpass = 0;   // vectors of the share, those of this pass not yet asked for, passes after it
+    const T *fstart = nullptr, *fat = nullptr;   // this thread's first vector of the pass, and its next
+    auto fetch = [&](int slot) {
+        if (fleft <= 0 && fpass > 0) {
+            fpass = 0;
+            fleft = fcount;
+            fat = fstart;
+        } else if (fleft <= 0) {
+            int64_t y;
+            do {
+                fr += ngroups;
+                y = fynext;
+                fynext = a.target && fr + ngroups < a.rows ? a.target[fr + ngroups] : 0;
+                if (fr >= a.rows || y < 0) continue;
+                const Row<T> row(static_cast<const T*>(a.x) + fr * a.ld, a.vocab);
+                int lo, hi;
+                share_of(row, lo, hi);
+                fleft = fcount = hi - lo;
+                fpass = twice && fcount > tile ? 1 : 0;
+                fat = fstart = row.x + row.head + int64_t(lo + tid) * N;
+            } while (fr < a.rows && fleft <= 0);   // a share may be empty
+        }
+        // behind the last row a group is empty
+        const uint32_t to = ring_at + 16u * uint32_t(slot * tile);
+        if (fleft >= tile) {
+#pragma unroll
+            for (int i = 0; i < kTileVecs; ++i) copy_async(to + 16u * B * i, fat + B * N * i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kTileVecs; ++i)
+                if (tid + B * i < fleft) copy_async(to + 16u * B * i, fat + B * N * i);
+        }
+        fat += tile * N;
+        fleft -= tile;
+        copy_commit();
+    };
+    int slot = 0;   // of the tile in use
+    auto next_tile = [&](bool first) {
+        if (!first) slot = slot + 1 == ST ? 0 : slot + 1;
+        fetch(slot == 0 ? ST - 1 : slot - 1);   // the slot of the tile before, which this thread has done with
+        copy_wait<ST - 1>();
+    };
+
     if (cluster > 1) cluster_barrier();   // every CTA of the group runs before any writes into another
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i) fetch(i);
+    bool first = true;
+    int64_t ynext = a.target && group < a.rows ? a.target[group] : 0;
     for (int64_t r = group; r < a.rows; r += ngroups) {
+        const int64_t y = ynext;
+        if (a.target && r + ngroups < a.rows) ynext = a.target[r + ngroups];
         const Row<T> row(static_cast<const T*>(a.x) + r * a.ld, a.vocab);
         T* dx = kGrad && a.dx ? static_cast<T*>(a.dx) + r * a.ldd : nullptr;
         const bool whole = kGrad && same_phase(row.x, static_cast<const T*>(dx));
-        const T* body = row.x + row.head;
-        const int share = (row.body + cluster - 1) / cluster;
-        const int lo = min(row.body, rank * share), hi = min(row.body, lo + share);
-        const int64_t y = a.target ? a.target[r] : 0;
+        int lo, hi;
+        share_of(row, lo, hi);
         const bool edge = rank == 0 && tid < row.edges;
         if (y < 0) {
             if (dx) {
@@ -385,146 +482,159 @@ __global__ void __launch_bounds__(512, 2) k_row(const LossArgs a, const int clus
             }
             continue;
         }
-        // the row's vectors, all loads under way before the first is used
-        uint4 raw[NV];
-        float m = kNegInf, s = 0.0f, s1 = 0.0f, xe = kNegInf;
-        if (edge) xe = to_f(row.x[row.edge_at(tid)]);
-        const int rounds = hi - lo > NV * B ? (hi - lo + NV * B - 1) / (NV * B) : 1;
-        if (tid == 0) {
-            float4 in;
-            in.x = to_f(row.x[y < a.vocab ? y : 0]);
+        const float xe = edge ? to_f(row.x[row.edge_at(tid)]) : kNegInf;
+        float xy = 0.0f, in1 = 0.0f, in2 = 0.0f, in3 = 0.0f;   // first warp: x_y, old, advantage, ref
+        if (warp == 0) {
+            xy = to_f(row.x[y < a.vocab ? y : 0]);
             if (OP == kPolicy) {
-                in.y = a.old_logp[r];
-                in.z = a.adv[r];
-                in.w = a.ref_logp ? a.ref_logp[r] : 0.0f;
+                in1 = a.old_logp[r];
+                in2 = a.adv[r];
             }
-            if (OP == kPrefStat) in.w = a.ref_logp ? a.ref_logp[r] : 0.0f;
-            rowin[par] = in;
+            if (OP == kPolicy || OP == kPrefStat) in3 = a.ref_logp ? a.ref_logp[r] : 0.0f;
         }
-        for (int q = 0; q < rounds; ++q) {
-            const int base = lo + q * NV * B;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int v = base + i * B + tid;
-                raw[i] = make_uint4(Vec<T>::kEmpty, Vec<T>::kEmpty, Vec<T>::kEmpty, Vec<T>::kEmpty);
-                if (v < hi) raw[i] = ld16(body + int64_t(v) * N);
+        if (kTeach && kd_on && warp * 32 < a.k) {
+            // the teacher's entries, a few per thread: logit, id, and the student's logit there
+            float* const tb = teach + par * 3 * a.k;
+            float tm = kNegInf, ts = 0.0f, td = 0.0f, bad = 0.0f;
+            for (int i = tid; i < a.k; i += B) {
+                const int64_t id = teacher_id(a, r * a.ldt + i);
+                const bool on = id >= 0 && id < a.vocab;
+                const float t = on ? teacher_logit(a, r * a.ldt + i) * a.it : kNegInf;
+                const float z = on ? to_f(row.x[id]) : 0.0f;
+                if (id >= a.vocab) bad = kNaN;
+                tb[i] = __int_as_float(on ? int(id) : -1);
+                tb[a.k + i] = t;
+                tb[2 * a.k + i] = z;
+                // running form: the entries of one thread are few
+                const float nm = fmaxf(tm, t), nr = part_ref(nm);
+                const float f = ex2((part_ref(tm) - nr) * kLog2e);
+                const float e = ex2((t - nr) * kLog2e);
+                ts = (tm == kNegInf ? ts : ts * f) + e;
+                td = (tm == kNegInf ? td : f != 0.0f ? td * f : 0.0f) + (e != 0.0f ? e * (t - z * a.it) : 0.0f);
+                tm = nm;
             }
-            if (kTeach && q == 0 && kd_on) {
-                // the teacher's entries, a few per thread: logit, id, and the student's logit there
-                float* const tb = teach + par * 3 * (a.k + 1);
-                float tm = kNegInf, ts = 0.0f, td = 0.0f, bad = 0.0f;
-                for (int i = tid; i < a.k; i += B) {
-                    const int64_t id = teacher_id(a, r * a.ldt + i);
-                    const bool on = id >= 0 && id < a.vocab;
-                    const float t = on ? teacher_logit(a, r * a.ldt + i) * a.it : kNegInf;
-                    const float z = on ? to_f(row.x[id]) : 0.0f;
-                    if (id >= a.vocab) bad = kNaN;
-                    tb[i] = __int_as_float(on ? int(id) : -1);
-                    tb[a.k + 1 + i] = t;
-                    tb[2 * (a.k + 1) + i] = z;
-                    // running form: the entries of one thread are few
-                    const float nm = fmaxf(tm, t), nr = part_ref(nm);
-                    const float f = ex2((part_ref(tm) - nr) * kLog2e);
-                    const float e = ex2((t - nr) * kLog2e);
-                    ts = (tm == kNegInf ? ts : ts * f) + e;
-                    td = (tm == kNegInf ? td : f != 0.0f ? td * f : 0.0f) + (e != 0.0f ? e * (t - z * a.it) : 0.0f);
-                    tm = nm;
-                }
-                const float wm = warp_max(tm), wr = part_ref(wm);
-                const float f = tm == kNegInf ? 1.0f : ex2((tm - wr) * kLog2e);
-                ts = warp_sum(ts * f);
-                td = warp_sum(f != 0.0f ? td * f : 0.0f);
-                bad = warp_sum(bad);
-                if (lane == 0) tparts[par][warp] = make_float4(wm, ts, td, bad);
-            }
-            // the warp's largest element; sums of earlier rounds are brought to it
-            float top = q == 0 ? xe : kNegInf;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) top = fmaxf(top, Vec<T>::top(raw[i]));
-            top = fmaxf(m, warp_max(top));
-            const float ref = part_ref(top);
-            if (q > 0) {
-                const float d = part_ref(m) - ref;
-                if (m != kNegInf) {
-                    s *= ex2(d * c2);
-                    if (DUAL) s1 *= ex2(d * kLog2e);
-                }
-            } else {
-                const float d = xe - ref, e = ex2(d * c2);
-                s = e;
-                if (DUAL) { float u, w; unpk(untempered(pk(e, 0.0f), pk(d, 0.0f), pow), u, w); s1 = u; }
+            const float wm = warp_max(tm), wr = part_ref(wm);
+            const float f = tm == kNegInf ? 1.0f : ex2((tm - wr) * kLog2e);
+            ts = warp_sum(ts * f);
+            td = warp_sum(f != 0.0f ? td * f : 0.0f);
+            bad = warp_sum(bad);
+            if (lane == 0) tparts[par][warp] = make_float4(wm, ts, td, bad);
+        }
+        // the thread's largest element and its sums, U vectors at a time
+        float m = kNegInf, acc[2] = {0.0f, 0.0f}, acc1[2] = {0.0f, 0.0f};
+        auto raise = [&](float top) {   // the sums so far to a larger element
+            if (top == m) return;
+            const float f = rescale(m, top, c2);
+            acc[0] *= f;
+            acc[1] *= f;
+            if (DUAL) {
+                const float f1 = rescale1(m, top, c2, pow);
+                acc1[0] *= f1;
+                acc1[1] *= f1;
             }
             m = top;
-            const f2 nref = pk(-ref, -ref), cc = pk(c2, c2);
-            f2 acc[2] = {pk(s, 0.0f), pk(0.0f, 0.0f)}, acc1[2] = {pk(s1, 0.0f), pk(0.0f, 0.0f)};
+        };
+        auto add_big = [&](const uint4* at) {
+#pragma unroll 1
+            for (int j = 0; j < N; ++j) {
+                const float x = to_f(reinterpret_cast<const T*>(at)[j]), d = x - part_ref(m);
+                acc[0] += ex2(d * c2);
+                if (DUAL) acc1[0] += ex2(d * kLog2e);
+            }
+        };
+        auto add = [&](uint4 raw, float u, float v) {
+            float f[N];
+            Vec<T>::wide(raw, f);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                if (base + i * B >= hi) break;   // the whole CTA has no vector left
-                f2 f[N / 2];
-                Vec<T>::wide(raw[i], f);
+            for (int j = 0; j < N; ++j) {
+                const float e = ex2(__fmaf_rn(f[j], c2, -u));
+                acc[j & 1] += e;
+                if (DUAL) acc1[j & 1] += untempered(e, f[j], v, pow);
+            }
+        };
+        for (int left = hi - lo; left > 0; left -= tile) {
+            next_tile(first);
+            first = false;
+            const uint4* const buf = ring + slot * tile + tid;
+            const int mine = left - tid;   // vector i of the thread exists where B i < mine
+#pragma unroll 1
+            for (int g = 0; g < kTileVecs; g += U) {
+                if (B * g >= mine) break;
+                uint4 raw[U];
+                if (B * (g + U - 1) < mine) {
 #pragma unroll
-                for (int j = 0; j < N / 2; ++j) {
-                    const f2 d = add2(f[j], nref), e = ex2x2(mul2(d, cc));
-                    acc[j & 1] = add2(acc[j & 1], e);
-                    if (DUAL) acc1[j & 1] = add2(acc1[j & 1], untempered(e, d, pow));
+                    for (int i = 0; i < U; ++i) raw[i] = buf[B * (g + i)];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < U; ++i) {
+                        raw[i] = make_uint4(Vec<T>::kEmpty, Vec<T>::kEmpty, Vec<T>::kEmpty, Vec<T>::kEmpty);
+                        if (B * (g + i) < mine) raw[i] = buf[B * (g + i)];
+                    }
+                }
+                float top = m;
+#pragma unroll
+                for (int i = 0; i < U; ++i) top = fmaxf(top, Vec<T>::top(raw[i]));
+                raise(top);
+                if (big(part_ref(m))) {
+#pragma unroll 1
+                    for (int i = 0; i < U; ++i)
+                        if (B * (g + i) < mine) add_big(buf + B * (g + i));
+                } else {
+                    const float u = part_ref(m) * c2, u1 = DUAL ? untempered_ref(part_ref(m), u, pow) : 0.0f;
+#pragma unroll
+                    for (int i = 0; i < U; ++i) add(raw[i], u, u1);
                 }
             }
-            float u, w;
-            unpk(add2(acc[0], acc[1]), u, w);
-            s = u + w;
-            if (DUAL) {
-                unpk(add2(acc1[0], acc1[1]), u, w);
-                s1 = u + w;
-            }
         }
-        s = warp_sum(s);
-        if (DUAL) s1 = warp_sum(s1);
-        if (cluster > 1) {
-            if (lane < cluster) store_remote(&parts[par][rank * nw + warp], uint32_t(lane), make_float4(m, s, s1, 0.0f));
-            cluster_barrier();
-        } else {
-            if (lane == 0) parts[par][warp] = make_float4(m, s, s1, 0.0f);
-            __syncthreads();
+        {
+            // the warp's part, edges included
+            const float top = warp_max(fmaxf(m, xe)), ref = part_ref(top);
+            const float ee = power(xe, ref, c2);
+            const float s = warp_sum((acc[0] + acc[1]) * rescale(m, ref, c2) + ee);
+            float s1 = 0.0f;
+            if (DUAL) s1 = warp_sum((acc1[0] + acc1[1]) * rescale1(m, ref, c2, pow) + power1(ee, xe, ref, c2, pow));
+            if (lane == 0) wparts[par][warp] = make_float4(top, s, s1, 0.0f);
         }
-        // every warp joins the parts of the whole row, in one order
+        __syncthreads();
         float S = 0.0f, S1 = 0.0f, M = kNegInf;
-        const int np = cluster * nw;
-        for (int i = lane; i < np; i += 32) M = fmaxf(M, parts[par][i].x);
-        M = warp_max(M);
-        const float R = part_ref(M);
-        for (int i = lane; i < np; i += 32) {
-            const float4 p = parts[par][i];
-            const float d = part_ref(p.x) - R;
-            S = __fmaf_rn(p.y, p.x == kNegInf ? 1.0f : ex2(d * c2), S);
-            if (DUAL) S1 = __fmaf_rn(p.z, p.x == kNegInf ? 1.0f : ex2(d * kLog2e), S1);
+        auto join = [&](float4 p) {   // the first warp: lane i holds part i, the others an empty one
+            M = warp_max(p.x);
+            S = warp_sum(p.y * rescale(p.x, part_ref(M), c2));
+            if (DUAL) S1 = warp_sum(p.z * rescale1(p.x, part_ref(M), c2, pow));
+        };
+        const float4 none = make_float4(kNegInf, 0.0f, 0.0f, 0.0f);
+        if (warp == 0) {
+            join(lane < nw ? wparts[par][lane] : none);
+            if (cluster > 1 && lane < cluster) store_remote(&cparts[par][rank], uint32_t(lane), make_float4(M, S, S1, 0.0f));
         }
-        S = warp_sum(S);
-        if (DUAL) S1 = warp_sum(S1);
-        const float4 in = rowin[par];
-        float bad = y >= a.vocab || M == kNegInf ? kNaN : 0.0f;
-        const float lg = log2f(S);
-        const float lp = __fmaf_rn(in.x - M, c2, -lg) * kLn2 + bad;
-        if (OP == kLogprob || OP == kPrefStat) {
-            if (rank == 0 && tid == 0) {
-                if (a.logp) a.logp[r] = lp;
-                if (OP == kPrefStat) a.stat[r] = {M + bad, 1.0f / S, 0.0f, lp - in.w};
-            }
-        } else {
-            float w = 0.0f, kq, cq = 0.0f, wc = 0.0f;   // gradient factors: label, q at the temperature, q at 1
-            float tm = kNegInf, ts = 0.0f, td = 0.0f;
-            bool row_kd = false;
-            if (OP == kPolicy) {
+        if (cluster > 1) {
+            cluster_barrier();
+            if (warp == 0) join(lane < cluster ? cparts[par][lane] : none);
+        }
+        if (warp == 0) {
+            float bad = y >= a.vocab || M == kNegInf ? kNaN : 0.0f;
+            const float lg = log2f(S);
+            const float gap = big(M) ? (xy - M) * c2 : __fmaf_rn(xy, c2, -(M * c2));   // log2 of the label's exponential
+            const float lp = (gap - lg) * kLn2 + bad;
+            const bool out = rank == 0 && lane == 0;
+            if (OP == kLogprob || OP == kPrefStat) {
+                if (out && a.logp) a.logp[r] = lp;
+                if (OP == kPrefStat && out) a.stat[r] = {M + bad, 1.0f / S, 0.0f, lp - in3};
+            } else if (OP == kPolicy) {
                 float loss, sur, kl;
-                w = policy_row(a, lp, in.y, in.z, in.w, loss, sur, kl) * step * a.it;
-                kq = -w / S;
-                if (rank == 0 && tid == 0) {
+                const float w = policy_row(a, lp, in1, in2, in3, loss, sur, kl) * step * a.it;
+                if (out) {
                     if (a.logp) a.logp[r] = lp;
                     if (a.loss) a.loss[r] = loss;
                     sum.loss += loss; sum.first += sur; sum.second += kl; sum.count += 1.0;
                 }
+                // the label's element: w (1 - q)
+                if (lane == 0) fac[0] = make_float4(M + bad, -w / S, __fmaf_rn(ex2(gap), -w / S, w), 0.0f);
             } else {
+                float tm = kNegInf, ts = 0.0f, td = 0.0f;
+                bool row_kd = false;
                 if (kd_on) {
-                    const float4 p = lane < nw ? tparts[par][lane] : make_float4(kNegInf, 0.0f, 0.0f, 0.0f);
+                    const float4 p = lane < nw && lane * 32 < a.k ? tparts[par][lane] : none;
                     tm = warp_max(p.x);
                     const float f = p.x == kNegInf ? 1.0f : ex2((p.x - part_ref(tm)) * kLog2e);
                     ts = warp_sum(p.y * f);
@@ -532,92 +642,107 @@ __global__ void __launch_bounds__(512, 2) k_row(const LossArgs a, const int clus
                     bad += warp_sum(p.w);
                     row_kd = ts != 0.0f;
                 }
-                const float lz = __fmaf_rn(M, a.it, lg * kLn2);   // log sum exp z
+                const float lz = big(M) ? __fmaf_rn(M, a.it, lg * kLn2) : (M * c2 + lg) * kLn2;   // log sum exp z
                 const float kd = row_kd ? (td / ts - tm - logf(ts) + lz) / (a.it * a.it) + bad : bad;
-                const float ce = ce_on ? (DUAL ? logf(S1) - (in.x - M) : -lp) + bad : 0.0f;
+                float log_sum1 = 0.0f;   // log sum exp x
+                if (DUAL) log_sum1 = big(M) ? M + logf(S1) : (untempered_ref(M, M * c2, pow) + log2f(S1)) * kLn2;
+                const float ce = ce_on ? (DUAL ? log_sum1 - xy : -lp) + bad : 0.0f;
                 const float loss = (row_kd ? a.kd_weight * kd : bad) + (ce_on ? a.ce_weight * ce : 0.0f);
-                if (rank == 0 && tid == 0) {
+                if (out) {
                     if (a.loss) a.loss[r] = loss;
                     sum.loss += loss; sum.first += kd; sum.second += ce; sum.count += 1.0;
                 }
-                kq = row_kd ? a.kd_weight * step / a.it / S : 0.0f;
-                wc = ce_on ? a.ce_weight * step : 0.0f;
-                if (DUAL) cq = wc / S1; else kq += wc / S;
-                kq += bad;
-            }
-            if (dx) {
-                const float Mb = M + bad;
-                const f2 nref = pk(-Mb, -Mb), cc = pk(c2, c2), k2 = pk(kq, kq), k1 = pk(cq, cq);
-                for (int q = 0; q < rounds; ++q) {
-                    const int base = lo + q * NV * B;
-                    if (rounds > 1) {
-#pragma unroll
-                        for (int i = 0; i < NV; ++i) {
-                            const int v = base + i * B + tid;
-                            if (v < hi) raw[i] = ld16(body + int64_t(v) * N);
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < NV; ++i) {
-                        const int v = base + i * B + tid;
-                        if (v < hi) {
-                            f2 f[N / 2];
-                            Vec<T>::wide(raw[i], f);
-#pragma unroll
-                            for (int j = 0; j < N / 2; ++j) {
-                                const f2 d = add2(f[j], nref), e = ex2x2(mul2(d, cc));
-                                f[j] = DUAL ? fma2(untempered(e, d, pow), k1, mul2(e, k2)) : mul2(e, k2);
-                            }
-                            store_vec<T>(dx + row.head + int64_t(v) * N, Vec<T>::narrow(f), whole);
-                        }
-                    }
+                // factors of the exponentials at the temperature and at 1, and of the teacher's
+                // (e_i = exp(t_i - tm) times wp; 0: none)
+                const float wk = row_kd ? a.kd_weight * step / a.it : 0.0f, wc = ce_on ? a.ce_weight * step : 0.0f;
+                const float kq = wk / S + (DUAL ? 0.0f : wc / S) + bad;
+                if (lane == 0) {
+                    fac[0] = make_float4(M + bad, row_kd || (!DUAL && ce_on) || bad != 0.0f ? kq : 0.0f, DUAL ? wc / S1 : 0.0f, tm);
+                    fac[1] = make_float4(row_kd ? wk / ts : 0.0f, bad, xy, wc);
                 }
-                auto dense = [&](float x) {
-                    const float d = x - Mb, e = ex2(d * c2);
-                    float u = 0.0f, t;
-                    if (DUAL) unpk(untempered(pk(e, 0.0f), pk(d, 0.0f), pow), u, t);
-                    return DUAL ? __fmaf_rn(u, cq, e * kq) : e * kq;
-                };
-                // who holds element j: the edges' threads of the first CTA, else the share
-                auto owned = [&](int j, int& holder) {
-                    const int v = (j - row.head) / N;
-                    if (j < row.head || v >= row.body) {
-                        holder = j < row.head ? j : j - row.body * N;
-                        return rank == 0;
+            }
+        }
+        if (kGrad && dx) {
+            __syncthreads();
+            const float4 fc = fac[0];
+            const float Mb = fc.x, kq = fc.y, cq = OP == kDistill ? fc.z : 0.0f;
+            const float u = Mb * c2, v1 = DUAL ? untempered_ref(Mb, u, pow) : 0.0f;
+            auto dense = [&](float x) {
+                const float e = power(x, Mb, c2);
+                return DUAL ? __fmaf_rn(power1(e, x, Mb, c2, pow), cq, e * kq) : e * kq;
+            };
+            for (int done = 0; done < hi - lo; done += tile) {
+                if (hi - lo > tile) next_tile(false);
+                const uint4* const buf = ring + slot * tile + tid;
+                const int mine = hi - lo - done - tid;
+                T* const to = dx + row.head + int64_t(lo + done + tid) * N;
+                if (big(Mb)) {   // NaN rows too
+#pragma unroll 1
+                    for (int i = 0; i < kTileVecs && B * i < mine; ++i)
+#pragma unroll 1
+                        for (int j = 0; j < N; ++j)
+                            to[B * N * i + j] = from_f<T>(dense(to_f(reinterpret_cast<const T*>(buf + B * i)[j])));
+                    continue;
+                }
+                auto emit = [&](int i) {
+                    float f[N];
+                    Vec<T>::wide(buf[B * i], f);
+#pragma unroll
+                    for (int j = 0; j < N; ++j) {
+                        const float e = ex2(__fmaf_rn(f[j], c2, -u));
+                        f[j] = DUAL ? __fmaf_rn(untempered(e, f[j], v1, pow), cq, e * kq) : e * kq;
                     }
-                    holder = (v - lo) % B;
-                    return v >= lo && v < hi;
+                    store_vec<T>(to + B * N * i, Vec<T>::narrow(f), whole);
                 };
-                if (edge) dx[row.edge_at(tid)] = from_f<T>(dense(xe));
-                if (OP == kPolicy) {
-                    // the label's element again, by the thread that stored it
-                    int holder;
-                    if (bad == 0.0f && owned(int(y), holder) && holder == tid) dx[y] = from_f<T>(w + dense(in.x));
+                if (whole && B * (kTileVecs - 1) < mine) {
+#pragma unroll
+                    for (int i = 0; i < kTileVecs; ++i) emit(i);
                 } else {
-                    // the listed elements again, once the CTA has stored its share: an id's first
-                    // entry takes the weights of all that are equal to it
-                    const int n = row_kd ? a.k : 0, entries = n + (ce_on && bad == 0.0f ? 1 : 0);
-                    const float* const tb = teach + par * 3 * (a.k + 1);
-                    const float wp = row_kd ? a.kd_weight * step / (a.it * ts) : 0.0f;
-                    __syncthreads();
-                    for (int i = tid; i < entries; i += B) {
-                        const int id = i < n ? __float_as_int(tb[i]) : int(y);
-                        int holder;
-                        if (id < 0 || !owned(id, holder)) continue;
-                        float v = ce_on && id == int(y) ? wc : 0.0f;
-                        bool first = true;
-                        for (int j = 0; j < n; ++j) {
-                            if (__float_as_int(tb[j]) != id) continue;
-                            if (j < i) { first = false; break; }
-                            v = __fmaf_rn(wp, ex2((tb[a.k + 1 + j] - tm) * kLog2e), v);
-                        }
-                        if (first) dx[id] = from_f<T>(dense(i < n ? tb[2 * (a.k + 1) + i] : in.x) - v);
+#pragma unroll 1
+                    for (int i = 0; i < kTileVecs && B * i < mine; ++i) emit(i);
+                }
+            }
+            // who holds element j: the edges' threads of the first CTA, else the share
+            auto owned = [&](int j, int& holder) {
+                const int v = (j - row.head) / N;
+                if (j < row.head || v >= row.body) {
+                    holder = j < row.head ? j : j - row.body * N;
+                    return rank == 0;
+                }
+                holder = (v - lo) & (B - 1);   // tiles are whole multiples of B
+                return v >= lo && v < hi;
+            };
+            if (edge) dx[row.edge_at(tid)] = from_f<T>(dense(xe));
+            if (OP == kPolicy) {
+                // the label's element again, by the thread that stored it
+                int holder;
+                if (y < a.vocab && owned(int(y), holder) && holder == tid) dx[y] = from_f<T>(fc.z);
+            } else {
+                // the listed elements again, once the CTA has stored its share: an id's first
+                // entry takes the weights of all that are equal to it
+                const float4 f1 = fac[1];   // teacher's factor, bad, x_y, the label's weight
+                const float tm = fc.w, wp = f1.x, bad = f1.y;
+                const int n = wp != 0.0f ? a.k : 0, entries = n + (ce_on && bad == 0.0f ? 1 : 0);
+                const float* const tb = teach + par * 3 * a.k;
+                __syncthreads();
+                for (int i = tid; i < entries; i += B) {
+                    const int id = i < n ? __float_as_int(tb[i]) : int(y);
+                    int holder;
+                    if (id < 0 || !owned(id, holder)) continue;
+                    float v = ce_on && id == int(y) ? f1.w : 0.0f;
+                    bool lead = true;
+                    for (int j = 0; j < n; ++j) {
+                        if (__float_as_int(tb[j]) != id) continue;
+                        if (j < i) { lead = false; break; }
+                        v = __fmaf_rn(wp, ex2((tb[a.k + j] - tm) * kLog2e), v);
                     }
+                    if (lead) dx[id] = from_f<T>(dense(i < n ? tb[2 * a.k + i] : f1.z) - v);
                 }
             }
         }
         par ^= 1;
     }
+    copy_wait<0>();
     if (OP != kLogprob && rank == 0) finish<OP>(a, sum, group, ngroups);
 }
 
@@ -661,87 +786,111 @@ __global__ void __launch_bounds__(256) k_pref_grad(const LossArgs a, const int s
             xy = to_f(row.x[j]);
         }
     }
-    const f2 nref = pk(-st.m, -st.m), cc = pk(c2, c2), k2 = pk(kq, kq);
+    const float u = st.m * c2;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int v = lo + i * 256 + tid;
         if (v < hi) {
-            f2 f[N / 2];
+            float f[N];
             Vec<T>::wide(raw[i], f);
+            if (big(st.m)) {
+                for (int j = 0; j < N; ++j) f[j] = ex2((f[j] - st.m) * c2) * kq;
+            } else {
 #pragma unroll
-            for (int j = 0; j < N / 2; ++j) f[j] = mul2(ex2x2(mul2(add2(f[j], nref), cc)), k2);
+                for (int j = 0; j < N; ++j) f[j] = ex2(__fmaf_rn(f[j], c2, -u)) * kq;
+            }
             store_vec<T>(dx + row.head + int64_t(v) * N, Vec<T>::narrow(f), whole);
         }
     }
-    if (edge) dx[row.edge_at(tid)] = from_f<T>(ex2((xe - st.m) * c2) * kq);
-    if (mine >= 0) dx[mine] = from_f<T>(__fmaf_rn(ex2((xy - st.m) * c2), kq, st.w));
+    if (edge) dx[row.edge_at(tid)] = from_f<T>(power(xe, st.m, c2) * kq);
+    if (mine >= 0) dx[mine] = from_f<T>(__fmaf_rn(power(xy, st.m, c2), kq, st.w));
 }
 
-// How a launch lays its rows out.
-struct RowShape {
-    int threads, nv, cluster;
-};
-
 template <typename T>
-RowShape shape_for(int op, int64_t rows, int vocab, int sms) {
+RowShape shape_for(int64_t rows, int vocab, bool grad, int sms) {
     const int vecs = (vocab + Vec<T>::N - 1) / Vec<T>::N;
-    RowShape s{64, 4, 1};
-    while (s.threads < 512 && s.threads * 4 < vecs) s.threads *= 2;
-    if (s.threads * 4 < vecs) s.nv = 8;
-    while (s.cluster < kMaxCluster && s.threads * s.nv * s.cluster < vecs) s.cluster *= 2;
+    RowShape s{64, 0};
+    while (s.threads < 256 && s.threads * 8 < vecs) s.threads *= 2;
+    // long rows read twice: more CTAs to a row keep the rows under way (two CTAs per SM) in L2
+    // for the second read.  4,096 x 128,256 bf16: 339 us with 2 CTAs per row (39 MB under
+    // way), 429 with 1 (78 MB), 390 with 4
+    if (grad && s.threads == 256)
+        while ((1 << s.clog) < kMaxCluster && (int64_t(2) * sms * vocab * int(sizeof(T))) >> s.clog > kRowsInL2) s.clog += 1;
     // few rows: spread each over more CTAs while the GPU has idle SMs and a thread more than one vector
-    while (s.cluster < kMaxCluster && rows * s.cluster * 2 <= sms && s.threads * s.cluster < vecs) s.cluster *= 2;
-    const int per = (vecs + s.cluster * s.threads - 1) / (s.cluster * s.threads);
-    s.nv = per <= 2 ? 2 : per <= 4 ? 4 : 8;
+    while ((1 << s.clog) < kMaxCluster && rows << (s.clog + 1) <= sms && s.threads << s.clog < vecs) s.clog += 1;
     return s;
 }
 
-template <typename T, int OP, int NV, bool DUAL>
-cudaError_t row_launch(const LossArgs& a, const RowShape& sh, int sms, cudaStream_t s) {
-    auto* kernel = k_row<T, OP, NV, DUAL>;
-    const size_t smem = OP == kDistill ? sizeof(float) * 2 * 3 * size_t(a.k + 1) : 0;
-    int per_sm = 0;
-    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, sh.threads, smem);
+// Row groups that a launch can have resident at once, from the context's cache.
+cudaError_t resident_groups(const void* kernel, const cudaLaunchConfig_t& cfg, const RowShape& sh, int sms,
+                            GroupCache& cache, int& groups) {
+    const int smem = int(cfg.dynamicSmemBytes);
+    for (int i = 0; i < cache.n; ++i) {
+        const GroupCache::Entry& e = cache.v[i];
+        if (e.kernel == kernel && e.threads == sh.threads && e.cluster == sh.clog && e.smem == smem) {
+            groups = e.groups;
+            return cudaSuccess;
+        }
+    }
+    // one limit for every shape of the kernel: the attribute belongs to the function
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRingBytes);
     if (e != cudaSuccess) return e;
-    int64_t groups = int64_t(per_sm) * sms / sh.cluster;
-    if (groups > kMaxLossClusters) groups = kMaxLossClusters;
-    if (groups > a.rows) groups = a.rows;
-    if (groups < 1) groups = 1;
+    if (sh.clog > 0) {
+        e = cudaOccupancyMaxActiveClusters(&groups, kernel, &cfg);
+    } else {
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&groups, kernel, sh.threads, cfg.dynamicSmemBytes);
+        groups *= sms;
+    }
+    if (e != cudaSuccess) return e;
+    groups = groups < 1 ? 1 : groups > kMaxLossClusters ? kMaxLossClusters : groups;
+    cache.v[cache.n % GroupCache::kEntries] = {kernel, sh.threads, sh.clog, smem, groups};
+    if (cache.n < GroupCache::kEntries) cache.n += 1;
+    return cudaSuccess;
+}
+
+template <typename T, int OP, int B, bool DUAL>
+cudaError_t row_launch(const LossArgs& a, const RowShape& sh, int sms, GroupCache& cache, cudaStream_t s) {
+    auto* kernel = k_row<T, OP, B, DUAL>;
     const int t = int(1.0f / a.it + 0.5f);
     const int pow = DUAL && t >= 2 && t <= 4 && a.it == 1.0f / float(t) ? t : 0;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned(groups * sh.cluster));
-    cfg.blockDim = dim3(unsigned(sh.threads));
-    cfg.dynamicSmemBytes = smem;
+    cfg.gridDim = dim3(1u << sh.clog);
+    cfg.blockDim = dim3(unsigned(B));
+    cfg.dynamicSmemBytes = size_t(16) * kStages * kTileVecs * B + (OP == kDistill ? sizeof(float) * 2 * 3 * size_t((a.k + 63) / 64 * 64) : 0);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = unsigned(sh.cluster);
+    attr[0].val.clusterDim.x = 1u << sh.clog;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = sh.cluster > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, a, int(sh.cluster), pow);
+    cfg.numAttrs = sh.clog > 0 ? 1 : 0;
+    int groups = 0;
+    cudaError_t e = resident_groups(reinterpret_cast<const void*>(kernel), cfg, sh, sms, cache, groups);
+    if (e != cudaSuccess) return e;
+    if (groups > a.rows) groups = a.rows < 1 ? 1 : int(a.rows);
+    cfg.gridDim.x = unsigned(groups) << sh.clog;
+    return cudaLaunchKernelEx(&cfg, kernel, a, int(sh.clog), pow);
 }
 
 template <typename T, int OP, bool DUAL>
-cudaError_t rows_by_nv(const LossArgs& a, const RowShape& sh, int sms, cudaStream_t s) {
-    if (sh.nv == 2) return row_launch<T, OP, 2, DUAL>(a, sh, sms, s);
-    if (sh.nv == 4) return row_launch<T, OP, 4, DUAL>(a, sh, sms, s);
-    return row_launch<T, OP, 8, DUAL>(a, sh, sms, s);
+cudaError_t rows_by_threads(const LossArgs& a, const RowShape& sh, int sms, GroupCache& cache, cudaStream_t s) {
+    if (sh.threads == 64) return row_launch<T, OP, 64, DUAL>(a, sh, sms, cache, s);
+    if (sh.threads == 128) return row_launch<T, OP, 128, DUAL>(a, sh, sms, cache, s);
+    return row_launch<T, OP, 256, DUAL>(a, sh, sms, cache, s);
 }
 
 template <typename T>
-cudaError_t rows_by_op(int op, const LossArgs& a, int sms, cudaStream_t s) {
-    const RowShape sh = shape_for<T>(op, a.rows, a.vocab, sms);
+cudaError_t rows_by_op(int op, const LossArgs& a, int sms, GroupCache& cache, cudaStream_t s) {
+    const RowShape sh = shape_for<T>(a.rows, a.vocab, a.dx != nullptr, sms);
     switch (op) {
-        case kLogprob: return rows_by_nv<T, kLogprob, false>(a, sh, sms, s);
-        case kPolicy: return rows_by_nv<T, kPolicy, false>(a, sh, sms, s);
-        case kPrefStat: return rows_by_nv<T, kPrefStat, false>(a, sh, sms, s);
+        case kLogprob: return rows_by_threads<T, kLogprob, false>(a, sh, sms, cache, s);
+        case kPolicy: return rows_by_threads<T, kPolicy, false>(a, sh, sms, cache, s);
+        case kPrefStat: return rows_by_threads<T, kPrefStat, false>(a, sh, sms, cache, s);
         default: break;
     }
-    if (a.k > 0 && a.ce_weight > 0.0f && a.it != 1.0f) return rows_by_nv<T, kDistill, true>(a, sh, sms, s);
-    return rows_by_nv<T, kDistill, false>(a, sh, sms, s);
+    if (a.k > 0 && a.ce_weight > 0.0f && a.it != 1.0f) return rows_by_threads<T, kDistill, true>(a, sh, sms, cache, s);
+    return rows_by_threads<T, kDistill, false>(a, sh, sms, cache, s);
 }
 
 template <typename T>
@@ -756,10 +905,10 @@ cudaError_t pref_grad(const LossArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_loss_rows(int op, int dt, const LossArgs& a, int sm_count, cudaStream_t s) {
-    if (dt == kF32) return rows_by_op<float>(op, a, sm_count, s);
-    if (dt == kBF16) return rows_by_op<__nv_bfloat16>(op, a, sm_count, s);
-    return rows_by_op<__half>(op, a, sm_count, s);
+cudaError_t launch_loss_rows(int op, int dt, const LossArgs& a, int sm_count, GroupCache& cache, cudaStream_t s) {
+    if (dt == kF32) return rows_by_op<float>(op, a, sm_count, cache, s);
+    if (dt == kBF16) return rows_by_op<__nv_bfloat16>(op, a, sm_count, cache, s);
+    return rows_by_op<__half>(op, a, sm_count, cache, s);
 }
 
 cudaError_t launch_pref_grad(int dt, const LossArgs& a, cudaStream_t s) {
