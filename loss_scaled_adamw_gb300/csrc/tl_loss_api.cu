@@ -126,7 +126,7 @@ void base_args(tl_loss_ctx* ctx, const tl_logits* x, const int64_t* target, Loss
     a.slots = ctx->d_slots;
     a.ticket = ctx->d_ticket;
     a.inv_n = 1.0f;
-    a.n = 1.0;
+    a.per_n = 1.0;
     sp.add(target, 8 * x->rows, false);
 }
 
@@ -164,7 +164,7 @@ int check_out(tl_loss_ctx* ctx, const tl_logits* x, const tl_loss_out* o, int64_
     a.ldd = o->ld_dlogits;
     a.seed = o->seed;
     a.inv_n = float(1.0 / double(o->n));
-    a.n = double(o->n);
+    a.per_n = 1.0 / double(o->n);
     a.logp = o->logp;
     a.loss = o->loss;
     a.result = reinterpret_cast<float*>(o->result);

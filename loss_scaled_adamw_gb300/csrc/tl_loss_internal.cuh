@@ -41,7 +41,7 @@ struct LossArgs {
     int64_t ldd;
     const float* seed;
     float inv_n;
-    double n;
+    double per_n;          // 1 / n
     // policy
     const float* old_logp;
     const float* ref_logp;

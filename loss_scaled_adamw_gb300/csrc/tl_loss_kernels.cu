@@ -14,6 +14,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -__builtin_huge_valf();
+constexpr int kMaxWarps = 8;   // 256 threads
 
 __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -70,58 +71,71 @@ __device__ __forceinline__ int64_t teacher_id(const LossArgs& a, int64_t at) {
     return a.id_bytes == 8 ? static_cast<const int64_t*>(a.tid)[at] : int64_t(static_cast<const int32_t*>(a.tid)[at]);
 }
 
+// Named barriers: `count` threads take part; arrive does not wait.
+__device__ __forceinline__ void bar_sync(int id, int count) {
+    __syncwarp();
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(int id, int count) {
+    __syncwarp();
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
 // The loss sums of one launch: each row group (a CTA or a cluster) adds its rows in
-// order, writes a slot, and the group that takes the last ticket adds the slots.
+// order and writes a slot, and the group that takes the last ticket adds the slots.
 struct LossSums {
     double loss = 0.0, first = 0.0, second = 0.0, count = 0.0;
 };
 
-__device__ __forceinline__ void write_result(const LossArgs& a, double loss, double first, double second,
-                                             double count) {
-    a.result[0] = float(loss / a.n);
-    a.result[1] = float(first / a.n);
-    a.result[2] = float(second / a.n);
-    a.result[3] = float(count);
+// The four sums over the first B threads of the CTA, and the result.
+template <int B> __device__ __forceinline__ void write_sums(const LossArgs& a, double (&v)[4]) {
+    constexpr int nw = B / 32;
+    __shared__ double sh[4 * nw];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        v[c] = warp_sum(v[c]);
+        if (lane == 0) sh[4 * warp + c] = v[c];
+    }
+    bar_sync(5, B);
+    if (warp == 0) {   // lane 4 w + c: sum c of warp w (at most 8 warps)
+        double s = lane < 4 * nw ? sh[lane] : 0.0;
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) s += __shfl_xor_sync(~0u, s, o);
+        if (lane < 4) a.result[lane] = float(lane < 3 ? s * a.per_n : s);
+    }
 }
 
-// Called by every thread of the group's first CTA.  Thread 0 holds the sums.
-__device__ void pair_stage(const LossArgs& a, double* sh);
+template <int B> __device__ void pair_stage(const LossArgs& a);
 
-template <int OP>
+// Called by every thread of a group's first CTA.  The statistics warp's first lane, thread
+// B, holds the sums and has written the rows' outputs.
+template <int OP, int B>
 __device__ void finish(const LossArgs& a, const LossSums& sum, int group, int ngroups) {
-    __shared__ double sh[4 * 32];
     __shared__ bool last;
-    const int tid = threadIdx.x, nw = blockDim.x >> 5, warp = tid >> 5, lane = tid & 31;
-    __syncthreads();   // the CTA's row outputs come before its ticket
-    if (tid == 0) {
+    const int tid = threadIdx.x;
+    if (tid == B) {
         if (OP == kPolicy || OP == kDistill) {
-            double* o = a.slots + 4 * int64_t(group);
-            o[0] = sum.loss; o[1] = sum.first; o[2] = sum.second; o[3] = sum.count;
+            double2* o = reinterpret_cast<double2*>(a.slots) + 2 * group;
+            o[0] = make_double2(sum.loss, sum.first);
+            o[1] = make_double2(sum.second, sum.count);
         }
         __threadfence();
         last = atomicAdd(a.ticket, 1u) == uint32_t(ngroups - 1);
         if (last) __threadfence();
     }
     __syncthreads();
-    if (!last) return;
+    if (!last || tid >= B) return;
     if (OP == kPrefStat) {
-        pair_stage(a, sh);
+        pair_stage<B>(a);
     } else {
         double v[4] = {0.0, 0.0, 0.0, 0.0};
-        for (int i = tid; i < ngroups; i += blockDim.x)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) v[c] += __ldcg(a.slots + 4 * int64_t(i) + c);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            v[c] = warp_sum(v[c]);
-            if (lane == 0) sh[c * 32 + warp] = v[c];
+        for (int i = tid; i < ngroups; i += B) {
+            const double2 p = __ldcg(reinterpret_cast<const double2*>(a.slots) + 2 * i);
+            const double2 q = __ldcg(reinterpret_cast<const double2*>(a.slots) + 2 * i + 1);
+            v[0] += p.x; v[1] += p.y; v[2] += q.x; v[3] += q.y;
         }
-        __syncthreads();
-        if (tid == 0) {
-            for (int w = 1; w < nw; ++w)
-                for (int c = 0; c < 4; ++c) v[c] += sh[c * 32 + w];
-            write_result(a, v[0], v[1], v[2], v[3]);
-        }
+        write_sums<B>(a, v);
     }
     if (tid == 0) *a.ticket = 0;   // ready for the next call
 }
@@ -129,8 +143,9 @@ __device__ void finish(const LossArgs& a, const LossSums& sum, int group, int ng
 // The pairs, by the last CTA of the first preference pass: a warp sums the
 // log-ratios of one pair's two sequences (lanes strided, fp64), forms the pair's
 // loss and its derivative, and writes the gradient factor of each of its rows.
-__device__ void pair_stage(const LossArgs& a, double* sh) {
-    const int tid = threadIdx.x, nw = blockDim.x >> 5, warp = tid >> 5, lane = tid & 31;
+template <int B> __device__ void pair_stage(const LossArgs& a) {
+    constexpr int nw = B / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const float step = (a.seed ? *a.seed : 1.0f) * a.inv_n * a.it;
     // rows outside every sequence keep w = 0, written by the row pass
     double loss = 0.0, margin = 0.0, won = 0.0, count = 0.0;
@@ -170,14 +185,8 @@ __device__ void pair_stage(const LossArgs& a, double* sh) {
             loss += l; margin += h; won += h > 0.0f ? 1.0 : 0.0; count += 1.0;
         }
     }
-    if (lane == 0) { sh[warp] = loss; sh[32 + warp] = margin; sh[64 + warp] = won; sh[96 + warp] = count; }
-    __syncthreads();
-    if (tid == 0) {
-        double v[4] = {0.0, 0.0, 0.0, 0.0};
-        for (int c = 0; c < 4; ++c)
-            for (int w = 0; w < nw; ++w) v[c] += sh[c * 32 + w];
-        write_result(a, v[0], v[1], v[2], v[3]);
-    }
+    double v[4] = {loss, margin, won, count};   // the first lanes' pairs
+    write_sums<B>(a, v);
 }
 
 // Policy: the row's loss and g = dL/dlp.
@@ -274,19 +283,29 @@ template <> struct Vec<__half> {
 };
 
 // Where a row's elements lie: `head` elements up to the first 16-byte boundary, `body`
-// whole vectors from there, and a tail; the head and tail elements ("edges", fewer than
-// 2 N) are held one per thread by the first CTA of the group.
-template <typename T> struct Row {
-    const T* x;
-    int head, body, edges;
-    __device__ __forceinline__ Row(const T* p, int vocab) : x(p) {
+// whole vectors from there, and a tail.  The head and tail elements ("edges", fewer than
+// 2 N) are held one per thread by the first CTA of the group; [lo, hi) are the vectors of
+// this CTA's share.
+template <typename T> struct Place {
+    int head, body, edges, lo, hi;
+    __device__ __forceinline__ Place(const T* row, int vocab, int rank, int clog) {
         constexpr int N = Vec<T>::N;
-        const int ph = int((reinterpret_cast<uintptr_t>(p) / sizeof(T)) % N);
+        const int ph = int((reinterpret_cast<uintptr_t>(row) / sizeof(T)) % N);
         head = ph == 0 ? 0 : min(N - ph, vocab);
         body = (vocab - head) / N;
         edges = vocab - body * N;
+        const int share = (body + (1 << clog) - 1) >> clog;
+        lo = min(body, rank * share);
+        hi = min(body, lo + share);
     }
     __device__ __forceinline__ int edge_at(int i) const { return i < head ? i : i + body * Vec<T>::N; }
+    // whether element j is this CTA's: edge element `i`, or in vector `i` of the row
+    __device__ __forceinline__ bool owns(int j, int rank, bool& at_edge, int& i) const {
+        i = (j - head) / Vec<T>::N;
+        at_edge = j < head || i >= body;
+        if (at_edge) i = j < head ? j : j - body * Vec<T>::N;
+        return at_edge ? rank == 0 : i >= lo && i < hi;
+    }
 };
 
 // Vector stores need the gradient row at the logits' phase; other rows are stored by elements.
@@ -311,13 +330,22 @@ __device__ __forceinline__ bool same_phase(const T* x, const T* dx) {
 // ---------------------------------------------------------------------------
 
 constexpr int kMaxCluster = 8;
-constexpr int kMaxWarps = 8;   // 256 threads
 
 __device__ __forceinline__ uint32_t cluster_rank() { uint32_t r; asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r)); return r; }
-__device__ __forceinline__ void cluster_barrier() {
+// The cluster's barrier in halves.  Only the statistics warps write into other CTAs, so
+// only their arrival releases: a releasing arrival of the others would wait for the
+// gradient's stores.
+__device__ __forceinline__ void cluster_arrive() {
     __syncwarp();
-    asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void store_remote(const void* smem, uint32_t rank, float4 v) {
     uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(smem)), to;
@@ -331,24 +359,24 @@ __device__ __forceinline__ float warp_max(float v) {
 }
 
 // The sum at temperature 1 beside the one at tau (distillation with both terms).  For tau
-// = 2, 3 or 4 (pow) its exponentials are powers of the tempered ones; else (pow = 0) they
-// are taken from the logits.
-__device__ __forceinline__ float untempered(float e, float x, float v, int pow) {
-    if (pow == 0) return ex2(__fmaf_rn(x, kLog2e, -v));
-    float r = e * e;
-    if (pow == 3) r *= e;
-    if (pow == 4) r *= r;
-    return r;
+// = 2 or 4 (POW) its exponentials are powers of the tempered ones; else (POW = 0) they are
+// taken from the logits.
+template <int POW> __device__ __forceinline__ float untempered(float e, float x, float v) {
+    if (POW == 0) return ex2(__fmaf_rn(x, kLog2e, -v));
+    const float r = e * e;
+    return POW == 4 ? r * r : r;
 }
 // The exponent's reference at temperature 1 for a largest element m, u = m c2.
-__device__ __forceinline__ float untempered_ref(float m, float u, int pow) { return pow == 0 ? m * kLog2e : u * float(pow); }
-__device__ __forceinline__ float rescale1(float m, float to, float c2, int pow) {
+template <int POW> __device__ __forceinline__ float untempered_ref(float m, float u) {
+    return POW == 0 ? m * kLog2e : u * float(POW);
+}
+template <int POW> __device__ __forceinline__ float rescale1(float m, float to, float c2) {
     if (m == kNegInf) return 1.0f;
-    return ex2(big(to) ? (m - to) * kLog2e : untempered_ref(m, m * c2, pow) - untempered_ref(to, to * c2, pow));
+    return ex2(big(to) ? (m - to) * kLog2e : untempered_ref<POW>(m, m * c2) - untempered_ref<POW>(to, to * c2));
 }
 // The same two exponentials of one element where m may be big.
-__device__ __forceinline__ float power1(float e, float x, float m, float c2, int pow) {
-    return big(m) ? ex2((x - m) * kLog2e) : untempered(e, x, untempered_ref(m, m * c2, pow), pow);
+template <int POW> __device__ __forceinline__ float power1(float e, float x, float m, float c2) {
+    return big(m) ? ex2((x - m) * kLog2e) : untempered<POW>(e, x, untempered_ref<POW>(m, m * c2));
 }
 
 __device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
@@ -361,6 +389,7 @@ constexpr int kMaxRingBytes = 220 * 1024;   // dynamic shared memory: tiles and 
 
 // A tile is kTileVecs vectors per thread, kStages of them are in shared memory.
 constexpr int kTileVecs = 8, kStages = 3;
+constexpr int kSingle = -1;   // POW of the kernels with one sum per row
 constexpr int64_t kRowsInL2 = 48 << 20;
 
 // How a launch lays its rows out: threads per CTA, and CTAs per row (2^clog).
@@ -368,314 +397,295 @@ struct RowShape {
     int threads, clog;
 };
 
-// One row at a time per group of `cluster` CTAs, each with a contiguous share of the
-// row's vectors.  The share comes through shared memory in tiles, copied asynchronously
-// ST - 1 tiles ahead of their use: while one row is worked on, the next ones are under
-// way.  A thread copies the vectors that it will itself use, so a tile needs no barrier.
-// Every thread keeps a running maximum and sum; the CTA's first warp joins its warps',
-// writes the CTA's part into every CTA of the group (distributed shared memory) and,
-// after one cluster barrier, joins the group's parts and works out the row's loss and
-// gradient factors; after a block barrier all warps write the gradient.  The factors are
-// the first warp's work alone: worked out by all warps they cost as many instructions as
-// the elements themselves.  A share of one tile is still in shared memory then, so the
-// row is read once; longer ones are streamed a second time.
-// DUAL: distillation with both terms at temperatures that differ, two sums per row.
-template <typename T, int OP, int B, bool DUAL>
-__global__ void __launch_bounds__(B, 512 / B) k_row(const LossArgs a, const int clog, const int pow) {
-    constexpr int N = Vec<T>::N, U = 4, tile = B * kTileVecs, ST = kStages;
+// A group of 2^clog CTAs takes one row at a time, each CTA a contiguous share of the row's
+// vectors.  The share comes through shared memory in tiles, copied asynchronously ahead of
+// their use; a thread copies the vectors that it will itself use, so a tile needs no
+// barrier.
+//
+// B threads work on the elements, in two passes over a row: A keeps each thread's running
+// maximum and sum, B writes the gradient.  One more warp has the statistics: it joins the
+// warps' parts, exchanges the CTAs' parts through distributed shared memory, and works
+// out the row's loss and gradient factors.  That takes about as long as a share, so pass B
+// of a row comes after pass A of the next one, and the element warps wait for nobody.
+// (Without the extra warp, and pass B right after A: 341 to 408 us for 4,096 x 128,256 bf16
+// policy rows, a third of the warps' time at barriers.)
+//
+// A share of at most one tile stays in shared memory between its passes, so the row is
+// read once; longer ones are streamed a second time, out of L2 (see shape_for).
+// POW: distillation with both terms at temperatures that differ, two sums per row (DUAL).
+template <typename T, int OP, int B, int POW>
+__global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row(const LossArgs a, const int clog) {
+    constexpr int N = Vec<T>::N, U = 4, tile = B * kTileVecs, ST = kStages, nw = B / 32;
+    constexpr bool DUAL = POW != kSingle;
     constexpr bool kTeach = OP == kDistill;
     constexpr bool kGrad = OP == kPolicy || OP == kDistill;
-    __shared__ float4 wparts[2][kMaxWarps];           // per warp, by row parity: m, s, s at temperature 1
-    __shared__ float4 tparts[2][kTeach ? kMaxWarps : 1]; // teacher: m, sum e, sum e (t - z), bad
-    __shared__ float4 cparts[2][kMaxCluster];         // per CTA of the group, by row parity
-    __shared__ float4 fac[2];                         // gradient factors of the row, from the first warp
-    extern __shared__ uint4 ring[];                   // [ST][tile] vectors; then [2][3][k] of id, t / tau, x
-    float* const teach = reinterpret_cast<float*>(ring + ST * tile);
-    constexpr int nw = B / 32;
+    __shared__ float4 wparts[2][nw];                // by row parity, per warp: m, s, s at temperature 1
+    __shared__ float4 tparts[2][kTeach ? nw : 1];   // teacher: m, sum e, sum e (t - z), bad
+    __shared__ float4 cparts[2][kMaxCluster];       // per CTA of the group
+    // Of four rows in turn: while a row is in pass A, its successor's factors may be worked
+    // out, its predecessor is in pass B and the one before that has its listed elements
+    // written; a warp may be a row ahead of another.
+    __shared__ float4 fac[4][2];                    // gradient factors
+    extern __shared__ uint4 ring[];                 // [ST][tile] vectors; then [4][3][kpad] of id, t / tau, x
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cluster = 1 << clog, rank = cluster > 1 ? int(cluster_rank()) : 0;
     const int group = int(blockIdx.x) >> clog, ngroups = int(gridDim.x) >> clog;
-    const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + 16u * uint32_t(tid);
     const float c2 = a.it * kLog2e;
     const bool kd_on = kTeach && a.k > 0, ce_on = kTeach && a.ce_weight > 0.0f;
+    const bool grad = kGrad && a.dx != nullptr;
     const float kNaN = __int_as_float(0x7fffffff);
-    const float step = (kGrad && a.seed ? *a.seed : 1.0f) * a.inv_n;
     LossSums sum;
-    int par = 0;
-
-    // this CTA's share of row r: [lo, hi) of its whole vectors
-    auto share_of = [&](const Row<T>& row, int& lo, int& hi) {
-        const int share = cluster > 1 ? (row.body + cluster - 1) >> clog : row.body;
-        lo = min(row.body, rank * share);
-        hi = min(row.body, lo + share);
-    };
-    // The copies run ahead in the order of their use: the tiles of a row, those of its
-    // second pass where there is one, the next row that is not ignored.
-    const bool twice = kGrad && a.dx != nullptr;   // a share longer than a tile is streamed again
-    int64_t fr = group - ngroups, fynext = a.target && group < a.rows ? a.target[group] : 0;
-    int fcount = 0, fleft = 0, fpass = 0;   // vectors of the share, those of this pass not yet asked for, passes after it
-    const T *fstart = nullptr, *fat = nullptr;   // this thread's first vector of the pass, and its next
-    auto fetch = [&](int slot) {
-        if (fleft <= 0 && fpass > 0) {
-            fpass = 0;
-            fleft = fcount;
-            fat = fstart;
-        } else if (fleft <= 0) {
-            int64_t y;
-            do {
-                fr += ngroups;
-                y = fynext;
-                fynext = a.target && fr + ngroups < a.rows ? a.target[fr + ngroups] : 0;
-                if (fr >= a.rows || y < 0) continue;
-                const Row<T> row(static_cast<const T*>(a.x) + fr * a.ld, a.vocab);
-                int lo, hi;
-                share_of(row, lo, hi);
-                fleft = fcount = hi - lo;
-                fpass = twice && fcount > tile ? 1 : 0;
-                fat = fstart = row.x + row.head + int64_t(lo + tid) * N;
-            } while (fr < a.rows && fleft <= 0);   // a share may be empty
-        }
-        // behind the last row a group is empty
-        const uint32_t to = ring_at + 16u * uint32_t(slot * tile);
-        if (fleft >= tile) {
-#pragma unroll
-            for (int i = 0; i < kTileVecs; ++i) copy_async(to + 16u * B * i, fat + B * N * i);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kTileVecs; ++i)
-                if (tid + B * i < fleft) copy_async(to + 16u * B * i, fat + B * N * i);
-        }
-        fat += tile * N;
-        fleft -= tile;
-        copy_commit();
-    };
-    int slot = 0;   // of the tile in use
-    auto next_tile = [&](bool first) {
-        if (!first) slot = slot + 1 == ST ? 0 : slot + 1;
-        fetch(slot == 0 ? ST - 1 : slot - 1);   // the slot of the tile before, which this thread has done with
-        copy_wait<ST - 1>();
-    };
-
-    if (cluster > 1) cluster_barrier();   // every CTA of the group runs before any writes into another
-#pragma unroll
-    for (int i = 0; i < ST - 1; ++i) fetch(i);
-    bool first = true;
+    int par = 0, buf4 = 0;   // of the row: which of two, which of four
     int64_t ynext = a.target && group < a.rows ? a.target[group] : 0;
-    for (int64_t r = group; r < a.rows; r += ngroups) {
+    // The label of row r, that of the group's next one under way.
+    auto label = [&](int64_t r) {
         const int64_t y = ynext;
         if (a.target && r + ngroups < a.rows) ynext = a.target[r + ngroups];
-        const Row<T> row(static_cast<const T*>(a.x) + r * a.ld, a.vocab);
-        T* dx = kGrad && a.dx ? static_cast<T*>(a.dx) + r * a.ldd : nullptr;
-        const bool whole = kGrad && same_phase(row.x, static_cast<const T*>(dx));
-        int lo, hi;
-        share_of(row, lo, hi);
-        const bool edge = rank == 0 && tid < row.edges;
-        if (y < 0) {
-            if (dx) {
-                for (int v = lo + tid; v < hi; v += B) store_vec<T>(dx + row.head + v * N, make_uint4(0, 0, 0, 0), whole);
-                if (edge) dx[row.edge_at(tid)] = from_f<T>(0.0f);
-            }
-            if (rank == 0 && tid == 0) {
-                if (OP != kDistill && a.logp) a.logp[r] = 0.0f;
-                if (kGrad && a.loss) a.loss[r] = 0.0f;
-                if (OP == kPrefStat) a.stat[r] = {0.0f, 0.0f, 0.0f, 0.0f};
-            }
-            continue;
+        return y;
+    };
+
+    if (warp == nw) {
+        // ------------------------------------------------------------ the statistics warp
+        const float step = (kGrad && a.seed ? *a.seed : 1.0f) * a.inv_n;
+        const bool out = rank == 0 && lane == 0;
+        if (cluster > 1) {   // every CTA of the group runs before any writes into another
+            cluster_arrive();
+            cluster_wait();
         }
-        const float xe = edge ? to_f(row.x[row.edge_at(tid)]) : kNegInf;
-        float xy = 0.0f, in1 = 0.0f, in2 = 0.0f, in3 = 0.0f;   // first warp: x_y, old, advantage, ref
-        if (warp == 0) {
-            xy = to_f(row.x[y < a.vocab ? y : 0]);
+        for (int64_t r = group; r < a.rows; r += ngroups) {
+            const int64_t y = label(r);
+            if (y < 0) {
+                if (out) {
+                    if (OP != kDistill && a.logp) a.logp[r] = 0.0f;
+                    if (kGrad && a.loss) a.loss[r] = 0.0f;
+                    if (OP == kPrefStat) a.stat[r] = {0.0f, 0.0f, 0.0f, 0.0f};
+                }
+                continue;
+            }
+            float xy = to_f(static_cast<const T*>(a.x)[r * a.ld + (y < a.vocab ? y : 0)]);
+            float old = 0.0f, adv = 0.0f, refl = 0.0f;
             if (OP == kPolicy) {
-                in1 = a.old_logp[r];
-                in2 = a.adv[r];
+                old = a.old_logp[r];
+                adv = a.adv[r];
             }
-            if (OP == kPolicy || OP == kPrefStat) in3 = a.ref_logp ? a.ref_logp[r] : 0.0f;
-        }
-        if (kTeach && kd_on && warp * 32 < a.k) {
-            // the teacher's entries, a few per thread: logit, id, and the student's logit there
-            float* const tb = teach + par * 3 * a.k;
-            float tm = kNegInf, ts = 0.0f, td = 0.0f, bad = 0.0f;
-            for (int i = tid; i < a.k; i += B) {
-                const int64_t id = teacher_id(a, r * a.ldt + i);
-                const bool on = id >= 0 && id < a.vocab;
-                const float t = on ? teacher_logit(a, r * a.ldt + i) * a.it : kNegInf;
-                const float z = on ? to_f(row.x[id]) : 0.0f;
-                if (id >= a.vocab) bad = kNaN;
-                tb[i] = __int_as_float(on ? int(id) : -1);
-                tb[a.k + i] = t;
-                tb[2 * a.k + i] = z;
-                // running form: the entries of one thread are few
-                const float nm = fmaxf(tm, t), nr = part_ref(nm);
-                const float f = ex2((part_ref(tm) - nr) * kLog2e);
-                const float e = ex2((t - nr) * kLog2e);
-                ts = (tm == kNegInf ? ts : ts * f) + e;
-                td = (tm == kNegInf ? td : f != 0.0f ? td * f : 0.0f) + (e != 0.0f ? e * (t - z * a.it) : 0.0f);
-                tm = nm;
-            }
-            const float wm = warp_max(tm), wr = part_ref(wm);
-            const float f = tm == kNegInf ? 1.0f : ex2((tm - wr) * kLog2e);
-            ts = warp_sum(ts * f);
-            td = warp_sum(f != 0.0f ? td * f : 0.0f);
-            bad = warp_sum(bad);
-            if (lane == 0) tparts[par][warp] = make_float4(wm, ts, td, bad);
-        }
-        // the thread's largest element and its sums, U vectors at a time
-        float m = kNegInf, acc[2] = {0.0f, 0.0f}, acc1[2] = {0.0f, 0.0f};
-        auto raise = [&](float top) {   // the sums so far to a larger element
-            if (top == m) return;
-            const float f = rescale(m, top, c2);
-            acc[0] *= f;
-            acc[1] *= f;
-            if (DUAL) {
-                const float f1 = rescale1(m, top, c2, pow);
-                acc1[0] *= f1;
-                acc1[1] *= f1;
-            }
-            m = top;
-        };
-        auto add_big = [&](const uint4* at) {
-#pragma unroll 1
-            for (int j = 0; j < N; ++j) {
-                const float x = to_f(reinterpret_cast<const T*>(at)[j]), d = x - part_ref(m);
-                acc[0] += ex2(d * c2);
-                if (DUAL) acc1[0] += ex2(d * kLog2e);
-            }
-        };
-        auto add = [&](uint4 raw, float u, float v) {
-            float f[N];
-            Vec<T>::wide(raw, f);
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const float e = ex2(__fmaf_rn(f[j], c2, -u));
-                acc[j & 1] += e;
-                if (DUAL) acc1[j & 1] += untempered(e, f[j], v, pow);
-            }
-        };
-        for (int left = hi - lo; left > 0; left -= tile) {
-            next_tile(first);
-            first = false;
-            const uint4* const buf = ring + slot * tile + tid;
-            const int mine = left - tid;   // vector i of the thread exists where B i < mine
-#pragma unroll 1
-            for (int g = 0; g < kTileVecs; g += U) {
-                if (B * g >= mine) break;
-                uint4 raw[U];
-                if (B * (g + U - 1) < mine) {
-#pragma unroll
-                    for (int i = 0; i < U; ++i) raw[i] = buf[B * (g + i)];
-                } else {
-#pragma unroll
-                    for (int i = 0; i < U; ++i) {
-                        raw[i] = make_uint4(Vec<T>::kEmpty, Vec<T>::kEmpty, Vec<T>::kEmpty, Vec<T>::kEmpty);
-                        if (B * (g + i) < mine) raw[i] = buf[B * (g + i)];
-                    }
-                }
-                float top = m;
-#pragma unroll
-                for (int i = 0; i < U; ++i) top = fmaxf(top, Vec<T>::top(raw[i]));
-                raise(top);
-                if (big(part_ref(m))) {
-#pragma unroll 1
-                    for (int i = 0; i < U; ++i)
-                        if (B * (g + i) < mine) add_big(buf + B * (g + i));
-                } else {
-                    const float u = part_ref(m) * c2, u1 = DUAL ? untempered_ref(part_ref(m), u, pow) : 0.0f;
-#pragma unroll
-                    for (int i = 0; i < U; ++i) add(raw[i], u, u1);
-                }
-            }
-        }
-        {
-            // the warp's part, edges included
-            const float top = warp_max(fmaxf(m, xe)), ref = part_ref(top);
-            const float ee = power(xe, ref, c2);
-            const float s = warp_sum((acc[0] + acc[1]) * rescale(m, ref, c2) + ee);
-            float s1 = 0.0f;
-            if (DUAL) s1 = warp_sum((acc1[0] + acc1[1]) * rescale1(m, ref, c2, pow) + power1(ee, xe, ref, c2, pow));
-            if (lane == 0) wparts[par][warp] = make_float4(top, s, s1, 0.0f);
-        }
-        __syncthreads();
-        float S = 0.0f, S1 = 0.0f, M = kNegInf;
-        auto join = [&](float4 p) {   // the first warp: lane i holds part i, the others an empty one
-            M = warp_max(p.x);
-            S = warp_sum(p.y * rescale(p.x, part_ref(M), c2));
-            if (DUAL) S1 = warp_sum(p.z * rescale1(p.x, part_ref(M), c2, pow));
-        };
-        const float4 none = make_float4(kNegInf, 0.0f, 0.0f, 0.0f);
-        if (warp == 0) {
+            if (OP == kPolicy || OP == kPrefStat) refl = a.ref_logp ? a.ref_logp[r] : 0.0f;
+            // x_y has arrived before this CTA lets any other overwrite the row in place
+            xy = __shfl_sync(~0u, xy, 0);
+            float S = 0.0f, S1 = 0.0f, M = kNegInf;
+            auto join = [&](float4 p) {   // lane i holds part i, the others an empty one
+                M = warp_max(p.x);
+                S = warp_sum(p.y * rescale(p.x, part_ref(M), c2));
+                if (DUAL) S1 = warp_sum(p.z * rescale1<POW>(p.x, part_ref(M), c2));
+            };
+            const float4 none = make_float4(kNegInf, 0.0f, 0.0f, 0.0f);
+            bar_sync(1 + par, B + 32);
             join(lane < nw ? wparts[par][lane] : none);
-            if (cluster > 1 && lane < cluster) store_remote(&cparts[par][rank], uint32_t(lane), make_float4(M, S, S1, 0.0f));
-        }
-        if (cluster > 1) {
-            cluster_barrier();
-            if (warp == 0) join(lane < cluster ? cparts[par][lane] : none);
-        }
-        if (warp == 0) {
+            float tm = kNegInf, ts = 0.0f, td = 0.0f, tbad = 0.0f;
+            auto teacher = [&]() {
+                const float4 p = lane < nw && lane * 32 < a.k ? tparts[par][lane] : none;
+                tm = warp_max(p.x);
+                const float f = rescale(p.x, part_ref(tm), kLog2e);
+                ts = warp_sum(p.y * f);
+                td = warp_sum(f != 0.0f ? p.z * f : 0.0f);
+                tbad = warp_sum(p.w);
+            };
+            if (cluster > 1) {
+                if (lane < cluster) store_remote(&cparts[par][rank], uint32_t(lane), make_float4(M, S, S1, 0.0f));
+                cluster_arrive();
+                if (kd_on) teacher();
+                cluster_wait();
+                join(lane < cluster ? cparts[par][lane] : none);
+            } else if (kd_on) {
+                teacher();
+            }
             float bad = y >= a.vocab || M == kNegInf ? kNaN : 0.0f;
             const float lg = log2f(S);
             const float gap = big(M) ? (xy - M) * c2 : __fmaf_rn(xy, c2, -(M * c2));   // log2 of the label's exponential
             const float lp = (gap - lg) * kLn2 + bad;
-            const bool out = rank == 0 && lane == 0;
             if (OP == kLogprob || OP == kPrefStat) {
                 if (out && a.logp) a.logp[r] = lp;
-                if (OP == kPrefStat && out) a.stat[r] = {M + bad, 1.0f / S, 0.0f, lp - in3};
+                if (OP == kPrefStat && out) a.stat[r] = {M + bad, 1.0f / S, 0.0f, lp - refl};
             } else if (OP == kPolicy) {
                 float loss, sur, kl;
-                const float w = policy_row(a, lp, in1, in2, in3, loss, sur, kl) * step * a.it;
+                const float w = policy_row(a, lp, old, adv, refl, loss, sur, kl) * step * a.it;
+                // the label's element: w (1 - q)
+                if (lane == 0) fac[buf4][0] = make_float4(M + bad, -w / S, __fmaf_rn(ex2(gap), -w / S, w), 0.0f);
                 if (out) {
                     if (a.logp) a.logp[r] = lp;
                     if (a.loss) a.loss[r] = loss;
                     sum.loss += loss; sum.first += sur; sum.second += kl; sum.count += 1.0;
                 }
-                // the label's element: w (1 - q)
-                if (lane == 0) fac[0] = make_float4(M + bad, -w / S, __fmaf_rn(ex2(gap), -w / S, w), 0.0f);
             } else {
-                float tm = kNegInf, ts = 0.0f, td = 0.0f;
-                bool row_kd = false;
-                if (kd_on) {
-                    const float4 p = lane < nw && lane * 32 < a.k ? tparts[par][lane] : none;
-                    tm = warp_max(p.x);
-                    const float f = p.x == kNegInf ? 1.0f : ex2((p.x - part_ref(tm)) * kLog2e);
-                    ts = warp_sum(p.y * f);
-                    td = warp_sum(f != 0.0f ? p.z * f : 0.0f);
-                    bad += warp_sum(p.w);
-                    row_kd = ts != 0.0f;
+                bad += tbad;
+                const bool row_kd = ts != 0.0f;
+                // factors of the exponentials at the temperature and at 1, and of the teacher's
+                // (e_i = exp(t_i - tm) times wp; 0: none)
+                const float wk = row_kd ? a.kd_weight * step / a.it : 0.0f, wc = ce_on ? a.ce_weight * step : 0.0f;
+                const float kq = wk / S + (DUAL ? 0.0f : wc / S) + bad;
+                if (lane == 0) {
+                    fac[buf4][0] = make_float4(M + bad, row_kd || (!DUAL && ce_on) || bad != 0.0f ? kq : 0.0f,
+                                              DUAL ? wc / S1 : 0.0f, tm);
+                    fac[buf4][1] = make_float4(row_kd ? wk / ts : 0.0f, bad, xy, wc);
                 }
                 const float lz = big(M) ? __fmaf_rn(M, a.it, lg * kLn2) : (M * c2 + lg) * kLn2;   // log sum exp z
                 const float kd = row_kd ? (td / ts - tm - logf(ts) + lz) / (a.it * a.it) + bad : bad;
                 float log_sum1 = 0.0f;   // log sum exp x
-                if (DUAL) log_sum1 = big(M) ? M + logf(S1) : (untempered_ref(M, M * c2, pow) + log2f(S1)) * kLn2;
+                if (DUAL) log_sum1 = big(M) ? M + logf(S1) : (untempered_ref<POW>(M, M * c2) + log2f(S1)) * kLn2;
                 const float ce = ce_on ? (DUAL ? log_sum1 - xy : -lp) + bad : 0.0f;
                 const float loss = (row_kd ? a.kd_weight * kd : bad) + (ce_on ? a.ce_weight * ce : 0.0f);
                 if (out) {
                     if (a.loss) a.loss[r] = loss;
                     sum.loss += loss; sum.first += kd; sum.second += ce; sum.count += 1.0;
                 }
-                // factors of the exponentials at the temperature and at 1, and of the teacher's
-                // (e_i = exp(t_i - tm) times wp; 0: none)
-                const float wk = row_kd ? a.kd_weight * step / a.it : 0.0f, wc = ce_on ? a.ce_weight * step : 0.0f;
-                const float kq = wk / S + (DUAL ? 0.0f : wc / S) + bad;
-                if (lane == 0) {
-                    fac[0] = make_float4(M + bad, row_kd || (!DUAL && ce_on) || bad != 0.0f ? kq : 0.0f, DUAL ? wc / S1 : 0.0f, tm);
-                    fac[1] = make_float4(row_kd ? wk / ts : 0.0f, bad, xy, wc);
-                }
             }
+            bar_arrive(3 + par, B + 32);
+            par ^= 1;
+            buf4 = (buf4 + 1) & 3;
         }
-        if (kGrad && dx) {
-            __syncthreads();
-            const float4 fc = fac[0];
+    } else {
+        // ------------------------------------------------------------ the element warps
+        const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + 16u * uint32_t(tid);
+        float* const teach = reinterpret_cast<float*>(ring + ST * tile);
+        const int kpad = (a.k + 3) & ~3;
+        auto row_at = [&](int64_t r) { return static_cast<const T*>(a.x) + r * a.ld; };
+        // all rows lie alike where their stride is a multiple of 16 bytes
+        const bool alike = (a.ld * int(sizeof(T))) % 16 == 0;
+        const Place<T> first_place(static_cast<const T*>(a.x), a.vocab, rank, clog);
+        auto place_of = [&](const T* x) { return alike ? first_place : Place<T>(x, a.vocab, rank, clog); };
+        // Between its passes a share stays in its slot (kept) where it fits a tile, whatever
+        // the row's phase; else its tiles are copied again.
+        const bool kept = grad && (a.vocab / N + cluster - 1) >> clog <= tile;
+        const bool again = grad && !kept;
+        // The copies run ahead in the order of their use.
+        int64_t fr = group - ngroups, fynext = a.target && group < a.rows ? a.target[group] : 0;
+        const T *fat = nullptr, *flast = nullptr;   // this thread's next vector, and where row fr's start
+        int fleft = 0, nlast = 0;                   // vectors left of the pass, and of the row's share
+        bool fback = false;                         // the pass is B
+        auto segment = [&]() {
+            if (again && nlast > 0 && !fback) {   // pass B of the row whose pass A is asked for
+                fat = flast;
+                fleft = nlast;
+                fback = true;
+                return;
+            }
+            fback = false;
+            nlast = 0;
+            while (nlast <= 0) {   // the next row that is not ignored and of which this CTA has a share
+                fr += ngroups;
+                if (fr >= a.rows) break;
+                const int64_t y = fynext;
+                if (a.target && fr + ngroups < a.rows) fynext = a.target[fr + ngroups];
+                if (y < 0) continue;
+                const T* const x = row_at(fr);
+                const Place<T> pl = place_of(x);
+                nlast = pl.hi - pl.lo;
+                flast = x + pl.head + (pl.lo + tid) * N;
+            }
+            fat = flast;
+            fleft = nlast;
+        };
+        auto fetch = [&](int slot) {
+            if (fleft <= 0) segment();
+            const uint32_t to = ring_at + 16u * uint32_t(slot * tile);
+            if (fleft >= tile) {
+#pragma unroll
+                for (int i = 0; i < kTileVecs; ++i) copy_async(to + 16u * B * i, fat + B * N * i);
+            } else {   // behind the last row a group is empty
+#pragma unroll
+                for (int i = 0; i < kTileVecs; ++i)
+                    if (tid + B * i < fleft) copy_async(to + 16u * B * i, fat + B * N * i);
+            }
+            fat += tile * N;
+            fleft -= tile;
+            copy_commit();
+        };
+        int slot = -1;   // of the tile last taken
+        auto take_tile = [&]() {
+            const int before = slot;
+            slot = slot + 1 == ST ? 0 : slot + 1;
+            if (kept) {
+                copy_wait<ST - 2>();
+            } else {   // the tile before is done with; its slot is the next to fill
+                fetch(before < 0 ? ST - 1 : before);
+                copy_wait<ST - 1>();
+            }
+        };
+
+        // the teacher's entry of this thread for the group's next row
+        int64_t nid = -1;
+        float nt = 0.0f;
+        auto ask_teacher = [&](int64_t r) {
+            if (tid < a.k && r < a.rows) {
+                nid = teacher_id(a, r * a.ldt + tid);
+                nt = teacher_logit(a, r * a.ldt + tid);
+            }
+        };
+
+        // The listed elements of a row (the teacher's and the label), written again over the
+        // dense gradient once every warp has stored its part of that: an id's first entry
+        // takes the weights of all that are equal to it.
+        int64_t listed = -1, listed_y = 0;
+        int listed_buf = 0;
+        auto relist = [&]() {
+            const float4 fc = fac[listed_buf][0], f1 = fac[listed_buf][1];
+            const float Mb = fc.x, kq = fc.y, cq = fc.z, tm = fc.w, wp = f1.x, bad = f1.y;
+            const int n = wp != 0.0f ? a.k : 0, entries = n + (ce_on && bad == 0.0f ? 1 : 0);
+            const float* const tb = teach + listed_buf * 3 * kpad;
+            const int* const ids = reinterpret_cast<const int*>(tb);
+            const Place<T> pl = place_of(row_at(listed));
+            T* const dx = static_cast<T*>(a.dx) + listed * a.ldd;
+            for (int i = tid; i < entries; i += B) {
+                const int id = i < n ? ids[i] : int(listed_y);
+                bool at_edge;
+                int v;
+                if (id < 0 || !pl.owns(id, rank, at_edge, v)) continue;
+                int same = 0;   // entries of this id
+#pragma unroll 4
+                for (int j = 0; j < n; j += 4) {   // ids are padded with -1 to a multiple of 4
+                    const int4 q = *reinterpret_cast<const int4*>(ids + j);
+                    same += int(q.x == id) + int(q.y == id) + int(q.z == id) + int(q.w == id);
+                }
+                float w = ce_on && id == int(listed_y) ? f1.w : 0.0f;
+                if (same == 1 && i < n) {
+                    w = __fmaf_rn(wp, ex2((tb[kpad + i] - tm) * kLog2e), w);
+                } else {
+                    bool lead = true;
+                    for (int j = 0; j < n; ++j) {
+                        if (ids[j] != id) continue;
+                        lead = lead && j >= i;
+                        w = __fmaf_rn(wp, ex2((tb[kpad + j] - tm) * kLog2e), w);
+                    }
+                    if (!lead) continue;
+                }
+                const float x = i < n ? tb[2 * kpad + i] : f1.z, e = power(x, Mb, c2);
+                dx[id] = from_f<T>((DUAL ? __fmaf_rn(power1<POW>(e, x, Mb, c2), cq, e * kq) : e * kq) - w);
+            }
+            listed = -1;
+        };
+
+        // pass B of row r: its label, the value of this thread's edge element, its slot (kept)
+        auto back = [&](int64_t r, int64_t y, float xe, int kept_slot, int was, int buffer) {
+            bar_sync(3 + was, B + 32);   // the row's factors
+            if (!grad) return;
+            if (kTeach && listed >= 0) relist();
+            const T* const x = row_at(r);
+            const Place<T> pl = place_of(x);
+            const int lo = pl.lo, hi = pl.hi;
+            T* const dx = static_cast<T*>(a.dx) + r * a.ldd;
+            const bool whole = same_phase(x, static_cast<const T*>(dx));
+            const bool edge = rank == 0 && tid < pl.edges;
+            const float4 fc = fac[buffer][0];
             const float Mb = fc.x, kq = fc.y, cq = OP == kDistill ? fc.z : 0.0f;
-            const float u = Mb * c2, v1 = DUAL ? untempered_ref(Mb, u, pow) : 0.0f;
+            const float u = Mb * c2, v1 = DUAL ? untempered_ref<POW>(Mb, u) : 0.0f;
             auto dense = [&](float x) {
                 const float e = power(x, Mb, c2);
-                return DUAL ? __fmaf_rn(power1(e, x, Mb, c2, pow), cq, e * kq) : e * kq;
+                return DUAL ? __fmaf_rn(power1<POW>(e, x, Mb, c2), cq, e * kq) : e * kq;
             };
             for (int done = 0; done < hi - lo; done += tile) {
-                if (hi - lo > tile) next_tile(false);
-                const uint4* const buf = ring + slot * tile + tid;
-                const int mine = hi - lo - done - tid;
-                T* const to = dx + row.head + int64_t(lo + done + tid) * N;
+                if (!kept) take_tile();
+                const uint4* const buf = ring + (kept ? kept_slot : slot) * tile + tid;
+                const int mine = hi - lo - done - tid;   // vector i of the thread exists where B i < mine
+                T* const to = dx + pl.head + (lo + done + tid) * N;
                 if (big(Mb)) {   // NaN rows too
 #pragma unroll 1
                     for (int i = 0; i < kTileVecs && B * i < mine; ++i)
@@ -690,60 +700,211 @@ __global__ void __launch_bounds__(B, 512 / B) k_row(const LossArgs a, const int 
 #pragma unroll
                     for (int j = 0; j < N; ++j) {
                         const float e = ex2(__fmaf_rn(f[j], c2, -u));
-                        f[j] = DUAL ? __fmaf_rn(untempered(e, f[j], v1, pow), cq, e * kq) : e * kq;
+                        f[j] = DUAL ? __fmaf_rn(untempered<POW>(e, f[j], v1), cq, e * kq) : e * kq;
                     }
                     store_vec<T>(to + B * N * i, Vec<T>::narrow(f), whole);
                 };
-                if (whole && B * (kTileVecs - 1) < mine) {
-#pragma unroll
-                    for (int i = 0; i < kTileVecs; ++i) emit(i);
-                } else {
 #pragma unroll 1
-                    for (int i = 0; i < kTileVecs && B * i < mine; ++i) emit(i);
-                }
-            }
-            // who holds element j: the edges' threads of the first CTA, else the share
-            auto owned = [&](int j, int& holder) {
-                const int v = (j - row.head) / N;
-                if (j < row.head || v >= row.body) {
-                    holder = j < row.head ? j : j - row.body * N;
-                    return rank == 0;
-                }
-                holder = (v - lo) & (B - 1);   // tiles are whole multiples of B
-                return v >= lo && v < hi;
-            };
-            if (edge) dx[row.edge_at(tid)] = from_f<T>(dense(xe));
-            if (OP == kPolicy) {
-                // the label's element again, by the thread that stored it
-                int holder;
-                if (y < a.vocab && owned(int(y), holder) && holder == tid) dx[y] = from_f<T>(fc.z);
-            } else {
-                // the listed elements again, once the CTA has stored its share: an id's first
-                // entry takes the weights of all that are equal to it
-                const float4 f1 = fac[1];   // teacher's factor, bad, x_y, the label's weight
-                const float tm = fc.w, wp = f1.x, bad = f1.y;
-                const int n = wp != 0.0f ? a.k : 0, entries = n + (ce_on && bad == 0.0f ? 1 : 0);
-                const float* const tb = teach + par * 3 * a.k;
-                __syncthreads();
-                for (int i = tid; i < entries; i += B) {
-                    const int id = i < n ? __float_as_int(tb[i]) : int(y);
-                    int holder;
-                    if (id < 0 || !owned(id, holder)) continue;
-                    float v = ce_on && id == int(y) ? f1.w : 0.0f;
-                    bool lead = true;
-                    for (int j = 0; j < n; ++j) {
-                        if (__float_as_int(tb[j]) != id) continue;
-                        if (j < i) { lead = false; break; }
-                        v = __fmaf_rn(wp, ex2((tb[a.k + j] - tm) * kLog2e), v);
+                for (int g = 0; g < kTileVecs; g += U) {
+                    if (whole && B * (g + U - 1) < mine) {
+#pragma unroll
+                        for (int i = 0; i < U; ++i) emit(g + i);
+                    } else {
+#pragma unroll 1
+                        for (int i = g; i < g + U && B * i < mine; ++i) emit(i);
                     }
-                    if (lead) dx[id] = from_f<T>(dense(i < n ? tb[2 * a.k + i] : f1.z) - v);
                 }
             }
+            if (kept && hi > lo) fetch(kept_slot);
+            if (edge) dx[pl.edge_at(tid)] = from_f<T>(dense(xe));
+            if (OP == kPolicy && y < a.vocab) {
+                // the label's element again, by the thread that stored it
+                bool at_edge;
+                int v;
+                if (pl.owns(int(y), rank, at_edge, v) && (at_edge ? v : (v - lo) & (B - 1)) == tid) dx[y] = from_f<T>(fc.z);
+            }
+            if (kTeach) {
+                listed = r;
+                listed_y = y;
+                listed_buf = buffer;
+            }
+        };
+
+#pragma unroll
+        for (int i = 0; i < ST - 1; ++i) fetch(i);
+        if (kept) fetch(ST - 1);
+        if (kTeach && kd_on) ask_teacher(group);
+        if (cluster > 1) {
+            cluster_arrive_relaxed();
+            cluster_wait();
         }
-        par ^= 1;
+        // the row whose pass B is next
+        int64_t back_row = -1, back_y = 0;
+        float back_xe = 0.0f;
+        int back_slot = 0, back_par = 0, back_buf = 0;
+        bool exchanged = false;   // some row's parts went to the cluster
+        for (int64_t r = group;; r += ngroups) {
+            const bool live = r < a.rows;
+            int64_t y = 0;
+            float xe = kNegInf;
+            if (live) {
+                y = label(r);
+                const T* const x = row_at(r);
+                const Place<T> pl = place_of(x);
+                const int lo = pl.lo, hi = pl.hi;
+                const bool edge = rank == 0 && tid < pl.edges;
+                if (y < 0) {
+                    if (grad) {
+                        T* const dx = static_cast<T*>(a.dx) + r * a.ldd;
+                        const bool whole = same_phase(x, static_cast<const T*>(dx));
+                        for (int v = lo + tid; v < hi; v += B) store_vec<T>(dx + pl.head + v * N, make_uint4(0, 0, 0, 0), whole);
+                        if (edge) dx[pl.edge_at(tid)] = from_f<T>(0.0f);
+                    }
+                    if (kTeach && kd_on) ask_teacher(r + ngroups);
+                    continue;
+                }
+                if (edge) xe = to_f(x[pl.edge_at(tid)]);
+                // the teacher's entry of this thread (asked for a row ago), and the student's logit there
+                const int64_t id0 = nid;
+                const float t0 = nt;
+                float z0 = 0.0f;
+                if (kTeach && kd_on) {
+                    if (tid < a.k && id0 >= 0 && id0 < a.vocab) z0 = to_f(x[id0]);
+                    ask_teacher(r + ngroups);
+                }
+                // pass A: the thread's largest element and its sums, U vectors at a time
+                float m = kNegInf, acc[2] = {0.0f, 0.0f}, acc1[2] = {0.0f, 0.0f};
+                auto raise = [&](float top) {   // the sums so far to a larger element
+                    if (top == m) return;
+                    const float f = rescale(m, top, c2);
+                    acc[0] *= f;
+                    acc[1] *= f;
+                    if (DUAL) {
+                        const float f1 = rescale1<POW>(m, top, c2);
+                        acc1[0] *= f1;
+                        acc1[1] *= f1;
+                    }
+                    m = top;
+                };
+                auto add_big = [&](const uint4* at) {
+#pragma unroll 1
+                    for (int j = 0; j < N; ++j) {
+                        const float x = to_f(reinterpret_cast<const T*>(at)[j]), d = x - part_ref(m);
+                        acc[0] += ex2(d * c2);
+                        if (DUAL) acc1[0] += ex2(d * kLog2e);
+                    }
+                };
+                auto add = [&](uint4 raw, float u, float v) {
+                    float f[N];
+                    Vec<T>::wide(raw, f);
+#pragma unroll
+                    for (int j = 0; j < N; ++j) {
+                        const float e = ex2(__fmaf_rn(f[j], c2, -u));
+                        acc[j & 1] += e;
+                        if (DUAL) acc1[j & 1] += untempered<POW>(e, f[j], v);
+                    }
+                };
+                for (int left = hi - lo; left > 0; left -= tile) {
+                    take_tile();
+                    const uint4* const buf = ring + slot * tile + tid;
+                    const int mine = left - tid;
+#pragma unroll 1
+                    for (int g = 0; g < kTileVecs; g += U) {
+                        if (B * g >= mine) break;
+                        uint4 raw[U];
+                        if (B * (g + U - 1) < mine) {
+#pragma unroll
+                            for (int i = 0; i < U; ++i) raw[i] = buf[B * (g + i)];
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < U; ++i) {
+                                raw[i] = make_uint4(Vec<T>::kEmpty, Vec<T>::kEmpty, Vec<T>::kEmpty, Vec<T>::kEmpty);
+                                if (B * (g + i) < mine) raw[i] = buf[B * (g + i)];
+                            }
+                        }
+                        float top = m;
+#pragma unroll
+                        for (int i = 0; i < U; ++i) top = fmaxf(top, Vec<T>::top(raw[i]));
+                        raise(top);
+                        if (big(part_ref(m))) {
+#pragma unroll 1
+                            for (int i = 0; i < U; ++i)
+                                if (B * (g + i) < mine) add_big(buf + B * (g + i));
+                        } else {
+                            const float u = part_ref(m) * c2, u1 = DUAL ? untempered_ref<POW>(part_ref(m), u) : 0.0f;
+#pragma unroll
+                            for (int i = 0; i < U; ++i) add(raw[i], u, u1);
+                        }
+                    }
+                }
+                {
+                    // the warp's part, edges included
+                    const float top = warp_max(fmaxf(m, xe)), ref = part_ref(top);
+                    const float ee = power(xe, ref, c2);
+                    const float s = warp_sum((acc[0] + acc[1]) * rescale(m, ref, c2) + ee);
+                    float s1 = 0.0f;
+                    if (DUAL) s1 = warp_sum((acc1[0] + acc1[1]) * rescale1<POW>(m, ref, c2) + power1<POW>(ee, xe, ref, c2));
+                    if (lane == 0) wparts[par][warp] = make_float4(top, s, s1, 0.0f);
+                }
+                if (kTeach && kd_on && warp * 32 < a.k) {
+                    // the teacher's largest logit and sums over the warp's entries; the first of each
+                    // thread is in registers
+                    float* const tb = teach + buf4 * 3 * kpad;
+                    if (tid < kpad - a.k) tb[a.k + tid] = __int_as_float(-1);
+                    float tm = kNegInf, ts = 0.0f, td = 0.0f, bad = 0.0f;
+                    for (int i = tid; i < a.k; i += B) {
+                        const int64_t id = i == tid ? id0 : teacher_id(a, r * a.ldt + i);
+                        const bool on = id >= 0 && id < a.vocab;
+                        const float t = !on ? kNegInf : (i == tid ? t0 : teacher_logit(a, r * a.ldt + i)) * a.it;
+                        const float z = !on ? 0.0f : i == tid ? z0 : to_f(x[id]);
+                        if (id >= a.vocab) bad = kNaN;
+                        tb[i] = __int_as_float(on ? int(id) : -1);
+                        tb[kpad + i] = t;
+                        tb[2 * kpad + i] = z;
+                        const float nm = fmaxf(tm, t), f = rescale(tm, part_ref(nm), kLog2e), e = power(t, part_ref(nm), kLog2e);
+                        ts = ts * f + e;
+                        td = (f != 0.0f ? td * f : 0.0f) + (e != 0.0f ? e * (t - z * a.it) : 0.0f);
+                        tm = nm;
+                    }
+                    const float wm = warp_max(tm), f = rescale(tm, part_ref(wm), kLog2e);
+                    ts = warp_sum(ts * f);
+                    td = warp_sum(f != 0.0f ? td * f : 0.0f);
+                    bad = warp_sum(bad);
+                    if (lane == 0) tparts[par][warp] = make_float4(wm, ts, td, bad);
+                }
+                if (cluster > 1) {
+                    if (exchanged) cluster_wait();   // of the row before: long past
+                    cluster_arrive_relaxed();
+                    exchanged = true;
+                }
+                bar_arrive(1 + par, B + 32);
+            }
+            if (again && live) {   // long rows are not kept waiting: two under way would not fit L2
+                back_row = r;
+                back_y = y;
+                back_xe = xe;
+                back_par = par;
+                back_buf = buf4;
+            }
+            if (back_row >= 0) back(back_row, back_y, back_xe, back_slot, back_par, back_buf);
+            if (!live) break;
+            back_row = again ? -1 : r;
+            back_y = y;
+            back_xe = xe;
+            back_slot = slot;
+            back_par = par;
+            back_buf = buf4;
+            par ^= 1;
+            buf4 = (buf4 + 1) & 3;
+        }
+        if (kTeach && listed >= 0) {
+            bar_sync(5, B);
+            relist();
+        }
+        if (exchanged) cluster_wait();
+        copy_wait<0>();
     }
-    copy_wait<0>();
-    if (OP != kLogprob && rank == 0) finish<OP>(a, sum, group, ngroups);
+    if (OP != kLogprob && rank == 0) finish<OP, B>(a, sum, group, ngroups);
 }
 
 // Second preference pass: every element from its row's statistics, one segment of a row
@@ -754,10 +915,11 @@ __global__ void __launch_bounds__(256) k_pref_grad(const LossArgs a, const int s
     const int tid = threadIdx.x;
     const int64_t item = int64_t(gridDim.x) - 1 - blockIdx.x, r = item / segs;
     const int seg = int(item - r * segs);
-    const Row<T> row(static_cast<const T*>(a.x) + r * a.ld, a.vocab);
+    const T* const x = static_cast<const T*>(a.x) + r * a.ld;
+    const Place<T> row(x, a.vocab, 0, 0);
     T* dx = static_cast<T*>(a.dx) + r * a.ldd;
-    const bool whole = same_phase(row.x, static_cast<const T*>(dx));
-    const T* body = row.x + row.head;
+    const bool whole = same_phase(x, static_cast<const T*>(dx));
+    const T* body = x + row.head;
     const int lo = seg * NV * 256, hi = min(row.body, lo + NV * 256);
     const RowStat st = a.stat[r];
     const int64_t y = a.target[r];
@@ -773,7 +935,7 @@ __global__ void __launch_bounds__(256) k_pref_grad(const LossArgs a, const int s
         const int v = lo + i * 256 + tid;
         if (v < hi) raw[i] = ld16(body + int64_t(v) * N);
     }
-    const float xe = edge ? to_f(row.x[row.edge_at(tid)]) : 0.0f;
+    const float xe = edge ? to_f(x[row.edge_at(tid)]) : 0.0f;
     const float c2 = a.it * kLog2e, kq = -st.w * st.rs;
     // the label's element: its thread stores it after its vector
     int mine = -1;
@@ -783,7 +945,7 @@ __global__ void __launch_bounds__(256) k_pref_grad(const LossArgs a, const int s
         const bool at_edge = j < row.head || v >= row.body;
         if (at_edge ? edge && row.edge_at(tid) == j : v >= lo && v < hi && (v - lo) % 256 == tid) {
             mine = j;
-            xy = to_f(row.x[j]);
+            xy = to_f(x[j]);
         }
     }
     const float u = st.m * c2;
@@ -838,7 +1000,7 @@ cudaError_t resident_groups(const void* kernel, const cudaLaunchConfig_t& cfg, c
     if (sh.clog > 0) {
         e = cudaOccupancyMaxActiveClusters(&groups, kernel, &cfg);
     } else {
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&groups, kernel, sh.threads, cfg.dynamicSmemBytes);
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&groups, kernel, int(cfg.blockDim.x), cfg.dynamicSmemBytes);
         groups *= sms;
     }
     if (e != cudaSuccess) return e;
@@ -848,15 +1010,13 @@ cudaError_t resident_groups(const void* kernel, const cudaLaunchConfig_t& cfg, c
     return cudaSuccess;
 }
 
-template <typename T, int OP, int B, bool DUAL>
+template <typename T, int OP, int B, int POW>
 cudaError_t row_launch(const LossArgs& a, const RowShape& sh, int sms, GroupCache& cache, cudaStream_t s) {
-    auto* kernel = k_row<T, OP, B, DUAL>;
-    const int t = int(1.0f / a.it + 0.5f);
-    const int pow = DUAL && t >= 2 && t <= 4 && a.it == 1.0f / float(t) ? t : 0;
+    auto* kernel = k_row<T, OP, B, POW>;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(1u << sh.clog);
-    cfg.blockDim = dim3(unsigned(B));
-    cfg.dynamicSmemBytes = size_t(16) * kStages * kTileVecs * B + (OP == kDistill ? sizeof(float) * 2 * 3 * size_t((a.k + 63) / 64 * 64) : 0);
+    cfg.blockDim = dim3(unsigned(B + 32));
+    cfg.dynamicSmemBytes = size_t(16) * kStages * kTileVecs * B + (OP == kDistill ? sizeof(float) * 4 * 3 * size_t((a.k + 63) / 64 * 64) : 0);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -870,27 +1030,29 @@ cudaError_t row_launch(const LossArgs& a, const RowShape& sh, int sms, GroupCach
     if (e != cudaSuccess) return e;
     if (groups > a.rows) groups = a.rows < 1 ? 1 : int(a.rows);
     cfg.gridDim.x = unsigned(groups) << sh.clog;
-    return cudaLaunchKernelEx(&cfg, kernel, a, int(sh.clog), pow);
+    return cudaLaunchKernelEx(&cfg, kernel, a, int(sh.clog));
 }
 
-template <typename T, int OP, bool DUAL>
+template <typename T, int OP, int POW = kSingle>
 cudaError_t rows_by_threads(const LossArgs& a, const RowShape& sh, int sms, GroupCache& cache, cudaStream_t s) {
-    if (sh.threads == 64) return row_launch<T, OP, 64, DUAL>(a, sh, sms, cache, s);
-    if (sh.threads == 128) return row_launch<T, OP, 128, DUAL>(a, sh, sms, cache, s);
-    return row_launch<T, OP, 256, DUAL>(a, sh, sms, cache, s);
+    if (sh.threads == 64) return row_launch<T, OP, 64, POW>(a, sh, sms, cache, s);
+    if (sh.threads == 128) return row_launch<T, OP, 128, POW>(a, sh, sms, cache, s);
+    return row_launch<T, OP, 256, POW>(a, sh, sms, cache, s);
 }
 
 template <typename T>
 cudaError_t rows_by_op(int op, const LossArgs& a, int sms, GroupCache& cache, cudaStream_t s) {
     const RowShape sh = shape_for<T>(a.rows, a.vocab, a.dx != nullptr, sms);
     switch (op) {
-        case kLogprob: return rows_by_threads<T, kLogprob, false>(a, sh, sms, cache, s);
-        case kPolicy: return rows_by_threads<T, kPolicy, false>(a, sh, sms, cache, s);
-        case kPrefStat: return rows_by_threads<T, kPrefStat, false>(a, sh, sms, cache, s);
+        case kLogprob: return rows_by_threads<T, kLogprob>(a, sh, sms, cache, s);
+        case kPolicy: return rows_by_threads<T, kPolicy>(a, sh, sms, cache, s);
+        case kPrefStat: return rows_by_threads<T, kPrefStat>(a, sh, sms, cache, s);
         default: break;
     }
-    if (a.k > 0 && a.ce_weight > 0.0f && a.it != 1.0f) return rows_by_threads<T, kDistill, true>(a, sh, sms, cache, s);
-    return rows_by_threads<T, kDistill, false>(a, sh, sms, cache, s);
+    if (a.k == 0 || a.ce_weight == 0.0f || a.it == 1.0f) return rows_by_threads<T, kDistill>(a, sh, sms, cache, s);
+    if (a.it == 0.5f) return rows_by_threads<T, kDistill, 2>(a, sh, sms, cache, s);
+    if (a.it == 0.25f) return rows_by_threads<T, kDistill, 4>(a, sh, sms, cache, s);
+    return rows_by_threads<T, kDistill, 0>(a, sh, sms, cache, s);
 }
 
 template <typename T>

@@ -18,15 +18,18 @@ until it has run.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
-from . import TL_BF16, TL_F16, TL_F32, TL_OK, TLError, _stream, load_library
+from . import TL_BF16, TL_F16, TL_F32, TL_OK, TLError, load_library
+from . import _stream as _any_stream
 
 LOSS_EXPORTED = ("tl_loss_create", "tl_loss_destroy", "tl_token_logprob", "tl_policy_loss", "tl_preference_loss",
                  "tl_distill_loss", "tl_loss_launch_count", "tl_loss_last_error")
 
 _DTYPES = {torch.float32: TL_F32, torch.bfloat16: TL_BF16, torch.float16: TL_F16}
+_ID_BYTES = {torch.int32: 4, torch.int64: 8}
 _vp, _i64, _i32, _f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
 
 
@@ -59,6 +62,11 @@ class tl_distill_args(ctypes.Structure):
 
 
 _lib = None
+_raw_stream = torch._C._cuda_getCurrentRawStream   # current_stream() without its Stream object (3 us a call)
+
+
+def _stream(lctx, stream):
+    return _raw_stream(lctx.device) if stream is None else _any_stream(stream)
 
 
 def _load():
@@ -82,16 +90,30 @@ def _load():
 
 
 class LossContext:
-    """Owns one tl_loss_ctx (its scratch lives on the device that was current at creation)."""
+    """Owns one tl_loss_ctx (its scratch lives on the device that was current at creation)
+    and the argument structures that its calls fill in (a context is used by one thread)."""
 
     def __init__(self, handle, device: int):
         self.handle = handle
         self.device = device
+        self._x, self._out = tl_logits(), tl_loss_out()
+        self._args = {c: c() for c in (tl_policy_args, tl_preference_args, tl_distill_args)}
+        # one pack per call and structure: assigning the fields one by one costs more than
+        # the launch
+        self._refs = {c: ctypes.byref(v) for c, v in self._args.items()}
+        self._x_ref, self._out_ref = ctypes.byref(self._x), ctypes.byref(self._out)
 
     def __del__(self):
         if getattr(self, "handle", None) and _lib is not None:
             _lib.tl_loss_destroy(self.handle)
             self.handle = None
+
+
+# The structures' layouts for struct.pack_into (native sizes and alignment).
+_PACK_LOGITS = struct.Struct("@Pqqqif")
+_PACK_OUT = struct.Struct("@qPPqPPP")
+_PACK = {tl_policy_args: struct.Struct("@PPPPfff"), tl_preference_args: struct.Struct("@PPqPffP"),
+         tl_distill_args: struct.Struct("@PPPqiiiff")}
 
 
 def _check(lctx, fn: str, rc: int):
@@ -104,7 +126,7 @@ def tl_loss_create(max_rows: int, max_pairs: int = 0, stream=None) -> LossContex
     """A context for calls of at most max_rows rows and max_pairs preference pairs."""
     lib = _load()
     h = _vp()
-    rc = lib.tl_loss_create(ctypes.byref(h), int(max_rows), int(max_pairs), _stream(stream))
+    rc = lib.tl_loss_create(ctypes.byref(h), int(max_rows), int(max_pairs), _any_stream(stream))
     if rc != TL_OK:
         raise TLError("tl_loss_create", rc, lib.tl_status_string(rc).decode())
     return LossContext(h, torch.cuda.current_device())
@@ -122,59 +144,67 @@ def tl_loss_launch_count(lctx: LossContext) -> int:
     return int(_load().tl_loss_launch_count(lctx.handle))
 
 
-def _vec(lctx, t, dtype, n: int, name: str):
-    """Address of a contiguous device vector of n elements, None for None."""
+_F32, _I64 = torch.float32, torch.int64
+
+
+def _vec(lctx, t, dtype, n: int, name: str) -> int:
+    """Address of a contiguous device vector of n elements, 0 for None."""
     if t is None:
-        return None
-    if t.dtype != dtype or t.numel() != n or not t.is_contiguous() or t.get_device() != lctx.device:
+        return 0
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or t.get_device() != lctx.device:
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements on cuda:{lctx.device}")
     return t.data_ptr()
 
 
 def _matrix(lctx, t, name: str):
-    """(address, row stride) of a 2-D device tensor with contiguous rows."""
+    """(address, rows, columns, row stride) of a 2-D device tensor with contiguous rows."""
     if t.dim() != 2 or t.get_device() != lctx.device:
         raise ValueError(f"{name} must be a 2-D tensor on cuda:{lctx.device}")
     rows, cols = t.shape
     ld, step = t.stride()
     if step != 1 and cols > 1:
         raise ValueError(f"the rows of {name} must be contiguous")
-    return t.data_ptr(), ld if rows > 1 else max(ld, cols)
+    return t.data_ptr(), rows, cols, ld if rows > 1 or ld > cols else cols
 
 
-def _logits(lctx, x, temperature) -> tl_logits:
-    addr, ld = _matrix(lctx, x, "logits")
+def _logits(lctx, x, temperature) -> int:
+    """Fills in the context's tl_logits; the number of rows."""
+    addr, rows, vocab, ld = _matrix(lctx, x, "logits")
     dt = _DTYPES.get(x.dtype)
     if dt is None:
         raise ValueError("logits must be float32, bfloat16 or float16")
-    return tl_logits(addr, x.shape[0], x.shape[1], ld, dt, float(temperature))
+    _PACK_LOGITS.pack_into(lctx._x, 0, addr, rows, vocab, ld, dt, temperature)
+    return rows
 
 
-def _seed(lctx, seed):
-    """A device address (tl_scale_ptr), a float32 CUDA tensor of one element, or None."""
-    if seed is None or isinstance(seed, int):
-        return seed
-    return _vec(lctx, seed, torch.float32, 1, "seed")
-
-
-def _out(lctx, x, n, result, seed, dlogits, logp, loss, losses) -> tl_loss_out:
-    d, ldd = None, 0
+def _out(lctx, x, n, result, seed, dlogits, logp, rows, loss, losses) -> None:
+    """Fills in the context's tl_loss_out.  seed: a device address (tl_scale_ptr), a float32
+    CUDA tensor of one element, or None."""
+    d = ldd = 0
     if dlogits is not None:
-        d, ldd = _matrix(lctx, dlogits, "dlogits")
-        if dlogits.dtype != x.dtype or dlogits.shape != x.shape:
+        d, _, _, ldd = _matrix(lctx, dlogits, "dlogits")
+        if dlogits.dtype is not x.dtype or dlogits.shape != x.shape:
             raise ValueError("dlogits must have the shape and dtype of the logits")
-    f = torch.float32
-    return tl_loss_out(int(n), _seed(lctx, seed), d, ldd, _vec(lctx, logp, f, x.shape[0], "logp"),
-                       _vec(lctx, loss, f, losses, "the loss output"), _vec(lctx, result, f, 4, "result"))
+    if not isinstance(seed, int):
+        seed = _vec(lctx, seed, _F32, 1, "seed")
+    _PACK_OUT.pack_into(lctx._out, 0, n, seed, d, ldd, _vec(lctx, logp, _F32, rows, "logp"),
+                        _vec(lctx, loss, _F32, losses, "the loss output"), _vec(lctx, result, _F32, 4, "result"))
+
+
+def _call(lctx, name: str, cls, stream, *fields) -> None:
+    _PACK[cls].pack_into(lctx._args[cls], 0, *fields)
+    rc = getattr(_load(), name)(lctx.handle, lctx._x_ref, lctx._refs[cls], lctx._out_ref, _stream(lctx, stream))
+    if rc != TL_OK:
+        _check(lctx, name, rc)
 
 
 def tl_token_logprob(lctx: LossContext, logits, targets, logp, temperature: float = 1.0, stream=None) -> None:
     """logp[t] = log softmax(logits[t] / temperature)[targets[t]]; 0 where targets[t] < 0."""
-    lib = _load()
-    x = _logits(lctx, logits, temperature)
-    _check(lctx, "tl_token_logprob", lib.tl_token_logprob(
-        lctx.handle, ctypes.byref(x), _vec(lctx, targets, torch.int64, x.rows, "targets"),
-        _vec(lctx, logp, torch.float32, x.rows, "logp"), _stream(stream)))
+    T = _logits(lctx, logits, temperature)
+    rc = _load().tl_token_logprob(lctx.handle, lctx._x_ref, _vec(lctx, targets, _I64, T, "targets"),
+                                  _vec(lctx, logp, _F32, T, "logp"), _stream(lctx, stream))
+    if rc != TL_OK:
+        _check(lctx, "tl_token_logprob", rc)
 
 
 def tl_policy_loss(lctx: LossContext, logits, targets, old_logp, advantages, n: int, result, ref_logp=None,
@@ -182,15 +212,11 @@ def tl_policy_loss(lctx: LossContext, logits, targets, old_logp, advantages, n: 
                    seed=None, dlogits=None, logp=None, row_loss=None, stream=None) -> None:
     """Clipped policy objective with a KL penalty, mean over n valid targets; its gradient
     into dlogits (which may be the logits themselves)."""
-    lib = _load()
-    x = _logits(lctx, logits, temperature)
-    T, f = x.rows, torch.float32
-    args = tl_policy_args(_vec(lctx, targets, torch.int64, T, "targets"), _vec(lctx, old_logp, f, T, "old_logp"),
-                          _vec(lctx, ref_logp, f, T, "ref_logp"), _vec(lctx, advantages, f, T, "advantages"),
-                          float(clip_low), float(clip_high), float(kl_weight))
-    out = _out(lctx, logits, n, result, seed, dlogits, logp, row_loss, T)
-    _check(lctx, "tl_policy_loss", lib.tl_policy_loss(lctx.handle, ctypes.byref(x), ctypes.byref(args),
-                                                      ctypes.byref(out), _stream(stream)))
+    T = _logits(lctx, logits, temperature)
+    _out(lctx, logits, n, result, seed, dlogits, logp, T, row_loss, T)
+    _call(lctx, "tl_policy_loss", tl_policy_args, stream, _vec(lctx, targets, _I64, T, "targets"),
+          _vec(lctx, old_logp, _F32, T, "old_logp"), _vec(lctx, ref_logp, _F32, T, "ref_logp"),
+          _vec(lctx, advantages, _F32, T, "advantages"), clip_low, clip_high, kl_weight)
 
 
 def tl_preference_loss(lctx: LossContext, logits, targets, seq, n: int, result, ref_logp=None, beta: float = 0.1,
@@ -198,19 +224,15 @@ def tl_preference_loss(lctx: LossContext, logits, targets, seq, n: int, result, 
                        pair_loss=None, reward=None, stream=None) -> None:
     """Paired preference objective, mean over n pairs.  seq: int64 CUDA tensor of
     2 * pairs + 1 row offsets (chosen, rejected, chosen, ...)."""
-    lib = _load()
-    x = _logits(lctx, logits, temperature)
-    T, f = x.rows, torch.float32
-    if seq.numel() % 2 != 1:
+    T = _logits(lctx, logits, temperature)
+    bounds = seq.numel()
+    if bounds % 2 != 1:
         raise ValueError("seq must hold 2 * pairs + 1 offsets")
-    pairs = seq.numel() // 2
-    args = tl_preference_args(_vec(lctx, targets, torch.int64, T, "targets"),
-                              _vec(lctx, seq, torch.int64, 2 * pairs + 1, "seq"), pairs,
-                              _vec(lctx, ref_logp, f, T, "ref_logp"), float(beta), float(label_smoothing),
-                              _vec(lctx, reward, f, 2 * pairs, "reward"))
-    out = _out(lctx, logits, n, result, seed, dlogits, logp, pair_loss, pairs)
-    _check(lctx, "tl_preference_loss", lib.tl_preference_loss(lctx.handle, ctypes.byref(x), ctypes.byref(args),
-                                                              ctypes.byref(out), _stream(stream)))
+    pairs = bounds // 2
+    _out(lctx, logits, n, result, seed, dlogits, logp, T, pair_loss, pairs)
+    _call(lctx, "tl_preference_loss", tl_preference_args, stream, _vec(lctx, targets, _I64, T, "targets"),
+          _vec(lctx, seq, _I64, bounds, "seq"), pairs, _vec(lctx, ref_logp, _F32, T, "ref_logp"), beta,
+          label_smoothing, _vec(lctx, reward, _F32, 2 * pairs, "reward"))
 
 
 def tl_distill_loss(lctx: LossContext, logits, teacher_logits, teacher_ids, n: int, result, targets=None,
@@ -218,21 +240,15 @@ def tl_distill_loss(lctx: LossContext, logits, teacher_logits, teacher_ids, n: i
                     row_loss=None, stream=None) -> None:
     """Distillation from a teacher's top-k logits ([rows, k], ids int32 or int64), mean over
     n valid rows.  teacher_logits = teacher_ids = None is the cross-entropy alone."""
-    lib = _load()
-    x = _logits(lctx, logits, temperature)
-    T = x.rows
-    t_addr = i_addr = None
-    ldt = k = tdt = id_bytes = 0
+    T = _logits(lctx, logits, temperature)
+    t_addr = i_addr = ldt = k = tdt = id_bytes = 0
     if teacher_logits is not None:
-        t_addr, ldt = _matrix(lctx, teacher_logits, "teacher_logits")
-        i_addr, ldi = _matrix(lctx, teacher_ids, "teacher_ids")
-        k = teacher_logits.shape[1]
+        t_addr, t_rows, k, ldt = _matrix(lctx, teacher_logits, "teacher_logits")
+        i_addr, i_rows, i_cols, ldi = _matrix(lctx, teacher_ids, "teacher_ids")
         tdt = _DTYPES.get(teacher_logits.dtype, -1)
-        id_bytes = {torch.int32: 4, torch.int64: 8}.get(teacher_ids.dtype, -1)
-        if teacher_logits.shape[0] != T or teacher_ids.shape != teacher_logits.shape or ldt != ldi:
+        id_bytes = _ID_BYTES.get(teacher_ids.dtype, -1)
+        if t_rows != T or i_rows != T or i_cols != k or ldt != ldi:
             raise ValueError("teacher_logits and teacher_ids must be [rows, k] with one row stride")
-    args = tl_distill_args(_vec(lctx, targets, torch.int64, T, "targets"), t_addr, i_addr, ldt, k, tdt, id_bytes,
-                           float(kd_weight), float(ce_weight))
-    out = _out(lctx, logits, n, result, seed, dlogits, None, row_loss, T)
-    _check(lctx, "tl_distill_loss", lib.tl_distill_loss(lctx.handle, ctypes.byref(x), ctypes.byref(args),
-                                                        ctypes.byref(out), _stream(stream)))
+    _out(lctx, logits, n, result, seed, dlogits, None, T, row_loss, T)
+    _call(lctx, "tl_distill_loss", tl_distill_args, stream, _vec(lctx, targets, _I64, T, "targets"), t_addr, i_addr,
+          ldt, k, tdt, id_bytes, kd_weight, ce_weight)
