@@ -140,27 +140,36 @@ __device__ void finish(const LossArgs& a, const LossSums& sum, int group, int ng
     if (tid == 0) *a.ticket = 0;   // ready for the next call
 }
 
-// The pairs, by the last CTA of the first preference pass: a warp sums the
-// log-ratios of one pair's two sequences (lanes strided, fp64), forms the pair's
-// loss and its derivative, and writes the gradient factor of each of its rows.
+// The pairs, by the last CTA of the first preference pass: a warp sums the log-ratios of
+// one pair's two sequences (lanes strided, eight loads under way, fp64), forms the pair's loss
+// and its derivative, and writes the gradient factor of each of its rows.
 template <int B> __device__ void pair_stage(const LossArgs& a) {
-    constexpr int nw = B / 32;
+    constexpr int nw = B / 32, U = 8;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const float step = (a.seed ? *a.seed : 1.0f) * a.inv_n * a.it;
     // rows outside every sequence keep w = 0, written by the row pass
     double loss = 0.0, margin = 0.0, won = 0.0, count = 0.0;
     for (int64_t p = warp; p < a.pairs; p += nw) {
         int64_t at[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) at[i] = a.seq[2 * p + i];
         int64_t prev = 0;
+#pragma unroll
         for (int i = 0; i < 3; ++i) {
-            int64_t v = a.seq[2 * p + i];
-            v = v < prev ? prev : v;
-            at[i] = prev = v > a.rows ? a.rows : v;
+            at[i] = at[i] < prev ? prev : at[i];
+            at[i] = prev = at[i] > a.rows ? a.rows : at[i];
         }
         double s[2];
+#pragma unroll
         for (int i = 0; i < 2; ++i) {
             double v = 0.0;
-            for (int64_t r = at[i] + lane; r < at[i + 1]; r += 32) v += double(__ldcg(&a.stat[r].ratio));
+            for (int64_t r = at[i] + lane; r < at[i + 1]; r += 32 * U) {
+                float q[U];
+#pragma unroll
+                for (int j = 0; j < U; ++j) q[j] = r + 32 * j < at[i + 1] ? __ldcg(&a.stat[r + 32 * j].ratio) : 0.0f;
+#pragma unroll
+                for (int j = 0; j < U; ++j) v += double(q[j]);
+            }
             s[i] = warp_sum(v);
         }
         const float h = float(double(a.beta) * (s[0] - s[1]));   // beta * h
@@ -170,12 +179,9 @@ template <int B> __device__ void pair_stage(const LossArgs& a) {
         const float big = 1.0f / (1.0f + t), small = t / (1.0f + t);
         const float down = h > 0.0f ? small : h <= 0.0f ? big : h, up = h > 0.0f ? big : h <= 0.0f ? small : h;
         const float l = -(1.0f - a.smooth) * log_up - (a.smooth > 0.0f ? a.smooth * log_down : 0.0f);
-        const float dh = -a.beta * ((1.0f - a.smooth) * down - a.smooth * up);
-        for (int i = 0; i < 2; ++i) {
-            const float w = (i == 0 ? dh : -dh) * step;
-            for (int64_t r = at[i] + lane; r < at[i + 1]; r += 32)
-                if (a.target[r] >= 0) a.stat[r].w = w;
-        }
+        const float w = -a.beta * ((1.0f - a.smooth) * down - a.smooth * up) * step;
+        // all rows of the pair; those that are ignored are zeros whatever their factor
+        for (int64_t r = at[0] + lane; r < at[2]; r += 32) a.stat[r].w = r < at[1] ? w : -w;
         if (lane == 0) {
             if (a.loss) a.loss[p] = l;
             if (a.reward) {
@@ -329,7 +335,7 @@ __device__ __forceinline__ bool same_phase(const T* x, const T* dx) {
 // The row kernel
 // ---------------------------------------------------------------------------
 
-constexpr int kMaxCluster = 8;
+constexpr int kMaxClusterLog = 3, kMaxCluster = 1 << kMaxClusterLog;
 
 __device__ __forceinline__ uint32_t cluster_rank() { uint32_t r; asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r)); return r; }
 // The cluster's barrier in halves.  Only the statistics warps write into other CTAs, so
@@ -390,11 +396,13 @@ constexpr int kMaxRingBytes = 220 * 1024;   // dynamic shared memory: tiles and 
 // A tile is kTileVecs vectors per thread, kStages of them are in shared memory.
 constexpr int kTileVecs = 8, kStages = 3;
 constexpr int kSingle = -1;   // POW of the kernels with one sum per row
-constexpr int64_t kRowsInL2 = 48 << 20;
+constexpr int64_t kRowsInL2 = 48 << 20, kTwoRowsInL2 = 64 << 20;
 
-// How a launch lays its rows out: threads per CTA, and CTAs per row (2^clog).
+// How a launch lays its rows out: threads per CTA, CTAs per row (2^clog), and whether a
+// streamed row's pass B waits for the next row's pass A (two rows under way per group).
 struct RowShape {
     int threads, clog;
+    bool two;
 };
 
 // A group of 2^clog CTAs takes one row at a time, each CTA a contiguous share of the row's
@@ -414,7 +422,7 @@ struct RowShape {
 // read once; longer ones are streamed a second time, out of L2 (see shape_for).
 // POW: distillation with both terms at temperatures that differ, two sums per row (DUAL).
 template <typename T, int OP, int B, int POW>
-__global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row(const LossArgs a, const int clog) {
+__global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row(const LossArgs a, const int clog, const bool two) {
     constexpr int N = Vec<T>::N, U = 4, tile = B * kTileVecs, ST = kStages, nw = B / 32;
     constexpr bool DUAL = POW != kSingle;
     constexpr bool kTeach = OP == kDistill;
@@ -430,6 +438,8 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cluster = 1 << clog, rank = cluster > 1 ? int(cluster_rank()) : 0;
     const int group = int(blockIdx.x) >> clog, ngroups = int(gridDim.x) >> clog;
+    float* const teach = reinterpret_cast<float*>(ring + ST * tile);
+    const int kpad = (a.k + 3) & ~3;
     const float c2 = a.it * kLog2e;
     const bool kd_on = kTeach && a.k > 0, ce_on = kTeach && a.ce_weight > 0.0f;
     const bool grad = kGrad && a.dx != nullptr;
@@ -437,6 +447,11 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
     LossSums sum;
     int par = 0, buf4 = 0;   // of the row: which of two, which of four
     int64_t ynext = a.target && group < a.rows ? a.target[group] : 0;
+    // The dense gradient of one logit x: its exponentials times their factors.
+    auto dense_value = [&](float x, float Mb, float kq, float cq) {
+        const float e = power(x, Mb, c2);
+        return DUAL ? __fmaf_rn(power1<POW>(e, x, Mb, c2), cq, e * kq) : e * kq;
+    };
     // The label of row r, that of the group's next one under way.
     auto label = [&](int64_t r) {
         const int64_t y = ynext;
@@ -503,13 +518,16 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
             const float gap = big(M) ? (xy - M) * c2 : __fmaf_rn(xy, c2, -(M * c2));   // log2 of the label's exponential
             const float lp = (gap - lg) * kLn2 + bad;
             if (OP == kLogprob || OP == kPrefStat) {
+                bar_arrive(3 + par, B + 32);   // nothing for pass B
                 if (out && a.logp) a.logp[r] = lp;
                 if (OP == kPrefStat && out) a.stat[r] = {M + bad, 1.0f / S, 0.0f, lp - refl};
             } else if (OP == kPolicy) {
                 float loss, sur, kl;
                 const float w = policy_row(a, lp, old, adv, refl, loss, sur, kl) * step * a.it;
                 // the label's element: w (1 - q)
-                if (lane == 0) fac[buf4][0] = make_float4(M + bad, -w / S, __fmaf_rn(ex2(gap), -w / S, w), 0.0f);
+                const float kq = -w / S;
+                if (lane == 0) fac[buf4][0] = make_float4(M + bad, kq, 0.0f, __fmaf_rn(ex2(gap), kq, w));
+                bar_arrive(3 + par, B + 32);
                 if (out) {
                     if (a.logp) a.logp[r] = lp;
                     if (a.loss) a.loss[r] = loss;
@@ -522,11 +540,21 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
                 // (e_i = exp(t_i - tm) times wp; 0: none)
                 const float wk = row_kd ? a.kd_weight * step / a.it : 0.0f, wc = ce_on ? a.ce_weight * step : 0.0f;
                 const float kq = wk / S + (DUAL ? 0.0f : wc / S) + bad;
-                if (lane == 0) {
-                    fac[buf4][0] = make_float4(M + bad, row_kd || (!DUAL && ce_on) || bad != 0.0f ? kq : 0.0f,
-                                              DUAL ? wc / S1 : 0.0f, tm);
-                    fac[buf4][1] = make_float4(row_kd ? wk / ts : 0.0f, bad, xy, wc);
+                const float kq0 = row_kd || (!DUAL && ce_on) || bad != 0.0f ? kq : 0.0f, cq = DUAL ? wc / S1 : 0.0f;
+                const float wp = row_kd ? wk / ts : 0.0f;
+                // the label's element: the teacher may list it too
+                float at_label = 0.0f;
+                if (ce_on && grad) {
+                    const float* const tb = teach + buf4 * 3 * kpad;
+                    for (int i = lane; i < (wp != 0.0f ? a.k : 0); i += 32)
+                        if (__float_as_int(tb[i]) == int(y)) at_label = __fmaf_rn(wp, ex2((tb[kpad + i] - tm) * kLog2e), at_label);
+                    at_label = dense_value(xy, M + bad, kq0, cq) - (warp_sum(at_label) + wc);
                 }
+                if (lane == 0) {
+                    fac[buf4][0] = make_float4(M + bad, kq0, cq, at_label);
+                    fac[buf4][1] = make_float4(wp, tm, 0.0f, 0.0f);
+                }
+                bar_arrive(3 + par, B + 32);
                 const float lz = big(M) ? __fmaf_rn(M, a.it, lg * kLn2) : (M * c2 + lg) * kLn2;   // log sum exp z
                 const float kd = row_kd ? (td / ts - tm - logf(ts) + lz) / (a.it * a.it) + bad : bad;
                 float log_sum1 = 0.0f;   // log sum exp x
@@ -538,15 +566,12 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
                     sum.loss += loss; sum.first += kd; sum.second += ce; sum.count += 1.0;
                 }
             }
-            bar_arrive(3 + par, B + 32);
             par ^= 1;
             buf4 = (buf4 + 1) & 3;
         }
     } else {
         // ------------------------------------------------------------ the element warps
         const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + 16u * uint32_t(tid);
-        float* const teach = reinterpret_cast<float*>(ring + ST * tile);
-        const int kpad = (a.k + 3) & ~3;
         auto row_at = [&](int64_t r) { return static_cast<const T*>(a.x) + r * a.ld; };
         // all rows lie alike where their stride is a multiple of 16 bytes
         const bool alike = (a.ld * int(sizeof(T))) % 16 == 0;
@@ -558,17 +583,17 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
         const bool again = grad && !kept;
         // The copies run ahead in the order of their use.
         int64_t fr = group - ngroups, fynext = a.target && group < a.rows ? a.target[group] : 0;
-        const T *fat = nullptr, *flast = nullptr;   // this thread's next vector, and where row fr's start
-        int fleft = 0, nlast = 0;                   // vectors left of the pass, and of the row's share
-        bool fback = false;                         // the pass is B
+        const T *fat = nullptr, *flast = nullptr, *fowed = nullptr;   // this thread's next vector; where the last pass A
+        int fleft = 0, nlast = 0, nowed = 0;                          // and the owed pass B start, and how long they are
         auto segment = [&]() {
-            if (again && nlast > 0 && !fback) {   // pass B of the row whose pass A is asked for
-                fat = flast;
-                fleft = nlast;
-                fback = true;
+            if (nowed > 0) {   // a pass B is owed
+                fat = fowed;
+                fleft = nowed;
+                nowed = 0;
                 return;
             }
-            fback = false;
+            const T* const before = flast;
+            const int nbefore = nlast;
             nlast = 0;
             while (nlast <= 0) {   // the next row that is not ignored and of which this CTA has a share
                 fr += ngroups;
@@ -583,6 +608,18 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
             }
             fat = flast;
             fleft = nlast;
+            if (again && !two) {   // its own pass B is next
+                fowed = flast;
+                nowed = nlast;
+            } else if (again) {    // that of the row before is next, or now where no row is left
+                fowed = before;
+                nowed = nbefore;
+                if (nlast <= 0 && nowed > 0) {
+                    fat = fowed;
+                    fleft = nowed;
+                    nowed = 0;
+                }
+            }
         };
         auto fetch = [&](int slot) {
             if (fleft <= 0) segment();
@@ -621,44 +658,44 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
             }
         };
 
-        // The listed elements of a row (the teacher's and the label), written again over the
-        // dense gradient once every warp has stored its part of that: an id's first entry
-        // takes the weights of all that are equal to it.
+        // The teacher's elements of a row, written again over the dense gradient once every warp
+        // has stored its part of that: an id's first entry takes the weights of all that are
+        // equal to it.  Four lanes to an entry, which look for equal ids.
         int64_t listed = -1, listed_y = 0;
         int listed_buf = 0;
         auto relist = [&]() {
             const float4 fc = fac[listed_buf][0], f1 = fac[listed_buf][1];
-            const float Mb = fc.x, kq = fc.y, cq = fc.z, tm = fc.w, wp = f1.x, bad = f1.y;
-            const int n = wp != 0.0f ? a.k : 0, entries = n + (ce_on && bad == 0.0f ? 1 : 0);
+            const float Mb = fc.x, kq = fc.y, cq = fc.z, tm = f1.y, wp = f1.x;
+            const int n = wp != 0.0f ? a.k : 0;
             const float* const tb = teach + listed_buf * 3 * kpad;
             const int* const ids = reinterpret_cast<const int*>(tb);
             const Place<T> pl = place_of(row_at(listed));
             T* const dx = static_cast<T*>(a.dx) + listed * a.ldd;
-            for (int i = tid; i < entries; i += B) {
-                const int id = i < n ? ids[i] : int(listed_y);
-                bool at_edge;
-                int v;
-                if (id < 0 || !pl.owns(id, rank, at_edge, v)) continue;
+            for (int base = warp * 8; base < n; base += B / 4) {
+                const int i = base + (lane >> 2), id = i < n ? ids[i] : -1;
                 int same = 0;   // entries of this id
-#pragma unroll 4
-                for (int j = 0; j < n; j += 4) {   // ids are padded with -1 to a multiple of 4
+                for (int j = 4 * (lane & 3); j < n; j += 16) {   // ids are padded with -1 to a multiple of 4
                     const int4 q = *reinterpret_cast<const int4*>(ids + j);
                     same += int(q.x == id) + int(q.y == id) + int(q.z == id) + int(q.w == id);
                 }
-                float w = ce_on && id == int(listed_y) ? f1.w : 0.0f;
-                if (same == 1 && i < n) {
-                    w = __fmaf_rn(wp, ex2((tb[kpad + i] - tm) * kLog2e), w);
+                same += __shfl_xor_sync(~0u, same, 1);
+                same += __shfl_xor_sync(~0u, same, 2);
+                bool at_edge;
+                int v;
+                // the label's element has its value already
+                if ((lane & 3) != 0 || id < 0 || (ce_on && id == int(listed_y)) || !pl.owns(id, rank, at_edge, v)) continue;
+                float w = 0.0f;
+                bool lead = true;
+                if (same == 1) {
+                    w = wp * ex2((tb[kpad + i] - tm) * kLog2e);
                 } else {
-                    bool lead = true;
                     for (int j = 0; j < n; ++j) {
                         if (ids[j] != id) continue;
                         lead = lead && j >= i;
                         w = __fmaf_rn(wp, ex2((tb[kpad + j] - tm) * kLog2e), w);
                     }
-                    if (!lead) continue;
                 }
-                const float x = i < n ? tb[2 * kpad + i] : f1.z, e = power(x, Mb, c2);
-                dx[id] = from_f<T>((DUAL ? __fmaf_rn(power1<POW>(e, x, Mb, c2), cq, e * kq) : e * kq) - w);
+                if (lead) dx[id] = from_f<T>(dense_value(tb[2 * kpad + i], Mb, kq, cq) - w);
             }
             listed = -1;
         };
@@ -677,10 +714,7 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
             const float4 fc = fac[buffer][0];
             const float Mb = fc.x, kq = fc.y, cq = OP == kDistill ? fc.z : 0.0f;
             const float u = Mb * c2, v1 = DUAL ? untempered_ref<POW>(Mb, u) : 0.0f;
-            auto dense = [&](float x) {
-                const float e = power(x, Mb, c2);
-                return DUAL ? __fmaf_rn(power1<POW>(e, x, Mb, c2), cq, e * kq) : e * kq;
-            };
+            auto dense = [&](float x) { return dense_value(x, Mb, kq, cq); };
             for (int done = 0; done < hi - lo; done += tile) {
                 if (!kept) take_tile();
                 const uint4* const buf = ring + (kept ? kept_slot : slot) * tile + tid;
@@ -717,13 +751,13 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
             }
             if (kept && hi > lo) fetch(kept_slot);
             if (edge) dx[pl.edge_at(tid)] = from_f<T>(dense(xe));
-            if (OP == kPolicy && y < a.vocab) {
+            if ((OP == kPolicy || ce_on) && y < a.vocab) {
                 // the label's element again, by the thread that stored it
                 bool at_edge;
                 int v;
-                if (pl.owns(int(y), rank, at_edge, v) && (at_edge ? v : (v - lo) & (B - 1)) == tid) dx[y] = from_f<T>(fc.z);
+                if (pl.owns(int(y), rank, at_edge, v) && (at_edge ? v : (v - lo) & (B - 1)) == tid) dx[y] = from_f<T>(fc.w);
             }
-            if (kTeach) {
+            if (kTeach && kd_on) {
                 listed = r;
                 listed_y = y;
                 listed_buf = buffer;
@@ -879,7 +913,7 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
                 }
                 bar_arrive(1 + par, B + 32);
             }
-            if (again && live) {   // long rows are not kept waiting: two under way would not fit L2
+            if (again && !two && live) {   // not kept waiting
                 back_row = r;
                 back_y = y;
                 back_xe = xe;
@@ -888,7 +922,7 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
             }
             if (back_row >= 0) back(back_row, back_y, back_xe, back_slot, back_par, back_buf);
             if (!live) break;
-            back_row = again ? -1 : r;
+            back_row = again && !two ? -1 : r;
             back_y = y;
             back_xe = xe;
             back_slot = slot;
@@ -971,15 +1005,17 @@ __global__ void __launch_bounds__(256) k_pref_grad(const LossArgs a, const int s
 template <typename T>
 RowShape shape_for(int64_t rows, int vocab, bool grad, int sms) {
     const int vecs = (vocab + Vec<T>::N - 1) / Vec<T>::N;
-    RowShape s{64, 0};
+    RowShape s{64, 0, true};
     while (s.threads < 256 && s.threads * 8 < vecs) s.threads *= 2;
-    // long rows read twice: more CTAs to a row keep the rows under way (two CTAs per SM) in L2
-    // for the second read.  4,096 x 128,256 bf16: 339 us with 2 CTAs per row (39 MB under
-    // way), 429 with 1 (78 MB), 390 with 4
-    if (grad && s.threads == 256)
-        while ((1 << s.clog) < kMaxCluster && (int64_t(2) * sms * vocab * int(sizeof(T))) >> s.clog > kRowsInL2) s.clog += 1;
+    // Long rows are read twice, the second time out of L2 if what is under way (two CTAs per
+    // SM) fits it: more CTAs to a row where it would not, and then one row at a time.
+    const int64_t under_way = int64_t(2) * sms * vocab * int(sizeof(T));
+    if (grad && s.threads == 256) {
+        while (s.clog < kMaxClusterLog && under_way >> s.clog > kRowsInL2) s.clog += 1;
+        s.two = 2 * (under_way >> s.clog) <= kTwoRowsInL2;
+    }
     // few rows: spread each over more CTAs while the GPU has idle SMs and a thread more than one vector
-    while ((1 << s.clog) < kMaxCluster && rows << (s.clog + 1) <= sms && s.threads << s.clog < vecs) s.clog += 1;
+    while (s.clog < kMaxClusterLog && rows << (s.clog + 1) <= sms && s.threads << s.clog < vecs) s.clog += 1;
     return s;
 }
 
@@ -1030,7 +1066,7 @@ cudaError_t row_launch(const LossArgs& a, const RowShape& sh, int sms, GroupCach
     if (e != cudaSuccess) return e;
     if (groups > a.rows) groups = a.rows < 1 ? 1 : int(a.rows);
     cfg.gridDim.x = unsigned(groups) << sh.clog;
-    return cudaLaunchKernelEx(&cfg, kernel, a, int(sh.clog));
+    return cudaLaunchKernelEx(&cfg, kernel, a, int(sh.clog), sh.two);
 }
 
 template <typename T, int OP, int POW = kSingle>
