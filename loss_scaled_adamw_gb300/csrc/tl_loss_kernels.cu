@@ -434,7 +434,9 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
     // out, its predecessor is in pass B and the one before that has its listed elements
     // written; a warp may be a row ahead of another.
     __shared__ float4 fac[4][2];                    // gradient factors
-    extern __shared__ uint4 ring[];                 // [ST][tile] vectors; then [4][3][kpad] of id, t / tau, x
+    // [ST][tile] vectors; then [4][3][kpad] of id, t / tau, x.  A copy of a warp into memory off a
+    // 128-byte boundary takes twice the requests: policy 341 or 408 us by what else was declared.
+    extern __shared__ __align__(128) uint4 ring[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cluster = 1 << clog, rank = cluster > 1 ? int(cluster_rank()) : 0;
     const int group = int(blockIdx.x) >> clog, ngroups = int(gridDim.x) >> clog;
@@ -1078,7 +1080,8 @@ cudaError_t rows_by_threads(const LossArgs& a, const RowShape& sh, int sms, Grou
 
 template <typename T>
 cudaError_t rows_by_op(int op, const LossArgs& a, int sms, GroupCache& cache, cudaStream_t s) {
-    const RowShape sh = shape_for<T>(a.rows, a.vocab, a.dx != nullptr, sms);
+    const bool grad = a.dx != nullptr && (op == kPolicy || op == kDistill);
+    const RowShape sh = shape_for<T>(a.rows, a.vocab, grad, sms);
     switch (op) {
         case kLogprob: return rows_by_threads<T, kLogprob>(a, sh, sms, cache, s);
         case kPolicy: return rows_by_threads<T, kPolicy>(a, sh, sms, cache, s);
