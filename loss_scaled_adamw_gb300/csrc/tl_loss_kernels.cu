@@ -291,9 +291,10 @@ template <> struct Vec<__half> {
 // Where a row's elements lie: `head` elements up to the first 16-byte boundary, `body`
 // whole vectors from there, and a tail.  The head and tail elements ("edges", fewer than
 // 2 N) are held one per thread by the first CTA of the group; [lo, hi) are the vectors of
-// this CTA's share.
+// this CTA's share.  The share begins `off` places behind a 128-byte boundary; those places
+// are empty, so that a warp's copies and stores cover whole lines.
 template <typename T> struct Place {
-    int head, body, edges, lo, hi;
+    int head, body, edges, lo, hi, off;
     __device__ __forceinline__ Place(const T* row, int vocab, int rank, int clog) {
         constexpr int N = Vec<T>::N;
         const int ph = int((reinterpret_cast<uintptr_t>(row) / sizeof(T)) % N);
@@ -303,6 +304,7 @@ template <typename T> struct Place {
         const int share = (body + (1 << clog) - 1) >> clog;
         lo = min(body, rank * share);
         hi = min(body, lo + share);
+        off = int(reinterpret_cast<uintptr_t>(row + head + lo * N) >> 4) & 7;
     }
     __device__ __forceinline__ int edge_at(int i) const { return i < head ? i : i + body * Vec<T>::N; }
     // whether element j is this CTA's: edge element `i`, or in vector `i` of the row
@@ -396,13 +398,11 @@ constexpr int kMaxRingBytes = 220 * 1024;   // dynamic shared memory: tiles and 
 // A tile is kTileVecs vectors per thread, kStages of them are in shared memory.
 constexpr int kTileVecs = 8, kStages = 3;
 constexpr int kSingle = -1;   // POW of the kernels with one sum per row
-constexpr int64_t kRowsInL2 = 48 << 20, kTwoRowsInL2 = 64 << 20;
+constexpr int64_t kRowsInL2 = 48 << 20;
 
-// How a launch lays its rows out: threads per CTA, CTAs per row (2^clog), and whether a
-// streamed row's pass B waits for the next row's pass A (two rows under way per group).
+// How a launch lays its rows out: threads per CTA, and CTAs per row (2^clog).
 struct RowShape {
     int threads, clog;
-    bool two;
 };
 
 // A group of 2^clog CTAs takes one row at a time, each CTA a contiguous share of the row's
@@ -422,7 +422,7 @@ struct RowShape {
 // read once; longer ones are streamed a second time, out of L2 (see shape_for).
 // POW: distillation with both terms at temperatures that differ, two sums per row (DUAL).
 template <typename T, int OP, int B, int POW>
-__global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row(const LossArgs a, const int clog, const bool two) {
+__global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row(const LossArgs a, const int clog) {
     constexpr int N = Vec<T>::N, U = 4, tile = B * kTileVecs, ST = kStages, nw = B / 32;
     constexpr bool DUAL = POW != kSingle;
     constexpr bool kTeach = OP == kDistill;
@@ -575,27 +575,29 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
         // ------------------------------------------------------------ the element warps
         const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + 16u * uint32_t(tid);
         auto row_at = [&](int64_t r) { return static_cast<const T*>(a.x) + r * a.ld; };
-        // all rows lie alike where their stride is a multiple of 16 bytes
-        const bool alike = (a.ld * int(sizeof(T))) % 16 == 0;
+        // all rows lie alike where their stride is a multiple of 128 bytes
+        const bool alike = (a.ld * int(sizeof(T))) % 128 == 0;
         const Place<T> first_place(static_cast<const T*>(a.x), a.vocab, rank, clog);
         auto place_of = [&](const T* x) { return alike ? first_place : Place<T>(x, a.vocab, rank, clog); };
         // Between its passes a share stays in its slot (kept) where it fits a tile, whatever
         // the row's phase; else its tiles are copied again.
-        const bool kept = grad && (a.vocab / N + cluster - 1) >> clog <= tile;
+        const bool kept = grad && ((a.vocab / N + cluster - 1) >> clog) + (alike ? first_place.off : 7) <= tile;
         const bool again = grad && !kept;
         // The copies run ahead in the order of their use.
         int64_t fr = group - ngroups, fynext = a.target && group < a.rows ? a.target[group] : 0;
-        const T *fat = nullptr, *flast = nullptr, *fowed = nullptr;   // this thread's next vector; where the last pass A
-        int fleft = 0, nlast = 0, nowed = 0;                          // and the owed pass B start, and how long they are
+        const T *fat = nullptr, *flast = nullptr;   // this thread's next vector, and where row fr's start
+        int fleft = 0, nlast = 0;                   // places left of the pass, and those of the row's share
+        int foff = 0, flo = 0;                      // empty places before the next vector, and before the row's share
+        bool fback = false;                         // the pass is B
         auto segment = [&]() {
-            if (nowed > 0) {   // a pass B is owed
-                fat = fowed;
-                fleft = nowed;
-                nowed = 0;
+            foff = flo;
+            if (again && nlast > 0 && !fback) {   // pass B of the row whose pass A is asked for
+                fat = flast;
+                fleft = nlast;
+                fback = true;
                 return;
             }
-            const T* const before = flast;
-            const int nbefore = nlast;
+            fback = false;
             nlast = 0;
             while (nlast <= 0) {   // the next row that is not ignored and of which this CTA has a share
                 fr += ngroups;
@@ -605,34 +607,26 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
                 if (y < 0) continue;
                 const T* const x = row_at(fr);
                 const Place<T> pl = place_of(x);
-                nlast = pl.hi - pl.lo;
-                flast = x + pl.head + (pl.lo + tid) * N;
+                foff = flo = pl.off;
+                nlast = pl.hi > pl.lo ? pl.hi - pl.lo + pl.off : 0;
+                flast = x + pl.head + (pl.lo + tid - pl.off) * N;
             }
             fat = flast;
             fleft = nlast;
-            if (again && !two) {   // its own pass B is next
-                fowed = flast;
-                nowed = nlast;
-            } else if (again) {    // that of the row before is next, or now where no row is left
-                fowed = before;
-                nowed = nbefore;
-                if (nlast <= 0 && nowed > 0) {
-                    fat = fowed;
-                    fleft = nowed;
-                    nowed = 0;
-                }
-            }
         };
         auto fetch = [&](int slot) {
             if (fleft <= 0) segment();
             const uint32_t to = ring_at + 16u * uint32_t(slot * tile);
-            if (fleft >= tile) {
+            if (fleft >= tile && foff == 0) {
 #pragma unroll
                 for (int i = 0; i < kTileVecs; ++i) copy_async(to + 16u * B * i, fat + B * N * i);
             } else {   // behind the last row a group is empty
 #pragma unroll
                 for (int i = 0; i < kTileVecs; ++i)
-                    if (tid + B * i < fleft) copy_async(to + 16u * B * i, fat + B * N * i);
+                    if (tid + B * i < fleft && (i > 0 || tid >= foff)) copy_async(to + 16u * B * i, fat + B * N * i);
+                if (tid < foff)
+                    ring[slot * tile + tid] = make_uint4(Vec<T>::kEmpty, Vec<T>::kEmpty, Vec<T>::kEmpty, Vec<T>::kEmpty);
+                foff = 0;
             }
             fat += tile * N;
             fleft -= tile;
@@ -662,7 +656,8 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
 
         // The teacher's elements of a row, written again over the dense gradient once every warp
         // has stored its part of that: an id's first entry takes the weights of all that are
-        // equal to it.  Four lanes to an entry, which look for equal ids.
+        // equal to it.  Four lanes to an entry look for equal ids where that keeps all of them
+        // busy at once, else one.
         int64_t listed = -1, listed_y = 0;
         int listed_buf = 0;
         auto relist = [&]() {
@@ -673,19 +668,23 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
             const int* const ids = reinterpret_cast<const int*>(tb);
             const Place<T> pl = place_of(row_at(listed));
             T* const dx = static_cast<T*>(a.dx) + listed * a.ldd;
-            for (int base = warp * 8; base < n; base += B / 4) {
-                const int i = base + (lane >> 2), id = i < n ? ids[i] : -1;
+            const int ls = 4 * n <= B ? 2 : 0, part = lane & ((1 << ls) - 1);
+            for (int base = (warp * 32) >> ls; base < n; base += B >> ls) {
+                const int i = base + (lane >> ls), id = i < n ? ids[i] : -1;
                 int same = 0;   // entries of this id
-                for (int j = 4 * (lane & 3); j < n; j += 16) {   // ids are padded with -1 to a multiple of 4
+#pragma unroll 2
+                for (int j = 4 * part; j < n; j += 4 << ls) {   // ids are padded with -1 to a multiple of 4
                     const int4 q = *reinterpret_cast<const int4*>(ids + j);
                     same += int(q.x == id) + int(q.y == id) + int(q.z == id) + int(q.w == id);
                 }
-                same += __shfl_xor_sync(~0u, same, 1);
-                same += __shfl_xor_sync(~0u, same, 2);
+                if (ls != 0) {
+                    same += __shfl_xor_sync(~0u, same, 1);
+                    same += __shfl_xor_sync(~0u, same, 2);
+                }
                 bool at_edge;
                 int v;
                 // the label's element has its value already
-                if ((lane & 3) != 0 || id < 0 || (ce_on && id == int(listed_y)) || !pl.owns(id, rank, at_edge, v)) continue;
+                if (part != 0 || id < 0 || (ce_on && id == int(listed_y)) || !pl.owns(id, rank, at_edge, v)) continue;
                 float w = 0.0f;
                 bool lead = true;
                 if (same == 1) {
@@ -717,14 +716,15 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
             const float Mb = fc.x, kq = fc.y, cq = OP == kDistill ? fc.z : 0.0f;
             const float u = Mb * c2, v1 = DUAL ? untempered_ref<POW>(Mb, u) : 0.0f;
             auto dense = [&](float x) { return dense_value(x, Mb, kq, cq); };
-            for (int done = 0; done < hi - lo; done += tile) {
+            for (int done = 0; hi > lo && done < hi - lo + pl.off; done += tile) {
                 if (!kept) take_tile();
                 const uint4* const buf = ring + (kept ? kept_slot : slot) * tile + tid;
-                const int mine = hi - lo - done - tid;   // vector i of the thread exists where B i < mine
-                T* const to = dx + pl.head + (lo + done + tid) * N;
+                const int mine = hi - lo + pl.off - done - tid;   // vector i of the thread exists where B i < mine
+                const bool none = done == 0 && tid < pl.off;      // but for its first one here
+                T* const to = dx + pl.head + (lo + done + tid - pl.off) * N;
                 if (big(Mb)) {   // NaN rows too
 #pragma unroll 1
-                    for (int i = 0; i < kTileVecs && B * i < mine; ++i)
+                    for (int i = none ? 1 : 0; i < kTileVecs && B * i < mine; ++i)
 #pragma unroll 1
                         for (int j = 0; j < N; ++j)
                             to[B * N * i + j] = from_f<T>(dense(to_f(reinterpret_cast<const T*>(buf + B * i)[j])));
@@ -742,12 +742,12 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
                 };
 #pragma unroll 1
                 for (int g = 0; g < kTileVecs; g += U) {
-                    if (whole && B * (g + U - 1) < mine) {
+                    if (whole && B * (g + U - 1) < mine && (g > 0 || !none)) {
 #pragma unroll
                         for (int i = 0; i < U; ++i) emit(g + i);
                     } else {
 #pragma unroll 1
-                        for (int i = g; i < g + U && B * i < mine; ++i) emit(i);
+                        for (int i = g == 0 && none ? 1 : g; i < g + U && B * i < mine; ++i) emit(i);
                     }
                 }
             }
@@ -757,7 +757,7 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
                 // the label's element again, by the thread that stored it
                 bool at_edge;
                 int v;
-                if (pl.owns(int(y), rank, at_edge, v) && (at_edge ? v : (v - lo) & (B - 1)) == tid) dx[y] = from_f<T>(fc.w);
+                if (pl.owns(int(y), rank, at_edge, v) && (at_edge ? v : (v - lo + pl.off) & (B - 1)) == tid) dx[y] = from_f<T>(fc.w);
             }
             if (kTeach && kd_on) {
                 listed = r;
@@ -840,7 +840,7 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
                         if (DUAL) acc1[j & 1] += untempered<POW>(e, f[j], v);
                     }
                 };
-                for (int left = hi - lo; left > 0; left -= tile) {
+                for (int left = hi > lo ? hi - lo + pl.off : 0; left > 0; left -= tile) {
                     take_tile();
                     const uint4* const buf = ring + slot * tile + tid;
                     const int mine = left - tid;
@@ -915,7 +915,7 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
                 }
                 bar_arrive(1 + par, B + 32);
             }
-            if (again && !two && live) {   // not kept waiting
+            if (again && live) {   // not kept waiting: two rows under way would not fit L2
                 back_row = r;
                 back_y = y;
                 back_xe = xe;
@@ -924,7 +924,7 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
             }
             if (back_row >= 0) back(back_row, back_y, back_xe, back_slot, back_par, back_buf);
             if (!live) break;
-            back_row = again && !two ? -1 : r;
+            back_row = again ? -1 : r;
             back_y = y;
             back_xe = xe;
             back_slot = slot;
@@ -956,12 +956,14 @@ __global__ void __launch_bounds__(256) k_pref_grad(const LossArgs a, const int s
     T* dx = static_cast<T*>(a.dx) + r * a.ldd;
     const bool whole = same_phase(x, static_cast<const T*>(dx));
     const T* body = x + row.head;
-    const int lo = seg * NV * 256, hi = min(row.body, lo + NV * 256);
+    // segments end on 128-byte boundaries: the first one is short by `off` vectors
+    const int lo = seg * NV * 256 - row.off, hi = min(row.body, lo + NV * 256);
     const RowStat st = a.stat[r];
     const int64_t y = a.target[r];
     const bool edge = seg == 0 && tid < row.edges;
     if (y < 0 || st.w == 0.0f) {   // ignored, outside every sequence, or a saturated pair
-        for (int v = lo + tid; v < hi; v += 256) store_vec<T>(dx + row.head + int64_t(v) * N, make_uint4(0, 0, 0, 0), whole);
+        for (int v = lo + tid; v < hi; v += 256)
+            if (v >= 0) store_vec<T>(dx + row.head + int64_t(v) * N, make_uint4(0, 0, 0, 0), whole);
         if (edge) dx[row.edge_at(tid)] = from_f<T>(0.0f);
         return;
     }
@@ -969,7 +971,7 @@ __global__ void __launch_bounds__(256) k_pref_grad(const LossArgs a, const int s
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int v = lo + i * 256 + tid;
-        if (v < hi) raw[i] = ld16(body + int64_t(v) * N);
+        if (v >= 0 && v < hi) raw[i] = ld16(body + int64_t(v) * N);
     }
     const float xe = edge ? to_f(x[row.edge_at(tid)]) : 0.0f;
     const float c2 = a.it * kLog2e, kq = -st.w * st.rs;
@@ -988,7 +990,7 @@ __global__ void __launch_bounds__(256) k_pref_grad(const LossArgs a, const int s
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int v = lo + i * 256 + tid;
-        if (v < hi) {
+        if (v >= 0 && v < hi) {
             float f[N];
             Vec<T>::wide(raw[i], f);
             if (big(st.m)) {
@@ -1005,17 +1007,20 @@ __global__ void __launch_bounds__(256) k_pref_grad(const LossArgs a, const int s
 }
 
 template <typename T>
-RowShape shape_for(int64_t rows, int vocab, bool grad, int sms) {
+RowShape shape_for(int op, int64_t rows, int vocab, bool grad, int sms) {
     const int vecs = (vocab + Vec<T>::N - 1) / Vec<T>::N;
-    RowShape s{64, 0, true};
-    while (s.threads < 256 && s.threads * 8 < vecs) s.threads *= 2;
+    RowShape s{64, 0};
+    // Threads: more where a row is long enough to keep them busy.  Share of the copy rate on
+    // thousands of bf16 rows with 64 / 128 / 256 threads: policy 58 / 55 / 31 % at 4,096
+    // entries, 64 / 80 / 59 at 8,192, 73 / 83 / 74 at 24,000, 77 / 77 / 88 at 32,768;
+    // log-probabilities 82 / 95 / 85 at 32,768, 89 / 93 / 97 at 80,000; distillation
+    // 56 / 70 / 58 at 32,768, 58 / 61 / 74 at 80,000.
+    if (vecs >= 512) s.threads = vecs > (op == kPolicy && grad ? 3500 : 8192) ? 256 : 128;
     // Long rows are read twice, the second time out of L2 if what is under way (two CTAs per
     // SM) fits it: more CTAs to a row where it would not, and then one row at a time.
     const int64_t under_way = int64_t(2) * sms * vocab * int(sizeof(T));
-    if (grad && s.threads == 256) {
+    if (grad && s.threads == 256)
         while (s.clog < kMaxClusterLog && under_way >> s.clog > kRowsInL2) s.clog += 1;
-        s.two = 2 * (under_way >> s.clog) <= kTwoRowsInL2;
-    }
     // few rows: spread each over more CTAs while the GPU has idle SMs and a thread more than one vector
     while (s.clog < kMaxClusterLog && rows << (s.clog + 1) <= sms && s.threads << s.clog < vecs) s.clog += 1;
     return s;
@@ -1068,7 +1073,7 @@ cudaError_t row_launch(const LossArgs& a, const RowShape& sh, int sms, GroupCach
     if (e != cudaSuccess) return e;
     if (groups > a.rows) groups = a.rows < 1 ? 1 : int(a.rows);
     cfg.gridDim.x = unsigned(groups) << sh.clog;
-    return cudaLaunchKernelEx(&cfg, kernel, a, int(sh.clog), sh.two);
+    return cudaLaunchKernelEx(&cfg, kernel, a, int(sh.clog));
 }
 
 template <typename T, int OP, int POW = kSingle>
@@ -1081,7 +1086,7 @@ cudaError_t rows_by_threads(const LossArgs& a, const RowShape& sh, int sms, Grou
 template <typename T>
 cudaError_t rows_by_op(int op, const LossArgs& a, int sms, GroupCache& cache, cudaStream_t s) {
     const bool grad = a.dx != nullptr && (op == kPolicy || op == kDistill);
-    const RowShape sh = shape_for<T>(a.rows, a.vocab, grad, sms);
+    const RowShape sh = shape_for<T>(op, a.rows, a.vocab, grad, sms);
     switch (op) {
         case kLogprob: return rows_by_threads<T, kLogprob>(a, sh, sms, cache, s);
         case kPolicy: return rows_by_threads<T, kPolicy>(a, sh, sms, cache, s);
@@ -1098,7 +1103,7 @@ template <typename T>
 cudaError_t pref_grad(const LossArgs& a, cudaStream_t s) {
     const int vecs = (a.vocab + Vec<T>::N - 1) / Vec<T>::N;
     constexpr int NV = 4;
-    const int64_t segs = vecs <= NV * 256 ? 1 : (vecs + NV * 256 - 1) / (NV * 256);
+    const int64_t segs = (vecs + 7 + NV * 256 - 1) / (NV * 256);
     if (a.rows * segs > 0x7fffffff) return cudaErrorInvalidValue;
     k_pref_grad<T, NV><<<unsigned(a.rows * segs), 256, 0, s>>>(a, int(segs));
     return cudaGetLastError();
