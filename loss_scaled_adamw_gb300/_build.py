@@ -2,12 +2,15 @@
 
 The translation units (kernels, host C ABI, the allocation-free entry point, the
 objectives over logits) compile in parallel, then link into one shared library with
-the CUDA runtime linked statically.
+the CUDA runtime linked statically.  The objectives' binding (_loss_bind, a CPython
+module over torch's headers) is host code of its own beside it.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -17,6 +20,8 @@ LIB = os.path.join(PKG, "libtl_gb300.so")
 SOURCES = ["tl_kernels.cu", "tl_kernels_split.cu", "tl_api.cu", "tl_noalloc.cu", "tl_loss_kernels.cu", "tl_loss_api.cu"]
 HEADERS = [os.path.join(CSRC, "tl_internal.cuh"), os.path.join(CSRC, "tl_loss_internal.cuh"),
            os.path.join(ROOT, "include", "tl.h"), os.path.join(ROOT, "include", "tl_loss.h")]
+BIND = os.path.join(PKG, "_loss_bind.so")
+BIND_SOURCE = os.path.join(CSRC, "tl_loss_bind.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-lineinfo", "-O3", "-std=c++17", "-fmad=false", "-Xcompiler", "-fPIC",
                      "-I" + os.path.join(ROOT, "include")]
@@ -35,10 +40,35 @@ def _stale(target: str, deps) -> bool:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link the library if any source or header is newer than it."""
+    """Compile and link the library and the objectives' binding where a source or header is newer."""
     srcs = [os.path.join(CSRC, s) for s in SOURCES]
-    if not force and not _stale(LIB, srcs + HEADERS + [__file__]):
-        return LIB
+    if force or _stale(LIB, srcs + HEADERS + [__file__]):
+        _build_library(srcs, verbose)
+    if force or _stale(BIND, [BIND_SOURCE, __file__] + HEADERS):
+        _build_binding(verbose)
+    return LIB
+
+
+def _run(cmd, verbose: bool, what: str) -> None:
+    if verbose:
+        print(" ".join(cmd))
+    r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n" + " ".join(cmd) + "\n" + r.stdout)
+
+
+def _build_binding(verbose: bool) -> None:
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    tmp = BIND + f".tmp{os.getpid()}"
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-I" + sysconfig.get_path("include"),
+          "-isystem", os.path.join(torch, "include"),
+          "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"), BIND_SOURCE, "-o", tmp,
+          "-L" + PKG, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(torch, "lib"),
+          "-ltorch_python", "-ltorch_cpu", "-lc10"], verbose, "g++")
+    os.replace(tmp, BIND)
+
+
+def _build_library(srcs, verbose: bool) -> None:
     os.makedirs(BUILD, exist_ok=True)
     objs, procs = [], []
     for src in srcs:
@@ -55,12 +85,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if verbose and out:
             print(out)
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
-    r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("link failed:\n" + " ".join(cmd) + "\n" + r.stdout)
+    _run([nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs], verbose, "link")
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":

@@ -18,18 +18,15 @@ until it has run.
 from __future__ import annotations
 
 import ctypes
-import struct
 
 import torch
 
-from . import TL_BF16, TL_F16, TL_F32, TL_OK, TLError, load_library
+from . import TL_OK, TLError, load_library
 from . import _stream as _any_stream
 
 LOSS_EXPORTED = ("tl_loss_create", "tl_loss_destroy", "tl_token_logprob", "tl_policy_loss", "tl_preference_loss",
                  "tl_distill_loss", "tl_loss_launch_count", "tl_loss_last_error")
 
-_DTYPES = {torch.float32: TL_F32, torch.bfloat16: TL_BF16, torch.float16: TL_F16}
-_ID_BYTES = {torch.int32: 4, torch.int64: 8}
 _vp, _i64, _i32, _f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
 
 
@@ -61,16 +58,18 @@ class tl_distill_args(ctypes.Structure):
                 ("teacher_dtype", _i32), ("id_bytes", _i32), ("kd_weight", _f32), ("ce_weight", _f32)]
 
 
-_lib = None
+_lib = _bind = None
 _raw_stream = torch._C._cuda_getCurrentRawStream   # current_stream() without its Stream object (3 us a call)
 
 
 def _stream(lctx, stream):
-    return _raw_stream(lctx.device) if stream is None else _any_stream(stream)
+    """The raw stream of a call, as an integer: the current one of the context's device for None."""
+    return _raw_stream(lctx.device) if stream is None else _any_stream(stream).value
 
 
 def _load():
-    global _lib
+    """The library and the module that passes tensors to it (_loss_bind, csrc/tl_loss_bind.cpp)."""
+    global _lib, _bind
     if _lib is None:
         lib = load_library()
         P = ctypes.POINTER
@@ -85,35 +84,30 @@ def _load():
                 ("tl_loss_last_error", ctypes.c_char_p, [_vp])):
             fn = getattr(lib, name)
             fn.restype, fn.argtypes = res, args
+        try:
+            from . import _loss_bind as _bind
+        except ImportError as e:
+            raise ImportError("loss_scaled_adamw_gb300/_loss_bind.so is missing: build it with "
+                              "loss_scaled_adamw_gb300._build.build(); there is no fallback") from e
         _lib = lib
     return _lib
 
 
 class LossContext:
-    """Owns one tl_loss_ctx (its scratch lives on the device that was current at creation)
-    and the argument structures that its calls fill in (a context is used by one thread)."""
+    """Owns one tl_loss_ctx (its scratch lives on the device that was current at creation)."""
 
     def __init__(self, handle, device: int):
         self.handle = handle
         self.device = device
-        self._x, self._out = tl_logits(), tl_loss_out()
-        self._args = {c: c() for c in (tl_policy_args, tl_preference_args, tl_distill_args)}
-        # one pack per call and structure: assigning the fields one by one costs more than
-        # the launch
-        self._refs = {c: ctypes.byref(v) for c, v in self._args.items()}
-        self._x_ref, self._out_ref = ctypes.byref(self._x), ctypes.byref(self._out)
+
+    @property
+    def _address(self):
+        return self.handle.value if self.handle else None
 
     def __del__(self):
         if getattr(self, "handle", None) and _lib is not None:
             _lib.tl_loss_destroy(self.handle)
             self.handle = None
-
-
-# The structures' layouts for struct.pack_into (native sizes and alignment).
-_PACK_LOGITS = struct.Struct("@Pqqqif")
-_PACK_OUT = struct.Struct("@qPPqPPP")
-_PACK = {tl_policy_args: struct.Struct("@PPPPfff"), tl_preference_args: struct.Struct("@PPqPffP"),
-         tl_distill_args: struct.Struct("@PPPqiiiff")}
 
 
 def _check(lctx, fn: str, rc: int):
@@ -144,65 +138,9 @@ def tl_loss_launch_count(lctx: LossContext) -> int:
     return int(_load().tl_loss_launch_count(lctx.handle))
 
 
-_F32, _I64 = torch.float32, torch.int64
-
-
-def _vec(lctx, t, dtype, n: int, name: str) -> int:
-    """Address of a contiguous device vector of n elements, 0 for None."""
-    if t is None:
-        return 0
-    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or t.get_device() != lctx.device:
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements on cuda:{lctx.device}")
-    return t.data_ptr()
-
-
-def _matrix(lctx, t, name: str):
-    """(address, rows, columns, row stride) of a 2-D device tensor with contiguous rows."""
-    if t.dim() != 2 or t.get_device() != lctx.device:
-        raise ValueError(f"{name} must be a 2-D tensor on cuda:{lctx.device}")
-    rows, cols = t.shape
-    ld, step = t.stride()
-    if step != 1 and cols > 1:
-        raise ValueError(f"the rows of {name} must be contiguous")
-    return t.data_ptr(), rows, cols, ld if rows > 1 or ld > cols else cols
-
-
-def _logits(lctx, x, temperature) -> int:
-    """Fills in the context's tl_logits; the number of rows."""
-    addr, rows, vocab, ld = _matrix(lctx, x, "logits")
-    dt = _DTYPES.get(x.dtype)
-    if dt is None:
-        raise ValueError("logits must be float32, bfloat16 or float16")
-    _PACK_LOGITS.pack_into(lctx._x, 0, addr, rows, vocab, ld, dt, temperature)
-    return rows
-
-
-def _out(lctx, x, n, result, seed, dlogits, logp, rows, loss, losses) -> None:
-    """Fills in the context's tl_loss_out.  seed: a device address (tl_scale_ptr), a float32
-    CUDA tensor of one element, or None."""
-    d = ldd = 0
-    if dlogits is not None:
-        d, _, _, ldd = _matrix(lctx, dlogits, "dlogits")
-        if dlogits.dtype is not x.dtype or dlogits.shape != x.shape:
-            raise ValueError("dlogits must have the shape and dtype of the logits")
-    if not isinstance(seed, int):
-        seed = _vec(lctx, seed, _F32, 1, "seed")
-    _PACK_OUT.pack_into(lctx._out, 0, n, seed, d, ldd, _vec(lctx, logp, _F32, rows, "logp"),
-                        _vec(lctx, loss, _F32, losses, "the loss output"), _vec(lctx, result, _F32, 4, "result"))
-
-
-def _call(lctx, name: str, cls, stream, *fields) -> None:
-    _PACK[cls].pack_into(lctx._args[cls], 0, *fields)
-    rc = getattr(_load(), name)(lctx.handle, lctx._x_ref, lctx._refs[cls], lctx._out_ref, _stream(lctx, stream))
-    if rc != TL_OK:
-        _check(lctx, name, rc)
-
-
 def tl_token_logprob(lctx: LossContext, logits, targets, logp, temperature: float = 1.0, stream=None) -> None:
     """logp[t] = log softmax(logits[t] / temperature)[targets[t]]; 0 where targets[t] < 0."""
-    T = _logits(lctx, logits, temperature)
-    rc = _load().tl_token_logprob(lctx.handle, lctx._x_ref, _vec(lctx, targets, _I64, T, "targets"),
-                                  _vec(lctx, logp, _F32, T, "logp"), _stream(lctx, stream))
+    rc = _bind.token_logprob(lctx._address, lctx.device, logits, temperature, targets, logp, _stream(lctx, stream))
     if rc != TL_OK:
         _check(lctx, "tl_token_logprob", rc)
 
@@ -211,12 +149,13 @@ def tl_policy_loss(lctx: LossContext, logits, targets, old_logp, advantages, n: 
                    clip_low: float = 0.2, clip_high: float = 0.2, kl_weight: float = 0.0, temperature: float = 1.0,
                    seed=None, dlogits=None, logp=None, row_loss=None, stream=None) -> None:
     """Clipped policy objective with a KL penalty, mean over n valid targets; its gradient
-    into dlogits (which may be the logits themselves)."""
-    T = _logits(lctx, logits, temperature)
-    _out(lctx, logits, n, result, seed, dlogits, logp, T, row_loss, T)
-    _call(lctx, "tl_policy_loss", tl_policy_args, stream, _vec(lctx, targets, _I64, T, "targets"),
-          _vec(lctx, old_logp, _F32, T, "old_logp"), _vec(lctx, ref_logp, _F32, T, "ref_logp"),
-          _vec(lctx, advantages, _F32, T, "advantages"), clip_low, clip_high, kl_weight)
+    into dlogits (which may be the logits themselves).  seed: a device address (tl_scale_ptr),
+    a float32 CUDA tensor of one element, or None."""
+    rc = _bind.policy_loss(lctx._address, lctx.device, logits, temperature, n, seed, dlogits, logp, row_loss, result,
+                           _stream(lctx, stream), targets, old_logp, ref_logp, advantages, clip_low, clip_high,
+                           kl_weight)
+    if rc != TL_OK:
+        _check(lctx, "tl_policy_loss", rc)
 
 
 def tl_preference_loss(lctx: LossContext, logits, targets, seq, n: int, result, ref_logp=None, beta: float = 0.1,
@@ -224,15 +163,10 @@ def tl_preference_loss(lctx: LossContext, logits, targets, seq, n: int, result, 
                        pair_loss=None, reward=None, stream=None) -> None:
     """Paired preference objective, mean over n pairs.  seq: int64 CUDA tensor of
     2 * pairs + 1 row offsets (chosen, rejected, chosen, ...)."""
-    T = _logits(lctx, logits, temperature)
-    bounds = seq.numel()
-    if bounds % 2 != 1:
-        raise ValueError("seq must hold 2 * pairs + 1 offsets")
-    pairs = bounds // 2
-    _out(lctx, logits, n, result, seed, dlogits, logp, T, pair_loss, pairs)
-    _call(lctx, "tl_preference_loss", tl_preference_args, stream, _vec(lctx, targets, _I64, T, "targets"),
-          _vec(lctx, seq, _I64, bounds, "seq"), pairs, _vec(lctx, ref_logp, _F32, T, "ref_logp"), beta,
-          label_smoothing, _vec(lctx, reward, _F32, 2 * pairs, "reward"))
+    rc = _bind.preference_loss(lctx._address, lctx.device, logits, temperature, n, seed, dlogits, logp, pair_loss,
+                               result, _stream(lctx, stream), targets, seq, ref_logp, beta, label_smoothing, reward)
+    if rc != TL_OK:
+        _check(lctx, "tl_preference_loss", rc)
 
 
 def tl_distill_loss(lctx: LossContext, logits, teacher_logits, teacher_ids, n: int, result, targets=None,
@@ -240,15 +174,7 @@ def tl_distill_loss(lctx: LossContext, logits, teacher_logits, teacher_ids, n: i
                     row_loss=None, stream=None) -> None:
     """Distillation from a teacher's top-k logits ([rows, k], ids int32 or int64), mean over
     n valid rows.  teacher_logits = teacher_ids = None is the cross-entropy alone."""
-    T = _logits(lctx, logits, temperature)
-    t_addr = i_addr = ldt = k = tdt = id_bytes = 0
-    if teacher_logits is not None:
-        t_addr, t_rows, k, ldt = _matrix(lctx, teacher_logits, "teacher_logits")
-        i_addr, i_rows, i_cols, ldi = _matrix(lctx, teacher_ids, "teacher_ids")
-        tdt = _DTYPES.get(teacher_logits.dtype, -1)
-        id_bytes = _ID_BYTES.get(teacher_ids.dtype, -1)
-        if t_rows != T or i_rows != T or i_cols != k or ldt != ldi:
-            raise ValueError("teacher_logits and teacher_ids must be [rows, k] with one row stride")
-    _out(lctx, logits, n, result, seed, dlogits, None, T, row_loss, T)
-    _call(lctx, "tl_distill_loss", tl_distill_args, stream, _vec(lctx, targets, _I64, T, "targets"), t_addr, i_addr,
-          ldt, k, tdt, id_bytes, kd_weight, ce_weight)
+    rc = _bind.distill_loss(lctx._address, lctx.device, logits, temperature, n, seed, dlogits, None, row_loss, result,
+                            _stream(lctx, stream), targets, teacher_logits, teacher_ids, kd_weight, ce_weight)
+    if rc != TL_OK:
+        _check(lctx, "tl_distill_loss", rc)
