@@ -81,11 +81,44 @@ __device__ __forceinline__ void bar_arrive(int id, int count) {
     asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
-// The loss sums of one launch: each row group (a CTA or a cluster) adds its rows in
-// order and writes a slot, and the group that takes the last ticket adds the slots.
+// The loss sums of one launch: each row group adds its rows in order and writes a slot, and
+// the group that takes the last ticket adds the slots.
 struct LossSums {
     double loss = 0.0, first = 0.0, second = 0.0, count = 0.0;
 };
+
+// Whether this group is the last of the launch to come here (lane 0 of one warp asks).
+__device__ __forceinline__ bool last_group(const LossArgs& a, int ngroups) {
+    __threadfence();
+    if (atomicAdd(a.ticket, 1u) != uint32_t(ngroups - 1)) return false;
+    __threadfence();
+    *a.ticket = 0;   // ready for the next call
+    return true;
+}
+
+// By the statistics warp of a group's first CTA, whose first lane holds the sums: the element
+// warps may still be writing gradients.
+__device__ __forceinline__ void finish_sums(const LossArgs& a, const LossSums& sum, int group, int ngroups) {
+    const int lane = threadIdx.x & 31;
+    double2* const slots = reinterpret_cast<double2*>(a.slots);
+    bool last = false;
+    if (lane == 0) {
+        slots[2 * group] = make_double2(sum.loss, sum.first);
+        slots[2 * group + 1] = make_double2(sum.second, sum.count);
+        last = last_group(a, ngroups);
+    }
+    if (!__shfl_sync(~0u, last, 0)) return;
+    double v[4] = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll 4
+    for (int i = lane; i < ngroups; i += 32) {
+        const double2 p = __ldcg(slots + 2 * i), q = __ldcg(slots + 2 * i + 1);
+        v[0] += p.x; v[1] += p.y; v[2] += q.x; v[3] += q.y;
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) v[c] = warp_sum(v[c]);
+    const double mine = lane == 0 ? v[0] : lane == 1 ? v[1] : lane == 2 ? v[2] : v[3];
+    if (lane < 4) a.result[lane] = float(lane < 3 ? mine * a.per_n : mine);
+}
 
 // The four sums over the first B threads of the CTA, and the result.
 template <int B> __device__ __forceinline__ void write_sums(const LossArgs& a, double (&v)[4]) {
@@ -108,36 +141,14 @@ template <int B> __device__ __forceinline__ void write_sums(const LossArgs& a, d
 
 template <int B> __device__ void pair_stage(const LossArgs& a);
 
-// Called by every thread of a group's first CTA.  The statistics warp's first lane, thread
-// B, holds the sums and has written the rows' outputs.
-template <int OP, int B>
-__device__ void finish(const LossArgs& a, const LossSums& sum, int group, int ngroups) {
+// The preference's first pass: called by every thread of a group's first CTA, whose thread B
+// (the statistics warp's first lane) has written the rows' statistics.
+template <int B> __device__ void finish_pairs(const LossArgs& a, int ngroups) {
     __shared__ bool last;
-    const int tid = threadIdx.x;
-    if (tid == B) {
-        if (OP == kPolicy || OP == kDistill) {
-            double2* o = reinterpret_cast<double2*>(a.slots) + 2 * group;
-            o[0] = make_double2(sum.loss, sum.first);
-            o[1] = make_double2(sum.second, sum.count);
-        }
-        __threadfence();
-        last = atomicAdd(a.ticket, 1u) == uint32_t(ngroups - 1);
-        if (last) __threadfence();
-    }
     __syncthreads();
-    if (!last || tid >= B) return;
-    if (OP == kPrefStat) {
-        pair_stage<B>(a);
-    } else {
-        double v[4] = {0.0, 0.0, 0.0, 0.0};
-        for (int i = tid; i < ngroups; i += B) {
-            const double2 p = __ldcg(reinterpret_cast<const double2*>(a.slots) + 2 * i);
-            const double2 q = __ldcg(reinterpret_cast<const double2*>(a.slots) + 2 * i + 1);
-            v[0] += p.x; v[1] += p.y; v[2] += q.x; v[3] += q.y;
-        }
-        write_sums<B>(a, v);
-    }
-    if (tid == 0) *a.ticket = 0;   // ready for the next call
+    if (threadIdx.x == B) last = last_group(a, ngroups);
+    __syncthreads();
+    if (last && threadIdx.x < B) pair_stage<B>(a);
 }
 
 // The pairs, by the last CTA of the first preference pass: a warp sums the log-ratios of
@@ -159,19 +170,18 @@ template <int B> __device__ void pair_stage(const LossArgs& a) {
             at[i] = at[i] < prev ? prev : at[i];
             at[i] = prev = at[i] > a.rows ? a.rows : at[i];
         }
-        double s[2];
+        double s[2] = {0.0, 0.0};
+        for (int64_t r = at[0] + lane; r < at[2]; r += 32 * U) {
+            float q[U];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            double v = 0.0;
-            for (int64_t r = at[i] + lane; r < at[i + 1]; r += 32 * U) {
-                float q[U];
+            for (int j = 0; j < U; ++j) q[j] = r + 32 * j < at[2] ? __ldcg(&a.stat[r + 32 * j].ratio) : 0.0f;
 #pragma unroll
-                for (int j = 0; j < U; ++j) q[j] = r + 32 * j < at[i + 1] ? __ldcg(&a.stat[r + 32 * j].ratio) : 0.0f;
-#pragma unroll
-                for (int j = 0; j < U; ++j) v += double(q[j]);
+            for (int j = 0; j < U; ++j) {
+                if (r + 32 * j < at[1]) s[0] += double(q[j]); else s[1] += double(q[j]);
             }
-            s[i] = warp_sum(v);
         }
+        s[0] = warp_sum(s[0]);
+        s[1] = warp_sum(s[1]);
         const float h = float(double(a.beta) * (s[0] - s[1]));   // beta * h
         // log sg(h) = min(h, 0) - log1p(exp(-|h|)); sg(-h) and sg(h) without overflow
         const float t = expf(-fabsf(h)), l1 = log1pf(t);
@@ -461,6 +471,8 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
         return y;
     };
 
+    if (OP == kPrefStat) asm volatile("griddepcontrol.launch_dependents;");   // the gradient's kernel, see there
+
     if (warp == nw) {
         // ------------------------------------------------------------ the statistics warp
         const float step = (kGrad && a.seed ? *a.seed : 1.0f) * a.inv_n;
@@ -571,6 +583,7 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
             par ^= 1;
             buf4 = (buf4 + 1) & 3;
         }
+        if (kGrad && rank == 0) finish_sums(a, sum, group, ngroups);
     } else {
         // ------------------------------------------------------------ the element warps
         const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + 16u * uint32_t(tid);
@@ -614,8 +627,7 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
             fat = flast;
             fleft = nlast;
         };
-        auto fetch = [&](int slot) {
-            if (fleft <= 0) segment();
+        auto issue = [&](int slot) {
             const uint32_t to = ring_at + 16u * uint32_t(slot * tile);
             if (fleft >= tile && foff == 0) {
 #pragma unroll
@@ -631,6 +643,10 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
             fat += tile * N;
             fleft -= tile;
             copy_commit();
+        };
+        auto fetch = [&](int slot) {
+            if (fleft <= 0) segment();
+            issue(slot);
         };
         int slot = -1;   // of the tile last taken
         auto take_tile = [&]() {
@@ -766,8 +782,26 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
             }
         };
 
+        // The group's first row is taken to count: its first tile is asked for along with its label.
+        bool guessed = false;
+        if (group < a.rows) {
+            const T* const x = row_at(group);
+            const Place<T> pl = place_of(x);
+            fr = group;
+            foff = flo = pl.off;
+            nlast = fleft = pl.hi > pl.lo ? pl.hi - pl.lo + pl.off : 0;
+            flast = fat = x + pl.head + (pl.lo + tid - pl.off) * N;
+            issue(0);
+            guessed = fynext >= 0 && nlast > 0;
+            if (a.target && group + ngroups < a.rows) fynext = a.target[group + ngroups];
+            if (!guessed) {
+                copy_wait<0>();
+                fleft = nlast = 0;
+            }
+        }
+        if (!guessed) fetch(0);
 #pragma unroll
-        for (int i = 0; i < ST - 1; ++i) fetch(i);
+        for (int i = 1; i < ST - 1; ++i) fetch(i);
         if (kept) fetch(ST - 1);
         if (kTeach && kd_on) ask_teacher(group);
         if (cluster > 1) {
@@ -940,11 +974,13 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
         if (exchanged) cluster_wait();
         copy_wait<0>();
     }
-    if (OP != kLogprob && rank == 0) finish<OP, B>(a, sum, group, ngroups);
+    if (OP == kPrefStat && rank == 0) finish_pairs<B>(a, ngroups);
 }
 
 // Second preference pass: every element from its row's statistics, one segment of a row
-// per CTA, the last rows first (the first pass left them in L2).
+// per CTA, the last rows first (the first pass left them in L2).  It is launched to start
+// while the first pass runs: its CTAs read their part of the logits, and wait for that
+// kernel's end before they use the statistics.
 template <typename T, int NV>
 __global__ void __launch_bounds__(256) k_pref_grad(const LossArgs a, const int segs) {
     constexpr int N = Vec<T>::N;
@@ -958,13 +994,18 @@ __global__ void __launch_bounds__(256) k_pref_grad(const LossArgs a, const int s
     const T* body = x + row.head;
     // segments end on 128-byte boundaries: the first one is short by `off` vectors
     const int lo = seg * NV * 256 - row.off, hi = min(row.body, lo + NV * 256);
-    const RowStat st = a.stat[r];
     const int64_t y = a.target[r];
     const bool edge = seg == 0 && tid < row.edges;
-    if (y < 0 || st.w == 0.0f) {   // ignored, outside every sequence, or a saturated pair
+    auto zeros = [&]() {
         for (int v = lo + tid; v < hi; v += 256)
             if (v >= 0) store_vec<T>(dx + row.head + int64_t(v) * N, make_uint4(0, 0, 0, 0), whole);
         if (edge) dx[row.edge_at(tid)] = from_f<T>(0.0f);
+    };
+    // every CTA waits for the first pass, so that this grid does not end before it
+    auto first_pass = [] { asm volatile("griddepcontrol.wait;" ::: "memory"); };
+    if (y < 0) {   // ignored: the first pass does not look at the row
+        zeros();
+        first_pass();
         return;
     }
     uint4 raw[NV];
@@ -974,7 +1015,6 @@ __global__ void __launch_bounds__(256) k_pref_grad(const LossArgs a, const int s
         if (v >= 0 && v < hi) raw[i] = ld16(body + int64_t(v) * N);
     }
     const float xe = edge ? to_f(x[row.edge_at(tid)]) : 0.0f;
-    const float c2 = a.it * kLog2e, kq = -st.w * st.rs;
     // the label's element: its thread stores it after its vector
     int mine = -1;
     float xy = 0.0f;
@@ -986,7 +1026,14 @@ __global__ void __launch_bounds__(256) k_pref_grad(const LossArgs a, const int s
             xy = to_f(x[j]);
         }
     }
-    const float u = st.m * c2;
+    // everything so far was input; the statistics are the first pass's, which may still be running
+    first_pass();
+    const RowStat st = a.stat[r];
+    if (st.w == 0.0f) {   // outside every sequence, or of a saturated pair
+        zeros();
+        return;
+    }
+    const float c2 = a.it * kLog2e, kq = -st.w * st.rs, u = st.m * c2;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int v = lo + i * 256 + tid;
@@ -1021,8 +1068,8 @@ RowShape shape_for(int op, int64_t rows, int vocab, bool grad, int sms) {
     const int64_t under_way = int64_t(2) * sms * vocab * int(sizeof(T));
     if (grad && s.threads == 256)
         while (s.clog < kMaxClusterLog && under_way >> s.clog > kRowsInL2) s.clog += 1;
-    // few rows: spread each over more CTAs while the GPU has idle SMs and a thread more than one vector
-    while (s.clog < kMaxClusterLog && rows << (s.clog + 1) <= sms && s.threads << s.clog < vecs) s.clog += 1;
+    // few rows: spread each over more CTAs while the GPU has idle SMs and the share is over a tile
+    while (s.clog < kMaxClusterLog && rows << (s.clog + 1) <= sms && (s.threads * kTileVecs) << s.clog < vecs) s.clog += 1;
     return s;
 }
 
@@ -1105,8 +1152,16 @@ cudaError_t pref_grad(const LossArgs& a, cudaStream_t s) {
     constexpr int NV = 4;
     const int64_t segs = (vecs + 7 + NV * 256 - 1) / (NV * 256);
     if (a.rows * segs > 0x7fffffff) return cudaErrorInvalidValue;
-    k_pref_grad<T, NV><<<unsigned(a.rows * segs), 256, 0, s>>>(a, int(segs));
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned(a.rows * segs));
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // starts while the first pass runs
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_pref_grad<T, NV>, a, int(segs));
 }
 
 }  // namespace
