@@ -384,6 +384,16 @@ template <int POW> __device__ __forceinline__ float untempered(float e, float x,
     const float r = e * e;
     return POW == 4 ? r * r : r;
 }
+// acc plus the untempered exponential; e kq plus it times cq.  Powers fold into multiply-adds.
+template <int POW> __device__ __forceinline__ float add_untempered(float acc, float e, float x, float v) {
+    if (POW == 0) return acc + untempered<POW>(e, x, v);
+    const float r = POW == 4 ? e * e : e;
+    return __fmaf_rn(r, r, acc);
+}
+template <int POW> __device__ __forceinline__ float mix(float e, float x, float v, float kq, float cq) {
+    if (POW == 2) return e * __fmaf_rn(e, cq, kq);
+    return __fmaf_rn(untempered<POW>(e, x, v), cq, e * kq);
+}
 // The exponent's reference at temperature 1 for a largest element m, u = m c2.
 template <int POW> __device__ __forceinline__ float untempered_ref(float m, float u) {
     return POW == 0 ? m * kLog2e : u * float(POW);
@@ -721,7 +731,7 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
         auto back = [&](int64_t r, int64_t y, float xe, int kept_slot, int was, int buffer) {
             bar_sync(3 + was, B + 32);   // the row's factors
             if (!grad) return;
-            if (kTeach && listed >= 0) relist();
+            if (kTeach && listed >= 0 && !again) relist();
             const T* const x = row_at(r);
             const Place<T> pl = place_of(x);
             const int lo = pl.lo, hi = pl.hi;
@@ -752,7 +762,7 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
 #pragma unroll
                     for (int j = 0; j < N; ++j) {
                         const float e = ex2(__fmaf_rn(f[j], c2, -u));
-                        f[j] = DUAL ? __fmaf_rn(untempered<POW>(e, f[j], v1), cq, e * kq) : e * kq;
+                        f[j] = DUAL ? mix<POW>(e, f[j], v1, kq, cq) : e * kq;
                     }
                     store_vec<T>(to + B * N * i, Vec<T>::narrow(f), whole);
                 };
@@ -871,7 +881,7 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
                     for (int j = 0; j < N; ++j) {
                         const float e = ex2(__fmaf_rn(f[j], c2, -u));
                         acc[j & 1] += e;
-                        if (DUAL) acc1[j & 1] += untempered<POW>(e, f[j], v);
+                        if (DUAL) acc1[j & 1] = add_untempered<POW>(acc1[j & 1], e, f[j], v);
                     }
                 };
                 for (int left = hi > lo ? hi - lo + pl.off : 0; left > 0; left -= tile) {
@@ -921,16 +931,26 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
                     // thread is in registers
                     float* const tb = teach + buf4 * 3 * kpad;
                     if (tid < kpad - a.k) tb[a.k + tid] = __int_as_float(-1);
-                    float tm = kNegInf, ts = 0.0f, td = 0.0f, bad = 0.0f;
-                    for (int i = tid; i < a.k; i += B) {
-                        const int64_t id = i == tid ? id0 : teacher_id(a, r * a.ldt + i);
+                    auto entry = [&](int j, int64_t id, float logit, float z, float& t) {   // into the buffer; t / tau
                         const bool on = id >= 0 && id < a.vocab;
-                        const float t = !on ? kNegInf : (i == tid ? t0 : teacher_logit(a, r * a.ldt + i)) * a.it;
-                        const float z = !on ? 0.0f : i == tid ? z0 : to_f(x[id]);
-                        if (id >= a.vocab) bad = kNaN;
-                        tb[i] = __int_as_float(on ? int(id) : -1);
-                        tb[kpad + i] = t;
-                        tb[2 * kpad + i] = z;
+                        t = on ? logit * a.it : kNegInf;
+                        tb[j] = __int_as_float(on ? int(id) : -1);
+                        tb[kpad + j] = t;
+                        tb[2 * kpad + j] = z;
+                    };
+                    float tm = kNegInf, ts = 0.0f, td = 0.0f;
+                    bool beyond = tid < a.k && id0 >= a.vocab;
+                    if (tid < a.k) {
+                        entry(tid, id0, t0, z0, tm);
+                        ts = tm > kNegInf || tm != tm ? 1.0f : 0.0f;   // exp(t - t)
+                        td = ts != 0.0f ? tm - z0 * a.it : 0.0f;
+                    }
+                    for (int j = tid + B; j < a.k; j += B) {
+                        const int64_t id = teacher_id(a, r * a.ldt + j);
+                        const float z = id >= 0 && id < a.vocab ? to_f(x[id]) : 0.0f;
+                        float t;
+                        entry(j, id, teacher_logit(a, r * a.ldt + j), z, t);
+                        beyond = beyond || id >= a.vocab;
                         const float nm = fmaxf(tm, t), f = rescale(tm, part_ref(nm), kLog2e), e = power(t, part_ref(nm), kLog2e);
                         ts = ts * f + e;
                         td = (f != 0.0f ? td * f : 0.0f) + (e != 0.0f ? e * (t - z * a.it) : 0.0f);
@@ -939,7 +959,7 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
                     const float wm = warp_max(tm), f = rescale(tm, part_ref(wm), kLog2e);
                     ts = warp_sum(ts * f);
                     td = warp_sum(f != 0.0f ? td * f : 0.0f);
-                    bad = warp_sum(bad);
+                    const float bad = __any_sync(~0u, beyond) ? kNaN : 0.0f;
                     if (lane == 0) tparts[par][warp] = make_float4(wm, ts, td, bad);
                 }
                 if (cluster > 1) {
@@ -947,7 +967,14 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
                     cluster_arrive_relaxed();
                     exchanged = true;
                 }
-                bar_arrive(1 + par, B + 32);
+                if (kTeach && again) {
+                    // pass B of this row waits for its factors anyway: meanwhile the row before,
+                    // of which every warp has stored its part
+                    bar_sync(1 + par, B + 32);
+                    if (listed >= 0) relist();
+                } else {
+                    bar_arrive(1 + par, B + 32);
+                }
             }
             if (again && live) {   // not kept waiting: two rows under way would not fit L2
                 back_row = r;
