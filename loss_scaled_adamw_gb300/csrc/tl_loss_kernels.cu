@@ -31,26 +31,54 @@ __device__ __forceinline__ float ex2(float v) {
     return r;
 }
 
-// Exponents.  exp((x - m) it) is 2^(x c2 - m c2) with c2 = it log2(e): one multiply-add
-// per element once u = m c2 is rounded, and that rounding cancels, since every later use
-// (joining parts, log S, q) takes the same u.  Where u could overflow (|m| from 2^120 on:
-// logits at a type's lowest or highest values) the difference is taken first.
-constexpr float kBig = 1.329227995784916e36f;   // 2^120
-__device__ __forceinline__ bool big(float m) { return !(fabsf(m) < kBig); }
+// Exponents.  With c2 = it log2(e) an element's exponential is taken as 2^(x c2 - u), u the
+// whole number next to m c2 of the largest element m: one multiply-add, and sums over parts
+// with other u join by exact powers of two.  From |m c2| = 2^24 on (u would not be exact;
+// logits at a type's lowest value, masks of -1e9) it is 2^((x - m) c2) instead.  (At
+// temperature 1, for the cross-entropy, the exponent is x log2(e).)
+__device__ __forceinline__ bool big(float m, float c2) { return !(fabsf(m) * fmaxf(c2, kLog2e) < 16777216.0f); }
+__device__ __forceinline__ float anchor(float m, float c2) { return rintf(m * c2); }
 
-// A part of a row (a thread's or a warp's elements) has its largest element m and its sum
-// s of 2^((x - m) c2).  A part without an element above -inf takes 0 in the place of m, so
-// its s is 0 (NaN if it holds a NaN), and parts join without -inf - -inf.
+// 2^n for a whole n <= 0.
+__device__ __forceinline__ float power_of_two(float n) { return __int_as_float((int(fmaxf(n, -127.0f)) + 127) << 23); }
+
+// A part of a row (a thread's or a warp's elements) has its largest element m and its sum s
+// of exponentials.  A part without an element above -inf takes 0 in the place of m, so its s
+// is 0 (NaN if it holds a NaN), and parts join without -inf - -inf.
 __device__ __forceinline__ float part_ref(float m) { return m == kNegInf ? 0.0f : m; }
-// 2^((x - m) c2)
+// The exponential of x in a part whose largest element is m.
 __device__ __forceinline__ float power(float x, float m, float c2) {
-    return ex2(big(m) ? (x - m) * c2 : __fmaf_rn(x, c2, -(m * c2)));
+    return ex2(big(m, c2) ? (x - m) * c2 : __fmaf_rn(x, c2, -anchor(m, c2)));
 }
 // What brings a part's sum from its largest element m to the joined one.
 __device__ __forceinline__ float rescale(float m, float to, float c2) {
     if (m == kNegInf) return 1.0f;   // an empty part's 0 (or NaN) stays
-    return ex2(big(to) ? (m - to) * c2 : m * c2 - to * c2);
+    if (!big(to, c2) && !big(m, c2)) return power_of_two(anchor(m, c2) - anchor(to, c2));
+    if (!big(to, c2)) return ex2(__fmaf_rn(m, c2, -anchor(to, c2)));   // from 2^((x - m) c2)
+    // to 2^((x - to) c2)
+    return ex2((m - to) * c2 - (big(m, c2) ? 0.0f : __fmaf_rn(m, c2, -anchor(m, c2))));
 }
+
+// The hardware's exponential is low by 5.05e-8 relative in the mean (measured over [-20, 0]),
+// which a sum over a row keeps and a sum of log-probabilities over a sequence adds up:
+// log2 of a sum of them is raised by this much.
+constexpr float kEx2Low = 7.3e-8f;
+
+// log2 of s exponentials' sum as a whole part and the rest, so that neither is rounded to the
+// size of the whole.
+__device__ __forceinline__ void log2_parts(float s, float& n, float& rest) {
+    const int e = (__float_as_int(s) >> 23) - 127;
+    const bool usual = s > 1e-30f && s < 1e30f;
+    n = usual ? float(e) : 0.0f;
+    rest = log2f(usual ? __int_as_float(__float_as_int(s) - (e << 23)) : s) + kEx2Low;
+}
+// log(exponential of x / s) in a part whose largest element is m; x's scale is c.
+__device__ __forceinline__ float log_share(float x, float m, float u, float c, bool far, float s) {
+    float n, rest;
+    log2_parts(s, n, rest);
+    return ((far ? (x - m) * c - n : __fmaf_rn(x, c, -(u + n))) - rest) * kLn2;
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
@@ -394,17 +422,22 @@ template <int POW> __device__ __forceinline__ float mix(float e, float x, float 
     if (POW == 2) return e * __fmaf_rn(e, cq, kq);
     return __fmaf_rn(untempered<POW>(e, x, v), cq, e * kq);
 }
-// The exponent's reference at temperature 1 for a largest element m, u = m c2.
+// The exponent's reference at temperature 1 for a largest element m, u = anchor(m, c2).
 template <int POW> __device__ __forceinline__ float untempered_ref(float m, float u) {
-    return POW == 0 ? m * kLog2e : u * float(POW);
+    return POW == 0 ? anchor(m, kLog2e) : u * float(POW);
 }
 template <int POW> __device__ __forceinline__ float rescale1(float m, float to, float c2) {
     if (m == kNegInf) return 1.0f;
-    return ex2(big(to) ? (m - to) * kLog2e : untempered_ref<POW>(m, m * c2) - untempered_ref<POW>(to, to * c2));
+    const float ref = untempered_ref<POW>(m, anchor(m, c2));
+    if (!big(to, c2)) {
+        const float end = untempered_ref<POW>(to, anchor(to, c2));
+        return big(m, c2) ? ex2(__fmaf_rn(m, kLog2e, -end)) : power_of_two(ref - end);
+    }
+    return ex2((m - to) * kLog2e - (big(m, c2) ? 0.0f : __fmaf_rn(m, kLog2e, -ref)));
 }
 // The same two exponentials of one element where m may be big.
 template <int POW> __device__ __forceinline__ float power1(float e, float x, float m, float c2) {
-    return big(m) ? ex2((x - m) * kLog2e) : untempered<POW>(e, x, untempered_ref<POW>(m, m * c2));
+    return big(m, c2) ? ex2((x - m) * kLog2e) : untempered<POW>(e, x, untempered_ref<POW>(m, anchor(m, c2)));
 }
 
 __device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
@@ -433,13 +466,21 @@ struct RowShape {
 // B threads work on the elements, in two passes over a row: A keeps each thread's running
 // maximum and sum, B writes the gradient.  One more warp has the statistics: it joins the
 // warps' parts, exchanges the CTAs' parts through distributed shared memory, and works
-// out the row's loss and gradient factors.  That takes about as long as a share, so pass B
-// of a row comes after pass A of the next one, and the element warps wait for nobody.
-// (Without the extra warp, and pass B right after A: 341 to 408 us for 4,096 x 128,256 bf16
-// policy rows, a third of the warps' time at barriers.)
+// out the row's loss and gradient factors (by all warps they cost as many instructions as
+// the elements).
 //
-// A share of at most one tile stays in shared memory between its passes, so the row is
-// read once; longer ones are streamed a second time, out of L2 (see shape_for).
+// A share of at most one tile stays in shared memory between its passes (kept): the row is
+// read once, and its pass B comes after pass A of the next row, so that the element warps
+// do not wait for the factors.  Longer shares are streamed a second time, out of L2 (see
+// shape_for), and their pass B comes at once: with two rows under way per group the second
+// read misses L2 (2,432 rows of 50,000: 63 % of the copy rate, one at a time 79 %).
+//
+// What bounds it: the longest rows, memory (4,096 x 128,256 bf16, one in eight ignored:
+// log-probabilities 133 us, 6.9 TB/s; policy 321 us, 6.1 TB/s, 92 % of the copy rate);
+// rows below about 10,000 entries, the chain from a row's last element to its factors, with
+// 16 instructions per element in the passes.  Ring and grid: three tiles of 32 KB per CTA of
+// 256 threads, two CTAs per SM, measured against 4 and 16 vectors per thread, two and four
+// tiles, three CTAs per SM, 64 to 512 threads, and groups of 1 to 8 CTAs.
 // POW: distillation with both terms at temperatures that differ, two sums per row (DUAL).
 template <typename T, int OP, int B, int POW>
 __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row(const LossArgs a, const int clog) {
@@ -450,12 +491,11 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
     __shared__ float4 wparts[2][nw];                // by row parity, per warp: m, s, s at temperature 1
     __shared__ float4 tparts[2][kTeach ? nw : 1];   // teacher: m, sum e, sum e (t - z), bad
     __shared__ float4 cparts[2][kMaxCluster];       // per CTA of the group
-    // Of four rows in turn: while a row is in pass A, its successor's factors may be worked
-    // out, its predecessor is in pass B and the one before that has its listed elements
-    // written; a warp may be a row ahead of another.
+    // Of four rows in turn: while a row is in pass A its predecessor is in pass B and the one
+    // before that has its listed elements written, and a warp may be a row ahead of another.
     __shared__ float4 fac[4][2];                    // gradient factors
     // [ST][tile] vectors; then [4][3][kpad] of id, t / tau, x.  A copy of a warp into memory off a
-    // 128-byte boundary takes twice the requests: policy 341 or 408 us by what else was declared.
+    // 128-byte boundary takes twice the requests (4,096 x 128,256 bf16 policy: 361 us, on it 326).
     extern __shared__ __align__(128) uint4 ring[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cluster = 1 << clog, rank = cluster > 1 ? int(cluster_rank()) : 0;
@@ -538,9 +578,9 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
                 teacher();
             }
             float bad = y >= a.vocab || M == kNegInf ? kNaN : 0.0f;
-            const float lg = log2f(S);
-            const float gap = big(M) ? (xy - M) * c2 : __fmaf_rn(xy, c2, -(M * c2));   // log2 of the label's exponential
-            const float lp = (gap - lg) * kLn2 + bad;
+            const bool far = big(M, c2);
+            const float u = anchor(M, c2);
+            const float lp = log_share(xy, M, u, c2, far, S) + bad;
             if (OP == kLogprob || OP == kPrefStat) {
                 bar_arrive(3 + par, B + 32);   // nothing for pass B
                 if (out && a.logp) a.logp[r] = lp;
@@ -550,7 +590,7 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
                 const float w = policy_row(a, lp, old, adv, refl, loss, sur, kl) * step * a.it;
                 // the label's element: w (1 - q)
                 const float kq = -w / S;
-                if (lane == 0) fac[buf4][0] = make_float4(M + bad, kq, 0.0f, __fmaf_rn(ex2(gap), kq, w));
+                if (lane == 0) fac[buf4][0] = make_float4(M + bad, kq, 0.0f, __fmaf_rn(power(xy, M, c2), kq, w));
                 bar_arrive(3 + par, B + 32);
                 if (out) {
                     if (a.logp) a.logp[r] = lp;
@@ -571,19 +611,24 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
                 if (ce_on && grad) {
                     const float* const tb = teach + buf4 * 3 * kpad;
                     for (int i = lane; i < (wp != 0.0f ? a.k : 0); i += 32)
-                        if (__float_as_int(tb[i]) == int(y)) at_label = __fmaf_rn(wp, ex2((tb[kpad + i] - tm) * kLog2e), at_label);
+                        if (__float_as_int(tb[i]) == int(y)) at_label = __fmaf_rn(wp, power(tb[kpad + i], part_ref(tm), kLog2e), at_label);
                     at_label = dense_value(xy, M + bad, kq0, cq) - (warp_sum(at_label) + wc);
                 }
                 if (lane == 0) {
                     fac[buf4][0] = make_float4(M + bad, kq0, cq, at_label);
-                    fac[buf4][1] = make_float4(wp, tm, 0.0f, 0.0f);
+                    fac[buf4][1] = make_float4(wp, tm, anchor(tm, kLog2e), 0.0f);
                 }
                 bar_arrive(3 + par, B + 32);
-                const float lz = big(M) ? __fmaf_rn(M, a.it, lg * kLn2) : (M * c2 + lg) * kLn2;   // log sum exp z
-                const float kd = row_kd ? (td / ts - tm - logf(ts) + lz) / (a.it * a.it) + bad : bad;
-                float log_sum1 = 0.0f;   // log sum exp x
-                if (DUAL) log_sum1 = big(M) ? M + logf(S1) : (untempered_ref<POW>(M, M * c2) + log2f(S1)) * kLn2;
-                const float ce = ce_on ? (DUAL ? log_sum1 - xy : -lp) + bad : 0.0f;
+                // kd = sum p (t - z) - log sum exp t + log sum exp z
+                const float lse_z = far ? M * a.it - log_share(M, M, u, c2, far, S) : -log_share(0.0f, M, u, c2, far, S);
+                const bool tfar = big(tm, kLog2e);
+                const float lse_t = tfar ? tm - log_share(tm, tm, 0.0f, kLog2e, tfar, ts)
+                                         : -log_share(0.0f, tm, anchor(tm, kLog2e), kLog2e, tfar, ts);
+                const float kd = row_kd ? (td / ts - lse_t + lse_z) / (a.it * a.it) + bad : bad;
+                const float ce = !ce_on ? 0.0f
+                                 : DUAL ? kLn2 * kEx2Low * float(POW < 2 ? 0 : POW - 1) + bad -
+                                              log_share(xy, M, untempered_ref<POW>(M, u), kLog2e, far, S1)
+                                        : bad - lp;
                 const float loss = (row_kd ? a.kd_weight * kd : bad) + (ce_on ? a.ce_weight * ce : 0.0f);
                 if (out) {
                     if (a.loss) a.loss[r] = loss;
@@ -688,9 +733,13 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
         int listed_buf = 0;
         auto relist = [&]() {
             const float4 fc = fac[listed_buf][0], f1 = fac[listed_buf][1];
-            const float Mb = fc.x, kq = fc.y, cq = fc.z, tm = f1.y, wp = f1.x;
-            const int n = wp != 0.0f ? a.k : 0;
             const float* const tb = teach + listed_buf * 3 * kpad;
+            const float Mb = fc.x, kq = fc.y, cq = fc.z, tm = f1.y, tu = f1.z, wp = f1.x;
+            const bool tfar = big(tm, kLog2e);
+            auto share = [&](int j) {   // the teacher's exponential of entry j
+                return ex2(tfar ? (tb[kpad + j] - tm) * kLog2e : __fmaf_rn(tb[kpad + j], kLog2e, -tu));
+            };
+            const int n = wp != 0.0f ? a.k : 0;
             const int* const ids = reinterpret_cast<const int*>(tb);
             const Place<T> pl = place_of(row_at(listed));
             T* const dx = static_cast<T*>(a.dx) + listed * a.ldd;
@@ -714,12 +763,12 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
                 float w = 0.0f;
                 bool lead = true;
                 if (same == 1) {
-                    w = wp * ex2((tb[kpad + i] - tm) * kLog2e);
+                    w = wp * share(i);
                 } else {
                     for (int j = 0; j < n; ++j) {
                         if (ids[j] != id) continue;
                         lead = lead && j >= i;
-                        w = __fmaf_rn(wp, ex2((tb[kpad + j] - tm) * kLog2e), w);
+                        w = __fmaf_rn(wp, share(j), w);
                     }
                 }
                 if (lead) dx[id] = from_f<T>(dense_value(tb[2 * kpad + i], Mb, kq, cq) - w);
@@ -740,7 +789,7 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
             const bool edge = rank == 0 && tid < pl.edges;
             const float4 fc = fac[buffer][0];
             const float Mb = fc.x, kq = fc.y, cq = OP == kDistill ? fc.z : 0.0f;
-            const float u = Mb * c2, v1 = DUAL ? untempered_ref<POW>(Mb, u) : 0.0f;
+            const float u = anchor(Mb, c2), v1 = DUAL ? untempered_ref<POW>(Mb, u) : 0.0f;
             auto dense = [&](float x) { return dense_value(x, Mb, kq, cq); };
             for (int done = 0; hi > lo && done < hi - lo + pl.off; done += tile) {
                 if (!kept) take_tile();
@@ -748,7 +797,7 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
                 const int mine = hi - lo + pl.off - done - tid;   // vector i of the thread exists where B i < mine
                 const bool none = done == 0 && tid < pl.off;      // but for its first one here
                 T* const to = dx + pl.head + (lo + done + tid - pl.off) * N;
-                if (big(Mb)) {   // NaN rows too
+                if (big(Mb, c2)) {   // NaN rows too
 #pragma unroll 1
                     for (int i = none ? 1 : 0; i < kTileVecs && B * i < mine; ++i)
 #pragma unroll 1
@@ -906,12 +955,12 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
 #pragma unroll
                         for (int i = 0; i < U; ++i) top = fmaxf(top, Vec<T>::top(raw[i]));
                         raise(top);
-                        if (big(part_ref(m))) {
+                        if (big(part_ref(m), c2)) {
 #pragma unroll 1
                             for (int i = 0; i < U; ++i)
                                 if (B * (g + i) < mine) add_big(buf + B * (g + i));
                         } else {
-                            const float u = part_ref(m) * c2, u1 = DUAL ? untempered_ref<POW>(part_ref(m), u) : 0.0f;
+                            const float u = anchor(part_ref(m), c2), u1 = DUAL ? untempered_ref<POW>(part_ref(m), u) : 0.0f;
 #pragma unroll
                             for (int i = 0; i < U; ++i) add(raw[i], u, u1);
                         }
@@ -942,8 +991,8 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
                     bool beyond = tid < a.k && id0 >= a.vocab;
                     if (tid < a.k) {
                         entry(tid, id0, t0, z0, tm);
-                        ts = tm > kNegInf || tm != tm ? 1.0f : 0.0f;   // exp(t - t)
-                        td = ts != 0.0f ? tm - z0 * a.it : 0.0f;
+                        ts = tm == kNegInf ? 0.0f : power(tm, tm, kLog2e);
+                        td = ts != 0.0f ? ts * (tm - z0 * a.it) : 0.0f;
                     }
                     for (int j = tid + B; j < a.k; j += B) {
                         const int64_t id = teacher_id(a, r * a.ldt + j);
@@ -1004,8 +1053,9 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
     if (OP == kPrefStat && rank == 0) finish_pairs<B>(a, ngroups);
 }
 
-// Second preference pass: every element from its row's statistics, one segment of a row
-// per CTA, the last rows first (the first pass left them in L2).  It is launched to start
+// Second preference pass: every element from its row's statistics (the pair's derivative
+// needs whole sequences first), one segment of a row per CTA, the last rows first (the first
+// pass left them in L2).  4,096 x 128,256 bf16, a quarter ignored: 255 us for 1.84 GB.  It is launched to start
 // while the first pass runs: its CTAs read their part of the logits, and wait for that
 // kernel's end before they use the statistics.
 template <typename T, int NV>
@@ -1060,14 +1110,14 @@ __global__ void __launch_bounds__(256) k_pref_grad(const LossArgs a, const int s
         zeros();
         return;
     }
-    const float c2 = a.it * kLog2e, kq = -st.w * st.rs, u = st.m * c2;
+    const float c2 = a.it * kLog2e, kq = -st.w * st.rs, u = anchor(st.m, c2);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int v = lo + i * 256 + tid;
         if (v >= 0 && v < hi) {
             float f[N];
             Vec<T>::wide(raw[i], f);
-            if (big(st.m)) {
+            if (big(st.m, c2)) {
                 for (int j = 0; j < N; ++j) f[j] = ex2((f[j] - st.m) * c2) * kq;
             } else {
 #pragma unroll
@@ -1091,10 +1141,13 @@ RowShape shape_for(int op, int64_t rows, int vocab, bool grad, int sms) {
     // 56 / 70 / 58 at 32,768, 58 / 61 / 74 at 80,000.
     if (vecs >= 512) s.threads = vecs > (op == kPolicy && grad ? 3500 : 8192) ? 256 : 128;
     // Long rows are read twice, the second time out of L2 if what is under way (two CTAs per
-    // SM) fits it: more CTAs to a row where it would not, and then one row at a time.
+    // SM) fits it: more CTAs to a row where it would not.
     const int64_t under_way = int64_t(2) * sms * vocab * int(sizeof(T));
-    if (grad && s.threads == 256)
+    if (grad && s.threads == 256) {
+        // 1,824 rows of 80,000 (49 MB): 75 % of the copy rate with 1 CTA per row, 76 with 2;
+        // 1,216 of 128,256 (78 MB): 67 with 1, 85 with 2; 2,432 of 50,000 (30 MB): 79 with 1, 58 with 2
         while (s.clog < kMaxClusterLog && under_way >> s.clog > kRowsInL2) s.clog += 1;
+    }
     // few rows: spread each over more CTAs while the GPU has idle SMs and the share is over a tile
     while (s.clog < kMaxClusterLog && rows << (s.clog + 1) <= sms && (s.threads * kTileVecs) << s.clog < vecs) s.clog += 1;
     return s;

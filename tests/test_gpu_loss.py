@@ -15,7 +15,8 @@ Tolerances, derived from the arithmetic (eps = 2^-24, the unit roundoff of fp32)
 * distill: a mean over p of logits' differences: REL plus 8 eps of the largest magnitude
   entering it, times tau^2.
 * a gradient w (1[j = y] - q_j): |w| (rel(w) + 2 REL) q, plus |w| (rel(w) + 2 REL) at
-  listed entries, rounded once to the type (half an ulp; fp16 subnormals 2^-25).
+  listed entries, rounded once to the type (half an ulp; fp16 subnormals 2^-25).  An
+  exponential below 2^-126 is taken as 0: |w| 2^-126.
 """
 import math
 
@@ -91,7 +92,7 @@ def check_dx(got, want, dtype, w, rel_w, entries, what):
     """w: bound of |w| per row; rel_w: its relative error; entries: bool [T, V], listed positions."""
     band = (w * (rel_w + 2 * REL))[:, None]
     tol = (2 * REL + rel_w)[:, None] * want.abs() + band * entries.double()
-    tol = tol + (want.abs() + tol) * HALF_ULP[dtype] + TINY[dtype]
+    tol = tol + (want.abs() + tol) * HALF_ULP[dtype] + TINY[dtype] + (w * 2.0 ** -126)[:, None]
     close(got.float(), want, torch.nan_to_num(tol, nan=0.0, posinf=0.0), what)
 
 
@@ -233,6 +234,37 @@ def test_rows_with_masks_and_non_finite_logits(lctx, V, dtype):
     lp_gpu = lp.cuda()
     tl.tl_token_logprob(lctx, x.cuda(), y.cuda(), lp_gpu)
     assert float(lp_gpu[1]) == -INF and float(lp_gpu[8]) == 0.0
+
+
+@pytest.mark.parametrize("tau", [1.0, 0.1, 2.0, 1e-4, 1e30])
+@pytest.mark.parametrize("V", [300, 9000, 70000])
+def test_logits_of_any_magnitude(lctx, V, tau):
+    """Logits far from zero (a common offset, finite masks of -1e9 and the like, in part of a
+    row and all over it), and temperatures far from 1: only differences count.  The offsets
+    are multiples of what keeps x itself exact; each fp32 difference is then exact too."""
+    g, x, y = make(8, V, "f32", 20, masked=0.0)
+    x = (x * 64).round() / 64                                   # 1/64 steps: exact below 2^18
+    for t, off in enumerate([0.0, 1e3, -3e4, 7.2e5 / 4, -2.0 ** 17, 0.0, 0.0, 0.0]):
+        x[t] += off
+    x[5, : V // 2] = -1e9
+    x[6] = -1e9
+    x[6, 3:6] = torch.tensor([-1e9 + 128, -1e9 + 64, -1e9])    # spacing of fp32 there
+    x[7] = -1e30
+    y[5], y[6] = V - 1, 3
+    lp = R.logprob(x, y, tau)
+    old, adv = torch.where(torch.isfinite(lp), lp, 0.0).float(), torch.ones(8)
+    got = run_policy(lctx, x, y, old, adv, 8, tau=tau, seed=4.0)
+    want = R.policy(x, y, old, adv, 8, tau=tau, seed=4.0)
+    check_policy(got, want, x, y, old, adv, 8, "f32", tau, 4.0, 0.0, None)
+    teacher, ids = teacher_of(8, V, 6, g)
+    if tau in (0.1, 1.0, 2.0):
+        got = run_distill(lctx, x, teacher, ids, 8, y, 0.5, 0.5, tau, 1.0)
+        want = R.distill(x, teacher, ids, 8, y, 0.5, 0.5, tau, 1.0)
+        listed = hot(y, V)
+        for t in range(8):
+            listed[t, ids[t].long()] = True
+        w = torch.full((8,), (0.5 * tau + 0.5) / 8, dtype=torch.float64)
+        check_dx(got["dx"], want["dx"], "f32", w, torch.full((8,), 2 * REL + 64 * EPS, dtype=torch.float64), listed, "dx")
 
 
 def test_all_rows_ignored_give_zeros(lctx):
@@ -600,3 +632,19 @@ def test_refusals_launch_nothing(lctx):
     both = torch.randn(T, 2 * V, device="cuda")
     tl.tl_policy_loss(lctx, both[:, :V], y, old, g, 4, res, dlogits=both[:, V:])
     torch.cuda.synchronize()
+
+
+def test_example_trains_with_every_objective(lctx):
+    """The example end to end: the objectives' gradients, scaled on the device, through the
+    optimizer step.  Each loss falls and no update is lost to an overflow that sticks."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "post_training.py")
+    spec = importlib.util.spec_from_file_location("post_training", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    for name in ("distill", "preference", "policy"):
+        losses, status = example.train(name, 30, lctx)
+        assert all(math.isfinite(v) for v in losses), name
+        assert losses[-1] < losses[0], name
+        assert status.t >= 25 and status.found_inf == 0, name
