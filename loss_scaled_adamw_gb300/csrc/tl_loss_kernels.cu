@@ -32,7 +32,7 @@ __device__ __forceinline__ float ex2(float v) {
 }
 
 // Exponents.  With c2 = it log2(e) an element's exponential is taken as 2^(x c2 - u), u the
-// whole number next to m c2 of the largest element m: one multiply-add, and sums over parts
+// whole number next to m c2 of the largest element m (or one near it): one multiply-add, and sums over parts
 // with other u join by exact powers of two.  From |m c2| = 2^24 on (u would not be exact;
 // logits at a type's lowest value, masks of -1e9) it is 2^((x - m) c2) instead.  (At
 // temperature 1, for the cross-entropy, the exponent is x log2(e).)
@@ -59,20 +59,16 @@ __device__ __forceinline__ float rescale(float m, float to, float c2) {
     return ex2((m - to) * c2 - (big(m, c2) ? 0.0f : __fmaf_rn(m, c2, -anchor(m, c2))));
 }
 
-// The hardware's exponential is low by 5.05e-8 relative in the mean (measured over [-20, 0]),
-// which a sum over a row keeps and a sum of log-probabilities over a sequence adds up:
-// log2 of a sum of them is raised by this much.
-constexpr float kEx2Low = 7.3e-8f;
-
 // log2 of s exponentials' sum as a whole part and the rest, so that neither is rounded to the
 // size of the whole.
 __device__ __forceinline__ void log2_parts(float s, float& n, float& rest) {
     const int e = (__float_as_int(s) >> 23) - 127;
     const bool usual = s > 1e-30f && s < 1e30f;
     n = usual ? float(e) : 0.0f;
-    rest = log2f(usual ? __int_as_float(__float_as_int(s) - (e << 23)) : s) + kEx2Low;
+    rest = log2f(usual ? __int_as_float(__float_as_int(s) - (e << 23)) : s);
 }
-// log(exponential of x / s) in a part whose largest element is m; x's scale is c.
+// log(exponential of x / s) in a part whose largest element is m, with anchor u; c: the scale
+// of x times log2(e).
 __device__ __forceinline__ float log_share(float x, float m, float u, float c, bool far, float s) {
     float n, rest;
     log2_parts(s, n, rest);
@@ -476,7 +472,7 @@ struct RowShape {
 // read misses L2 (2,432 rows of 50,000: 63 % of the copy rate, one at a time 79 %).
 //
 // What bounds it: the longest rows, memory (4,096 x 128,256 bf16, one in eight ignored:
-// log-probabilities 133 us, 6.9 TB/s; policy 321 us, 6.1 TB/s, 92 % of the copy rate);
+// log-probabilities 131 us, 7.0 TB/s; policy 321 us, 6.1 TB/s, 92 % of the copy rate);
 // rows below about 10,000 entries, the chain from a row's last element to its factors, with
 // 16 instructions per element in the passes.  Ring and grid: three tiles of 32 KB per CTA of
 // 256 threads, two CTAs per SM, measured against 4 and 16 vectors per thread, two and four
@@ -626,8 +622,7 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
                                          : -log_share(0.0f, tm, anchor(tm, kLog2e), kLog2e, tfar, ts);
                 const float kd = row_kd ? (td / ts - lse_t + lse_z) / (a.it * a.it) + bad : bad;
                 const float ce = !ce_on ? 0.0f
-                                 : DUAL ? kLn2 * kEx2Low * float(POW < 2 ? 0 : POW - 1) + bad -
-                                              log_share(xy, M, untempered_ref<POW>(M, u), kLog2e, far, S1)
+                                 : DUAL ? bad - log_share(xy, M, untempered_ref<POW>(M, u), kLog2e, far, S1)
                                         : bad - lp;
                 const float loss = (row_kd ? a.kd_weight * kd : bad) + (ce_on ? a.ce_weight * ce : 0.0f);
                 if (out) {
@@ -901,10 +896,12 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
                     if (tid < a.k && id0 >= 0 && id0 < a.vocab) z0 = to_f(x[id0]);
                     ask_teacher(r + ngroups);
                 }
-                // pass A: the thread's largest element and its sums, U vectors at a time
+                // pass A: the thread's reference (its largest element so far, or near it) and its sums, U
+                // vectors at a time
                 float m = kNegInf, acc[2] = {0.0f, 0.0f}, acc1[2] = {0.0f, 0.0f};
-                auto raise = [&](float top) {   // the sums so far to a larger element
-                    if (top == m) return;
+                auto raise = [&](float top) {   // the sums so far to a much larger element
+                    // smaller steps are left: m is a reference, and exponentials up to 2^32 of it do no harm
+                    if (!((top - m) * (DUAL ? fmaxf(c2, kLog2e) : c2) > 32.0f)) return;
                     const float f = rescale(m, top, c2);
                     acc[0] *= f;
                     acc[1] *= f;
