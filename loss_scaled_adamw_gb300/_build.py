@@ -58,7 +58,10 @@ def _run(cmd, verbose: bool, what: str) -> None:
 
 
 def _build_binding(verbose: bool) -> None:
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return   # the optimizer step's binding does without torch; losses.py says what is missing
+    torch = os.path.dirname(spec.origin)
     tmp = BIND + f".tmp{os.getpid()}"
     _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-I" + sysconfig.get_path("include"),
           "-isystem", os.path.join(torch, "include"),

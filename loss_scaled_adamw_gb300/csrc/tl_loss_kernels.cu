@@ -165,12 +165,12 @@ template <int B> __device__ __forceinline__ void write_sums(const LossArgs& a, d
 
 template <int B> __device__ void pair_stage(const LossArgs& a);
 
-// The preference's first pass: called by every thread of a group's first CTA, whose thread B
-// (the statistics warp's first lane) has written the rows' statistics.
-template <int B> __device__ void finish_pairs(const LossArgs& a, int ngroups) {
+// The preference's first pass: called by every thread of a group's first CTA; the rows'
+// statistics are written.  Thread TAKER takes the group's ticket.
+template <int B, int TAKER> __device__ void finish_pairs(const LossArgs& a, int ngroups) {
     __shared__ bool last;
     __syncthreads();
-    if (threadIdx.x == B) last = last_group(a, ngroups);
+    if (threadIdx.x == TAKER) last = last_group(a, ngroups);
     __syncthreads();
     if (last && threadIdx.x < B) pair_stage<B>(a);
 }
@@ -1047,7 +1047,128 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
         if (exchanged) cluster_wait();
         copy_wait<0>();
     }
-    if (OP == kPrefStat && rank == 0) finish_pairs<B>(a, ngroups);
+    if (OP == kPrefStat && rank == 0) finish_pairs<B, B>(a, ngroups);
+}
+
+// The same as ex2, taken again: the compiler would keep every exponential of the first pass
+// in a register instead (116 to 255 of them).
+__device__ __forceinline__ float ex2_again(float v) {
+    float r;
+    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// Many short rows: a warp per row, the row in its registers (NV vectors per lane), no barrier
+// at all.  What bounds it: instructions, about 300 for a row besides 11 per element.
+// 16,384 x 1,000 bf16 policy: @@SHORT@@
+template <typename T, int OP, int NV>
+__global__ void __launch_bounds__(256, NV > 8 ? 2 : 4) k_short(const LossArgs a) {
+    constexpr int N = Vec<T>::N;
+    constexpr bool kGrad = OP == kPolicy;
+    if (OP == kPrefStat) asm volatile("griddepcontrol.launch_dependents;");   // the gradient's kernel, see there
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t warps = int64_t(gridDim.x) * 8;
+    const float c2 = a.it * kLog2e, kNaN = __int_as_float(0x7fffffff);
+    const float step = (kGrad && a.seed ? *a.seed : 1.0f) * a.inv_n;
+    LossSums sum;
+    const int64_t start = int64_t(blockIdx.x) * 8 + warp;
+    int64_t ynext = start < a.rows ? a.target[start] : 0;
+    for (int64_t r = start; r < a.rows; r += warps) {
+        const int64_t y = ynext;
+        if (r + warps < a.rows) ynext = a.target[r + warps];
+        const T* const x = static_cast<const T*>(a.x) + r * a.ld;
+        T* const dx = kGrad && a.dx ? static_cast<T*>(a.dx) + r * a.ldd : nullptr;
+        const Place<T> pl(x, a.vocab, 0, 0);
+        const bool whole = kGrad && same_phase(x, static_cast<const T*>(dx)), edge = lane < pl.edges;
+        const T* const body = x + pl.head;
+        if (y < 0) {
+            if (dx) {
+                for (int v = lane; v < pl.body; v += 32) store_vec<T>(dx + pl.head + v * N, make_uint4(0, 0, 0, 0), whole);
+                if (edge) dx[pl.edge_at(lane)] = from_f<T>(0.0f);
+            }
+            if (lane == 0) {
+                if (a.logp) a.logp[r] = 0.0f;
+                if (kGrad && a.loss) a.loss[r] = 0.0f;
+                if (OP == kPrefStat) a.stat[r] = {0.0f, 0.0f, 0.0f, 0.0f};
+            }
+            continue;
+        }
+        uint4 raw[NV];
+        float m = kNegInf;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v = i * 32 + lane - pl.off;
+            raw[i] = make_uint4(Vec<T>::kEmpty, Vec<T>::kEmpty, Vec<T>::kEmpty, Vec<T>::kEmpty);
+            if (v >= 0 && v < pl.body) raw[i] = ld16(body + v * N);
+        }
+        const float xe = edge ? to_f(x[pl.edge_at(lane)]) : kNegInf, xy = to_f(x[y < a.vocab ? y : 0]);
+        float old = 0.0f, adv = 0.0f, refl = 0.0f;
+        if (OP == kPolicy) {
+            old = a.old_logp[r];
+            adv = a.adv[r];
+        }
+        if (OP != kLogprob) refl = a.ref_logp ? a.ref_logp[r] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) m = fmaxf(m, Vec<T>::top(raw[i]));
+        m = warp_max(fmaxf(m, xe));
+        // 2^(x c2 - u), or 2^((x - m) c2) of a big m
+        const bool far = big(part_ref(m), c2);
+        const float u = anchor(part_ref(m), c2), base = far ? m : 0.0f, off = far ? 0.0f : u;
+        float acc[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float f[N];
+            Vec<T>::wide(raw[i], f);
+#pragma unroll
+            for (int j = 0; j < N; ++j) acc[j & 1] += ex2(__fmaf_rn(f[j] - base, c2, -off));
+        }
+        const float S = warp_sum(acc[0] + acc[1] + ex2(__fmaf_rn(xe - base, c2, -off)));
+        const float bad = y >= a.vocab || m == kNegInf ? kNaN : 0.0f;
+        const float lp = log_share(xy, m, u, c2, far, S) + bad;
+        if (lane == 0 && a.logp) a.logp[r] = lp;
+        if (OP == kPrefStat && lane == 0) a.stat[r] = {m + bad, 1.0f / S, 0.0f, lp - refl};
+        if (OP != kPolicy) continue;
+        float loss, sur, kl;
+        const float w = policy_row(a, lp, old, adv, refl, loss, sur, kl) * step * a.it, kq = -w / S;
+        if (lane == 0) {
+            if (a.loss) a.loss[r] = loss;
+            sum.loss += loss; sum.first += sur; sum.second += kl; sum.count += 1.0;
+        }
+        if (!dx) continue;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v = i * 32 + lane - pl.off;
+            if (v >= 0 && v < pl.body) {
+                float f[N];
+                Vec<T>::wide(raw[i], f);
+#pragma unroll
+                for (int j = 0; j < N; ++j) f[j] = ex2_again(__fmaf_rn(f[j] - base, c2, -off)) * kq;
+                store_vec<T>(dx + pl.head + v * N, Vec<T>::narrow(f), whole);
+            }
+        }
+        if (edge) dx[pl.edge_at(lane)] = from_f<T>(ex2(__fmaf_rn(xe - base, c2, -off)) * kq);
+        if (y < a.vocab) {   // the label's element again, by the lane that stored it
+            bool at_edge;
+            int v;
+            pl.owns(int(y), 0, at_edge, v);
+            if ((at_edge ? v : (v + pl.off) & 31) == lane)
+                dx[y] = from_f<T>(__fmaf_rn(ex2(__fmaf_rn(xy - base, c2, -off)), kq, w));
+        }
+    }
+    if (OP == kPrefStat) finish_pairs<256, 0>(a, int(gridDim.x));
+    if (OP == kPolicy) {
+        __shared__ LossSums sums[8];
+        if (lane == 0) sums[warp] = sum;
+        __syncthreads();
+        if (warp == 0) {
+            if (lane == 0)
+                for (int w = 1; w < 8; ++w) {
+                    sum.loss += sums[w].loss; sum.first += sums[w].first;
+                    sum.second += sums[w].second; sum.count += sums[w].count;
+                }
+            finish_sums(a, sum, int(blockIdx.x), int(gridDim.x));
+        }
+    }
 }
 
 // Second preference pass: every element from its row's statistics (the pair's derivative
@@ -1207,14 +1328,40 @@ cudaError_t rows_by_threads(const LossArgs& a, const RowShape& sh, int sms, Grou
     return row_launch<T, OP, 256, POW>(a, sh, sms, cache, s);
 }
 
+// Rows of up to 32 NV places, where there are enough of them for a warp each.
+constexpr int64_t kShortRows = 1024;
+
+template <typename T, int OP, int NV>
+cudaError_t short_launch(const LossArgs& a, int sms, GroupCache& cache, cudaStream_t s) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    auto* kernel = k_short<T, OP, NV>;
+    int groups = 0;
+    cudaError_t e = resident_groups(reinterpret_cast<const void*>(kernel), cfg, RowShape{256, 0}, sms, cache, groups);
+    if (e != cudaSuccess) return e;
+    const int64_t want = (a.rows + 7) / 8;
+    cfg.gridDim.x = unsigned(groups < want ? groups : want);
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+template <typename T, int OP>
+cudaError_t rows_by_length(const LossArgs& a, const RowShape& sh, int sms, GroupCache& cache, cudaStream_t s) {
+    const int places = (a.vocab + Vec<T>::N - 1) / Vec<T>::N + 7;
+    if (a.rows >= kShortRows && places <= 32 * 4) return short_launch<T, OP, 4>(a, sms, cache, s);
+    if (a.rows >= kShortRows && places <= 32 * 8) return short_launch<T, OP, 8>(a, sms, cache, s);
+    if (a.rows >= kShortRows && places <= 32 * 17) return short_launch<T, OP, 17>(a, sms, cache, s);
+    return rows_by_threads<T, OP>(a, sh, sms, cache, s);
+}
+
 template <typename T>
 cudaError_t rows_by_op(int op, const LossArgs& a, int sms, GroupCache& cache, cudaStream_t s) {
     const bool grad = a.dx != nullptr && (op == kPolicy || op == kDistill);
     const RowShape sh = shape_for<T>(op, a.rows, a.vocab, grad, sms);
     switch (op) {
-        case kLogprob: return rows_by_threads<T, kLogprob>(a, sh, sms, cache, s);
-        case kPolicy: return rows_by_threads<T, kPolicy>(a, sh, sms, cache, s);
-        case kPrefStat: return rows_by_threads<T, kPrefStat>(a, sh, sms, cache, s);
+        case kLogprob: return rows_by_length<T, kLogprob>(a, sh, sms, cache, s);
+        case kPolicy: return rows_by_length<T, kPolicy>(a, sh, sms, cache, s);
+        case kPrefStat: return rows_by_length<T, kPrefStat>(a, sh, sms, cache, s);
         default: break;
     }
     if (a.k == 0 || a.ce_weight == 0.0f || a.it == 1.0f) return rows_by_threads<T, kDistill>(a, sh, sms, cache, s);

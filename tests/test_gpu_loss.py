@@ -570,6 +570,39 @@ def test_results_repeat_bit_for_bit_and_in_a_graph_and_on_another_stream(lctx):
     assert all(torch.equal(2 * a, b) for a, b in zip(first[:3], outs))
 
 
+@pytest.mark.parametrize("V", [1, 7, 33, 257, 1000, 1025, 2040, 4096, 4290])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_many_rows(lctx, V, dtype):
+    """Over a thousand rows, where the short ones take a warp each: every operator that has
+    that form, at every row phase, masks and non-finite rows among them, in place and not."""
+    T = 1061
+    g, x, y = make(T, V, dtype, 21)
+    low = torch.finfo(DT[dtype]).min
+    x[3], y[3] = -INF, 0
+    x[4], y[4] = low, 0
+    x[5, V - 1], y[5] = NAN, 0
+    y[6] = V
+    x[7, 0], y[7] = INF, 0
+    x[8], y[8] = NAN, -1
+    good = torch.ones(T, dtype=torch.bool)
+    good[torch.tensor([3, 5, 6, 7])] = False
+    lp = R.logprob(x, y)
+    old = (torch.nan_to_num(lp, nan=0.0) + 0.2 * torch.randn(T, generator=g)).float()
+    adv, ref = torch.randn(T, generator=g), (torch.nan_to_num(lp, nan=0.0) + 0.3).float()
+    for kw in (dict(pad=3, lead=1), dict(in_place=True)):
+        got = run_policy(lctx, x, y, old, adv, 900, ref, 0.05, seed=64.0, **kw)
+        want = R.policy(x, y, old, adv, 900, ref, kl_weight=0.05, seed=64.0)
+        check_policy(got, want, x, y, old, adv, 900, dtype, 1.0, 64.0, 0.05, ref)
+    X, out = Rows(T, V, DT[dtype], 5, 2, x.cuda()), torch.full((T,), 9.0, device="cuda")
+    tl.tl_token_logprob(lctx, X.t, y.cuda(), out)
+    close(out, lp, lp_tol(lp), "logp")
+    # preference: the bad rows in a pair of their own
+    seq = [0, 4, 9, 100, 200, 500, 1061]
+    got = run_preference(lctx, x, y, seq, 3, ref, 0.02, 0.0, 1.0, 32.0, pad=1)
+    want = R.preference(x, y, seq, 3, ref, 0.02, 0.0, 1.0, 32.0)
+    check_preference(got, want, x, y, seq, 3, dtype, 0.02, 1.0, 32.0, ref)
+
+
 def test_offsets_beyond_32_bits(lctx):
     """Rows 2^29 elements apart: the last starts at element 2^32."""
     T, V, ld = 9, 1000, 1 << 29
