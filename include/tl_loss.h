@@ -47,7 +47,8 @@
  *
  * Calls are asynchronous on the given stream and never wait for the device
  * (tl_loss_create and tl_loss_destroy do).  They can be captured in a CUDA
- * graph.  A context is not thread-safe, and its calls must be ordered on the
+ * graph; make one call of each kind, with the sizes to be captured, before the
+ * capture, so that its kernel is loaded.  A context is not thread-safe, and its calls must be ordered on the
  * device (one stream, or events between streams), since they share its scratch.
  * Status codes are those of tl.h; a call that returns TL_EINVAL or TL_ESTATE
  * has launched nothing.

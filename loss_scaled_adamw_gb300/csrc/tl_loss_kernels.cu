@@ -1059,10 +1059,13 @@ __device__ __forceinline__ float ex2_again(float v) {
 }
 
 // Many short rows: a warp per row, the row in its registers (NV vectors per lane), no barrier
-// at all.  What bounds it: instructions, about 300 for a row besides 11 per element.
-// 16,384 x 1,000 bf16 policy: @@SHORT@@
+// at all.  What bounds it: instructions, about 300 for a row besides 11 per element, and the
+// latency of a row's loads with 16 to 24 warps per SM.  Share of the copy rate on 16,384 bf16
+// rows against k_row: policy 37 / 17 % at 1,000 entries, 39 / 25 at 2,001, 65 / 51 at 4,096;
+// log-probabilities 36 / 15, 40 / 25, 69 / 45.  Preference's statistics take it too;
+// distillation, whose entries want more lanes, does not.
 template <typename T, int OP, int NV>
-__global__ void __launch_bounds__(256, NV > 8 ? 2 : 4) k_short(const LossArgs a) {
+__global__ void __launch_bounds__(256, NV > 4 ? 2 : 3) k_short(const LossArgs a) {
     constexpr int N = Vec<T>::N;
     constexpr bool kGrad = OP == kPolicy;
     if (OP == kPrefStat) asm volatile("griddepcontrol.launch_dependents;");   // the gradient's kernel, see there
@@ -1176,8 +1179,8 @@ __global__ void __launch_bounds__(256, NV > 8 ? 2 : 4) k_short(const LossArgs a)
 // pass left them in L2).  4,096 x 128,256 bf16, a quarter ignored: 255 us for 1.84 GB.  It is launched to start
 // while the first pass runs: its CTAs read their part of the logits, and wait for that
 // kernel's end before they use the statistics.
-template <typename T, int NV>
-__global__ void __launch_bounds__(256) k_pref_grad(const LossArgs a, const int segs) {
+template <typename T, int NV, int TB>
+__global__ void __launch_bounds__(TB) k_pref_grad(const LossArgs a, const int segs) {
     constexpr int N = Vec<T>::N;
     const int tid = threadIdx.x;
     const int64_t item = int64_t(gridDim.x) - 1 - blockIdx.x, r = item / segs;
@@ -1188,11 +1191,11 @@ __global__ void __launch_bounds__(256) k_pref_grad(const LossArgs a, const int s
     const bool whole = same_phase(x, static_cast<const T*>(dx));
     const T* body = x + row.head;
     // segments end on 128-byte boundaries: the first one is short by `off` vectors
-    const int lo = seg * NV * 256 - row.off, hi = min(row.body, lo + NV * 256);
+    const int lo = seg * NV * TB - row.off, hi = min(row.body, lo + NV * TB);
     const int64_t y = a.target[r];
     const bool edge = seg == 0 && tid < row.edges;
     auto zeros = [&]() {
-        for (int v = lo + tid; v < hi; v += 256)
+        for (int v = lo + tid; v < hi; v += TB)
             if (v >= 0) store_vec<T>(dx + row.head + int64_t(v) * N, make_uint4(0, 0, 0, 0), whole);
         if (edge) dx[row.edge_at(tid)] = from_f<T>(0.0f);
     };
@@ -1206,7 +1209,7 @@ __global__ void __launch_bounds__(256) k_pref_grad(const LossArgs a, const int s
     uint4 raw[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int v = lo + i * 256 + tid;
+        const int v = lo + i * TB + tid;
         if (v >= 0 && v < hi) raw[i] = ld16(body + int64_t(v) * N);
     }
     const float xe = edge ? to_f(x[row.edge_at(tid)]) : 0.0f;
@@ -1216,7 +1219,7 @@ __global__ void __launch_bounds__(256) k_pref_grad(const LossArgs a, const int s
     if (y < a.vocab) {
         const int j = int(y), v = (j - row.head) / N;
         const bool at_edge = j < row.head || v >= row.body;
-        if (at_edge ? edge && row.edge_at(tid) == j : v >= lo && v < hi && (v - lo) % 256 == tid) {
+        if (at_edge ? edge && row.edge_at(tid) == j : v >= lo && v < hi && (v - lo) % TB == tid) {
             mine = j;
             xy = to_f(x[j]);
         }
@@ -1231,7 +1234,7 @@ __global__ void __launch_bounds__(256) k_pref_grad(const LossArgs a, const int s
     const float c2 = a.it * kLog2e, kq = -st.w * st.rs, u = anchor(st.m, c2);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int v = lo + i * 256 + tid;
+        const int v = lo + i * TB + tid;
         if (v >= 0 && v < hi) {
             float f[N];
             Vec<T>::wide(raw[i], f);
@@ -1328,7 +1331,8 @@ cudaError_t rows_by_threads(const LossArgs& a, const RowShape& sh, int sms, Grou
     return row_launch<T, OP, 256, POW>(a, sh, sms, cache, s);
 }
 
-// Rows of up to 32 NV places, where there are enough of them for a warp each.
+// Rows of up to 32 NV places, where there are enough of them for a warp each to fill the GPU.
+//.
 constexpr int64_t kShortRows = 1024;
 
 template <typename T, int OP, int NV>
@@ -1370,22 +1374,29 @@ cudaError_t rows_by_op(int op, const LossArgs& a, int sms, GroupCache& cache, cu
     return rows_by_threads<T, kDistill, 0>(a, sh, sms, cache, s);
 }
 
-template <typename T>
-cudaError_t pref_grad(const LossArgs& a, cudaStream_t s) {
-    const int vecs = (a.vocab + Vec<T>::N - 1) / Vec<T>::N;
+template <typename T, int TB>
+cudaError_t pref_grad_by(const LossArgs& a, cudaStream_t s) {
     constexpr int NV = 4;
-    const int64_t segs = (vecs + 7 + NV * 256 - 1) / (NV * 256);
+    const int vecs = (a.vocab + Vec<T>::N - 1) / Vec<T>::N;
+    const int64_t segs = (vecs + 7 + NV * TB - 1) / (NV * TB);
     if (a.rows * segs > 0x7fffffff) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(unsigned(a.rows * segs));
-    cfg.blockDim = dim3(256);
+    cfg.blockDim = dim3(TB);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // starts while the first pass runs
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_pref_grad<T, NV>, a, int(segs));
+    return cudaLaunchKernelEx(&cfg, k_pref_grad<T, NV, TB>, a, int(segs));
+}
+// A CTA no larger than a short row's vectors.
+template <typename T>
+cudaError_t pref_grad(const LossArgs& a, cudaStream_t s) {
+    const int places = (a.vocab + Vec<T>::N - 1) / Vec<T>::N + 7;
+    if (places <= 4 * 64) return pref_grad_by<T, 64>(a, s);
+    return places <= 4 * 128 ? pref_grad_by<T, 128>(a, s) : pref_grad_by<T, 256>(a, s);
 }
 
 }  // namespace
