@@ -1331,9 +1331,13 @@ cudaError_t rows_by_threads(const LossArgs& a, const RowShape& sh, int sms, Grou
     return row_launch<T, OP, 256, POW>(a, sh, sms, cache, s);
 }
 
-// Rows of up to 32 NV places, where there are enough of them for a warp each to fill the GPU.
-//.
-constexpr int64_t kShortRows = 1024;
+// Rows of up to 32 NV places, where there are enough of them for a warp each: from kShortRows
+// on with NV 4 and 8, from kLongerRows on with NV 17.  us of k_short / k_row, bf16 policy:
+// 1,000 entries 7.1 / 6.7 with 128 rows, 7.1 / 7.7 with 256, 7.5 / 11.8 with 1,024; 4,096 entries
+// 9.7 / 7.8 with 256 rows, 10.4 / 10.0 with 512, 10.6 / 12.2 with 768; f32 policy of 2,001 entries
+// 7.9 / 7.8 with 256 rows, 8.2 / 9.7 with 512; fp16 preference, gradient and all, of 1,000 entries
+// 9.5 / 14.7 with 256 rows, of 4,096 entries 10.9 / 13.4 with 512.
+constexpr int64_t kShortRows = 256, kLongerRows = 512;
 
 template <typename T, int OP, int NV>
 cudaError_t short_launch(const LossArgs& a, int sms, GroupCache& cache, cudaStream_t s) {
@@ -1354,7 +1358,7 @@ cudaError_t rows_by_length(const LossArgs& a, const RowShape& sh, int sms, Group
     const int places = (a.vocab + Vec<T>::N - 1) / Vec<T>::N + 7;
     if (a.rows >= kShortRows && places <= 32 * 4) return short_launch<T, OP, 4>(a, sms, cache, s);
     if (a.rows >= kShortRows && places <= 32 * 8) return short_launch<T, OP, 8>(a, sms, cache, s);
-    if (a.rows >= kShortRows && places <= 32 * 17) return short_launch<T, OP, 17>(a, sms, cache, s);
+    if (a.rows >= kLongerRows && places <= 32 * 17) return short_launch<T, OP, 17>(a, sms, cache, s);
     return rows_by_threads<T, OP>(a, sh, sms, cache, s);
 }
 
