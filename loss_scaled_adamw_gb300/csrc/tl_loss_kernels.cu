@@ -67,12 +67,31 @@ __device__ __forceinline__ void log2_parts(float s, float& n, float& rest) {
     n = usual ? float(e) : 0.0f;
     rest = log2f(usual ? __int_as_float(__float_as_int(s) - (e << 23)) : s);
 }
+// a + b, and what its rounding left out.
+__device__ __forceinline__ float sum_parts(float a, float b, float& left) {
+    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+    left = __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t));
+    return s;
+}
 // log(exponential of x / s) in a part whose largest element is m, with anchor u; c: the scale
 // of x times log2(e).
 __device__ __forceinline__ float log_share(float x, float m, float u, float c, bool far, float s) {
     float n, rest;
     log2_parts(s, n, rest);
-    return ((far ? (x - m) * c - n : __fmaf_rn(x, c, -(u + n))) - rest) * kLn2;
+    const float plain = ((far ? (x - m) * c - n : __fmaf_rn(x, c, -(u + n))) - rest) * kLn2;
+    // The same with the error of each step carried along, so that the log-probability is rounded
+    // once at its own size: of the 3.7e-7 rms that three roundings left on 128,256 entries a
+    // long sequence's reward is a sum.
+    constexpr double kExactLn2 = 0.693147180559945309;
+    constexpr float kLn2Low = float(kExactLn2 - double(kLn2));
+    const float z = far ? x - m : x, b = far ? n : u + n;
+    const float p = __fmul_rn(z, c), pe = __fmaf_rn(z, c, -p);
+    float de, he;
+    const float d = sum_parts(p, -b, de), h = sum_parts(d, -rest, he);
+    const float low = __fadd_rn(__fadd_rn(pe, de), he);
+    const float r = __fmul_rn(h, kLn2), re = __fmaf_rn(h, kLn2, -r);
+    const float lp = __fadd_rn(r, __fadd_rn(re, __fmaf_rn(low, kLn2, __fmul_rn(h, kLn2Low))));
+    return fabsf(lp) < INFINITY ? lp : plain;   // infinities leave no error to carry
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
