@@ -105,6 +105,24 @@ __device__ __forceinline__ double warp_sum(double v) {
     return v;
 }
 
+// Some of a row's teacher entries (a thread's, a warp's, all): their largest logit m, the sum s
+// of their exponentials, the student's logit z at m's entry, and d, the sum of the exponentials
+// times (t - m) - (x - z).  The divergence is made of d and of two logarithms of shares
+// (log_share): differences of logits only, so that an offset common to a row is not rounded
+// into its loss.  An entry that the student excludes (x of -inf) has z = 0 and d = inf.
+// Without entries m is -inf and s 0; a NaN s makes the row NaN.
+struct __align__(16) TeacherPart {
+    float m, s, d, z;
+};
+__device__ __forceinline__ TeacherPart teacher_entry(float t, float e, float x) {
+    const bool out = x == kNegInf;
+    return {t, e, out && e != 0.0f ? INFINITY : 0.0f, out ? 0.0f : x};
+}
+// p.d against another reference (m, z), times f.
+__device__ __forceinline__ float moved(const TeacherPart& p, float f, float m, float z) {
+    return f != 0.0f && p.s != 0.0f ? f * __fmaf_rn(p.s, (p.m - m) - (p.z - z), p.d) : 0.0f;
+}
+
 __device__ __forceinline__ float teacher_logit(const LossArgs& a, int64_t at) {
     if (a.teacher_dtype == kBF16) return to_f(static_cast<const __nv_bfloat16*>(a.teacher)[at]);
     if (a.teacher_dtype == kF16) return to_f(static_cast<const __half*>(a.teacher)[at]);
@@ -419,6 +437,17 @@ __device__ __forceinline__ float warp_max(float v) {
     return r;
 }
 
+// The lanes' teacher parts joined.
+__device__ __forceinline__ TeacherPart warp_join(const TeacherPart& p, float c2) {
+    TeacherPart r;
+    r.m = warp_max(p.m);
+    r.z = __shfl_sync(~0u, p.z, __ffs(__ballot_sync(~0u, p.m == r.m)) - 1);
+    const float f = rescale(p.m, part_ref(r.m), c2);
+    r.s = warp_sum(p.s * f);
+    r.d = warp_sum(moved(p, f, r.m, r.z));
+    return r;
+}
+
 // The sum at temperature 1 beside the one at tau (distillation with both terms).  For tau
 // = 2 or 4 (POW) its exponentials are powers of the tempered ones; else (POW = 0) they are
 // taken from the logits.
@@ -504,12 +533,12 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
     constexpr bool kTeach = OP == kDistill;
     constexpr bool kGrad = OP == kPolicy || OP == kDistill;
     __shared__ float4 wparts[2][nw];                // by row parity, per warp: m, s, s at temperature 1
-    __shared__ float4 tparts[2][kTeach ? nw : 1];   // teacher: m, sum e, sum e (t - z), bad
+    __shared__ TeacherPart tparts[2][kTeach ? nw : 1];
     __shared__ float4 cparts[2][kMaxCluster];       // per CTA of the group
     // Of four rows in turn: while a row is in pass A its predecessor is in pass B and the one
     // before that has its listed elements written, and a warp may be a row ahead of another.
     __shared__ float4 fac[4][2];                    // gradient factors
-    // [ST][tile] vectors; then [4][3][kpad] of id, t / tau, x.  A copy of a warp into memory off a
+    // [ST][tile] vectors; then [4][3][kpad] of id, t, x.  A copy of a warp into memory off a
     // 128-byte boundary takes twice the requests (4,096 x 128,256 bf16 policy: 361 us, on it 326).
     extern __shared__ __align__(128) uint4 ring[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -574,14 +603,10 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
             const float4 none = make_float4(kNegInf, 0.0f, 0.0f, 0.0f);
             bar_sync(1 + par, B + 32);
             join(lane < nw ? wparts[par][lane] : none);
-            float tm = kNegInf, ts = 0.0f, td = 0.0f, tbad = 0.0f;
+            TeacherPart te{kNegInf, 0.0f, 0.0f, 0.0f};
             auto teacher = [&]() {
-                const float4 p = lane < nw && lane * 32 < a.k ? tparts[par][lane] : none;
-                tm = warp_max(p.x);
-                const float f = rescale(p.x, part_ref(tm), kLog2e);
-                ts = warp_sum(p.y * f);
-                td = warp_sum(f != 0.0f ? p.z * f : 0.0f);
-                tbad = warp_sum(p.w);
+                if (lane < nw && lane * 32 < a.k) te = tparts[par][lane];
+                te = warp_join(te, c2);
             };
             if (cluster > 1) {
                 if (lane < cluster) store_remote(&cparts[par][rank], uint32_t(lane), make_float4(M, S, S1, 0.0f));
@@ -613,33 +638,31 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
                     sum.loss += loss; sum.first += sur; sum.second += kl; sum.count += 1.0;
                 }
             } else {
-                bad += tbad;
-                const bool row_kd = ts != 0.0f;
+                if (te.s != te.s) bad = kNaN;
+                const bool row_kd = te.s != 0.0f;
                 // factors of the exponentials at the temperature and at 1, and of the teacher's
-                // (e_i = exp(t_i - tm) times wp; 0: none)
+                // (e_i = exp((t_i - te.m) it) times wp; 0: none)
                 const float wk = row_kd ? a.kd_weight * step / a.it : 0.0f, wc = ce_on ? a.ce_weight * step : 0.0f;
                 const float kq = wk / S + (DUAL ? 0.0f : wc / S) + bad;
                 const float kq0 = row_kd || (!DUAL && ce_on) || bad != 0.0f ? kq : 0.0f, cq = DUAL ? wc / S1 : 0.0f;
-                const float wp = row_kd ? wk / ts : 0.0f;
+                const float wp = row_kd ? wk / te.s : 0.0f;
                 // the label's element: the teacher may list it too
                 float at_label = 0.0f;
                 if (ce_on && grad) {
                     const float* const tb = teach + buf4 * 3 * kpad;
                     for (int i = lane; i < (wp != 0.0f ? a.k : 0); i += 32)
-                        if (__float_as_int(tb[i]) == int(y)) at_label = __fmaf_rn(wp, power(tb[kpad + i], part_ref(tm), kLog2e), at_label);
+                        if (__float_as_int(tb[i]) == int(y)) at_label = __fmaf_rn(wp, power(tb[kpad + i], part_ref(te.m), c2), at_label);
                     at_label = dense_value(xy, M + bad, kq0, cq) - (warp_sum(at_label) + wc);
                 }
                 if (lane == 0) {
                     fac[buf4][0] = make_float4(M + bad, kq0, cq, at_label);
-                    fac[buf4][1] = make_float4(wp, tm, anchor(tm, kLog2e), 0.0f);
+                    fac[buf4][1] = make_float4(wp, te.m, anchor(te.m, c2), 0.0f);
                 }
                 bar_arrive(3 + par, B + 32);
-                // kd = sum p (t - z) - log sum exp t + log sum exp z
-                const float lse_z = far ? M * a.it - log_share(M, M, u, c2, far, S) : -log_share(0.0f, M, u, c2, far, S);
-                const bool tfar = big(tm, kLog2e);
-                const float lse_t = tfar ? tm - log_share(tm, tm, 0.0f, kLog2e, tfar, ts)
-                                         : -log_share(0.0f, tm, anchor(tm, kLog2e), kLog2e, tfar, ts);
-                const float kd = row_kd ? (td / ts - lse_t + lse_z) / (a.it * a.it) + bad : bad;
+                // kd = tau^2 (sum p ((t - te.m) - (x - te.z)) / tau + log p - log q at te's entry)
+                const float tau = 1.0f / a.it;
+                const float logs = log_share(te.m, te.m, anchor(te.m, c2), c2, big(te.m, c2), te.s) - log_share(te.z, M, u, c2, far, S);
+                const float kd = !row_kd ? bad : te.d == INFINITY ? te.d + bad : (te.d / te.s + logs * tau) * tau + bad;
                 const float ce = !ce_on ? 0.0f
                                  : DUAL ? bad - log_share(xy, M, untempered_ref<POW>(M, u), kLog2e, far, S1)
                                         : bad - lp;
@@ -749,9 +772,9 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
             const float4 fc = fac[listed_buf][0], f1 = fac[listed_buf][1];
             const float* const tb = teach + listed_buf * 3 * kpad;
             const float Mb = fc.x, kq = fc.y, cq = fc.z, tm = f1.y, tu = f1.z, wp = f1.x;
-            const bool tfar = big(tm, kLog2e);
+            const bool tfar = big(tm, c2);
             auto share = [&](int j) {   // the teacher's exponential of entry j
-                return ex2(tfar ? (tb[kpad + j] - tm) * kLog2e : __fmaf_rn(tb[kpad + j], kLog2e, -tu));
+                return ex2(tfar ? (tb[kpad + j] - tm) * c2 : __fmaf_rn(tb[kpad + j], c2, -tu));
             };
             const int n = wp != 0.0f ? a.k : 0;
             const int* const ids = reinterpret_cast<const int*>(tb);
@@ -996,36 +1019,33 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
                     // thread is in registers
                     float* const tb = teach + buf4 * 3 * kpad;
                     if (tid < kpad - a.k) tb[a.k + tid] = __int_as_float(-1);
-                    auto entry = [&](int j, int64_t id, float logit, float z, float& t) {   // into the buffer; t / tau
+                    auto entry = [&](int j, int64_t id, float logit, float x) {   // into the buffer; -inf: none
                         const bool on = id >= 0 && id < a.vocab;
-                        t = on ? logit * a.it : kNegInf;
+                        const float t = on ? logit : kNegInf;
                         tb[j] = __int_as_float(on ? int(id) : -1);
                         tb[kpad + j] = t;
-                        tb[2 * kpad + j] = z;
+                        tb[2 * kpad + j] = x;
+                        return t;
                     };
-                    float tm = kNegInf, ts = 0.0f, td = 0.0f;
+                    TeacherPart te{kNegInf, 0.0f, 0.0f, 0.0f};
                     bool beyond = tid < a.k && id0 >= a.vocab;
                     if (tid < a.k) {
-                        entry(tid, id0, t0, z0, tm);
-                        ts = tm == kNegInf ? 0.0f : power(tm, tm, kLog2e);
-                        td = ts != 0.0f ? ts * (tm - z0 * a.it) : 0.0f;
+                        const float t = entry(tid, id0, t0, z0);
+                        te = teacher_entry(t, t == kNegInf ? 0.0f : power(t, t, c2), z0);
                     }
                     for (int j = tid + B; j < a.k; j += B) {
                         const int64_t id = teacher_id(a, r * a.ldt + j);
                         const float z = id >= 0 && id < a.vocab ? to_f(x[id]) : 0.0f;
-                        float t;
-                        entry(j, id, teacher_logit(a, r * a.ldt + j), z, t);
+                        const float t = entry(j, id, teacher_logit(a, r * a.ldt + j), z);
                         beyond = beyond || id >= a.vocab;
-                        const float nm = fmaxf(tm, t), f = rescale(tm, part_ref(nm), kLog2e), e = power(t, part_ref(nm), kLog2e);
-                        ts = ts * f + e;
-                        td = (f != 0.0f ? td * f : 0.0f) + (e != 0.0f ? e * (t - z * a.it) : 0.0f);
-                        tm = nm;
+                        const float m = fmaxf(te.m, t), f = rescale(te.m, part_ref(m), c2);
+                        const TeacherPart one = teacher_entry(t, power(t, part_ref(m), c2), z);
+                        const float mz = t > te.m ? one.z : te.z;
+                        te = {m, te.s * f + one.s, moved(te, f, m, mz) + moved(one, 1.0f, m, mz), mz};
                     }
-                    const float wm = warp_max(tm), f = rescale(tm, part_ref(wm), kLog2e);
-                    ts = warp_sum(ts * f);
-                    td = warp_sum(f != 0.0f ? td * f : 0.0f);
-                    const float bad = __any_sync(~0u, beyond) ? kNaN : 0.0f;
-                    if (lane == 0) tparts[par][warp] = make_float4(wm, ts, td, bad);
+                    te = warp_join(te, c2);
+                    if (__any_sync(~0u, beyond)) te.s = kNaN;
+                    if (lane == 0) tparts[par][warp] = te;
                 }
                 if (cluster > 1) {
                     if (exchanged) cluster_wait();   // of the row before: long past

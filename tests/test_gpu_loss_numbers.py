@@ -1,0 +1,85 @@
+"""What the objectives' numbers promise beyond test_gpu_loss.py: a distillation loss made of
+differences alone.
+
+Constants of test_gpu_loss.py: EPS = 2^-24, REL bounds the relative error of an
+exponential's share and the absolute one of the logarithm of a row's sum.
+"""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import loss_reference as R
+import loss_scaled_adamw_gb300 as tl
+import test_gpu_loss as base
+from test_gpu_loss import EPS, INF, REL, close
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def lctx():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from loss_scaled_adamw_gb300 import _build
+    _build.build()
+    return tl.tl_loss_create(20000, 64)
+
+
+# --------------------------------------------------- distillation: differences alone
+
+def kd_tolerance(x, teacher, ids, tau):
+    """Per row, of kd = tau^2 (sum_i p_i (d_i / tau) + log p_r - log q_r), d_i = (t_i - t_r) -
+    (x_i - x_r) against one reference entry r, the largest of the teacher's.  With D the
+    largest |t_i - t_r| + |x_i - x_r|: a difference rounds three times, its product and the
+    quotient by the sum once each (8 EPS D), and the weights p_i are within 2 REL; log p_r and
+    log q_r are within REL and, through the scale of their exponent, 8 EPS of their own size."""
+    tol = torch.zeros(x.shape[0], dtype=torch.float64)
+    for t in range(x.shape[0]):
+        at = [i for i, j in enumerate(ids[t].tolist()) if 0 <= j < x.shape[1] and teacher[t, i] > -INF]
+        if not at:
+            continue
+        te, xe = teacher[t, at].double(), x[t, ids[t, at].long()].double()
+        D = float(te.max() - te.min() + xe.max() - xe.min())
+        log_q = (xe / tau - torch.logsumexp(x[t].double() / tau, 0)).abs().max()
+        log_p = math.log(len(at))
+        tol[t] = tau * (2 * REL + 8 * EPS) * D + tau * tau * (2 * REL + 8 * EPS * (log_p + float(log_q)))
+    return tol
+
+
+@pytest.mark.parametrize("tau", [0.1, 0.7, 1.0, 2.0, 3.0])
+@pytest.mark.parametrize("V,K", [(300, 6), (9000, 40), (9000, 300), (70000, 17)])
+def test_distillation_is_the_same_at_any_offset(lctx, V, K, tau):
+    """A common offset of a row's logits, of the student or the teacher, changes nothing, nor do
+    finite masks of -1e9 and -1e30 all over a row: the loss is a function of differences.
+    Logits are multiples of 1/64 below 2^18 (of 64 at 1e9), so every difference is exact."""
+    g, x, y = base.make(10, V, "f32", 30, masked=0.0)
+    x = (x * 64).round() / 64
+    teacher, ids = base.teacher_of(10, V, K, g)
+    teacher = (teacher * 64).round() / 64
+    for t, (student, other) in enumerate([(0.0, 0.0), (1e3, 0.0), (-3e4, 5e4), (1.8e5, -2.0 ** 17), (-2.0 ** 17, 1.0),
+                                          (0.0, 2.0 ** 17)]):
+        x[t] += student
+        teacher[t] += other
+    x[6] = -1e9
+    x[6, ids[6, :3].long()] = torch.tensor([-1e9 + 128, -1e9 + 64, -1e9])   # fp32 spacing there is 64
+    y[6] = ids[6, 0]
+    x[7], teacher[7] = -1e30, -1e30
+    teacher[8] = -1e9
+    x[9, : V // 2] = -1e9
+    ids[9] = V // 2 + ids[9] % (V - V // 2)
+    y[9] = V - 1
+    # the statement gets the teacher's differences: a log-sum at -1e30 would lose log K in 64 bits too
+    from_top = teacher.double() - teacher.double().amax(1, keepdim=True)
+    for kd, ce in ((1.0, 0.0), (0.5, 0.5)):
+        got = base.run_distill(lctx, x, teacher, ids, 10, y, kd, ce, tau, backward=False)
+        want = R.distill(x, from_top, ids, 10, y, kd, ce, tau)
+        kd_tol = kd_tolerance(x, teacher, ids, tau)
+        ce_row = (want["loss"] - kd * want["kd"]) / ce if ce else torch.zeros(10, dtype=torch.float64)
+        ce_tol = REL + 8 * EPS * ce_row.abs()
+        tol = kd * kd_tol + ce * ce_tol + 4 * EPS * want["loss"].abs()
+        close(got["loss"], want["loss"], tol, "loss")
+        r = want["result"].double()
+        st = torch.stack([tol.sum() / 10, kd_tol.sum() / 10, ce_tol.sum() / 10 * (ce > 0), torch.tensor(0.0).double()])
+        close(got["result"], r, st + 4 * EPS * r.abs(), "result")
