@@ -33,8 +33,9 @@
  * held in fp32 or fp64 whatever the logits' type; a gradient element is
  * computed in fp32 and rounded once to the logits' type.  Entries of -inf
  * (excluded tokens) have probability and gradient 0.  A row with a +inf or NaN
- * entry, or with nothing but -inf, has no softmax: its loss and gradient are
- * NaN.  Results do not depend on timing: every sum has a fixed order for given
+ * entry, or with nothing but -inf, has no softmax: its loss and all of its
+ * gradient are NaN, whatever the weights (also for a +inf or NaN among the teacher
+ * entries that a row uses).  Results do not depend on timing: every sum has a fixed order for given
  * sizes on a given device.
  *
  * Memory.  The caller owns every tensor.  Rows are contiguous, row t starting

@@ -638,7 +638,9 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
                     sum.loss += loss; sum.first += sur; sum.second += kl; sum.count += 1.0;
                 }
             } else {
-                if (te.s != te.s) bad = kNaN;
+                // without a softmax of the student (a NaN or +inf logit) or the teacher: a row with neither
+                // entries nor a cross-entropy takes nothing else from S
+                if (!(S < INFINITY) || te.s != te.s) bad = kNaN;
                 const bool row_kd = te.s != 0.0f;
                 // factors of the exponentials at the temperature and at 1, and of the teacher's
                 // (e_i = exp((t_i - te.m) it) times wp; 0: none)

@@ -1,5 +1,5 @@
 """What the objectives' numbers promise beyond test_gpu_loss.py: a distillation loss made of
-differences alone.
+differences alone, and rows without a softmax in distillation.
 
 Constants of test_gpu_loss.py: EPS = 2^-24, REL bounds the relative error of an
 exponential's share and the absolute one of the logarithm of a row's sum.
@@ -13,7 +13,7 @@ torch = pytest.importorskip("torch")
 import loss_reference as R
 import loss_scaled_adamw_gb300 as tl
 import test_gpu_loss as base
-from test_gpu_loss import EPS, INF, REL, close
+from test_gpu_loss import EPS, INF, NAN, REL, close
 
 pytestmark = pytest.mark.gpu
 
@@ -83,3 +83,49 @@ def test_distillation_is_the_same_at_any_offset(lctx, V, K, tau):
         r = want["result"].double()
         st = torch.stack([tol.sum() / 10, kd_tol.sum() / 10, ce_tol.sum() / 10 * (ce > 0), torch.tensor(0.0).double()])
         close(got["result"], r, st + 4 * EPS * r.abs(), "result")
+
+
+# ------------------------------------------------- distillation: rows without a softmax
+
+@pytest.mark.parametrize("V", [40, 700, 9000, 70000])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("tau", [1.0, 2.0, 3.0])
+def test_distillation_of_rows_without_a_softmax(lctx, V, dtype, tau):
+    """A valid row with a NaN or +inf logit, with nothing but -inf, or with a teacher entry of
+    NaN or +inf is NaN in its loss and in its whole gradient, whatever the teacher lists and
+    whatever the weights; the rows beside it are not."""
+    T, K = 16, 5
+    g, x, y = base.make(T, V, dtype, 31, masked=0.0)
+    teacher, ids = base.teacher_of(T, V, K, g)
+    for t in range(0, 9):                    # NaN, +inf, -inf: with entries, padded ones, -inf ones
+        x[t, V // 3] = (NAN, INF, 0.0)[t % 3]
+        if t % 3 == 2:
+            x[t] = -INF
+        if t in (3, 4, 5):
+            ids[t] = -1
+        if t in (6, 7, 8):
+            teacher[t] = -INF
+    teacher[9, 2], teacher[10, 4] = NAN, INF
+    ids[11] = -1                              # no entries: kd = 0
+    teacher[12] = -INF                        # the same
+    bad = torch.zeros(T, dtype=torch.bool)
+    for kd, ce, k in ((1.0, 0.0, K), (0.6, 0.4, K), (0.6, 0.0, 0), (0.6, 0.4, 0), (0.0, 0.0, K)):
+        bad[:9], bad[9:11] = True, k > 0 and kd > 0
+        te, ti = (teacher, ids) if k else (None, None)
+        for in_place in (False, True):
+            got = base.run_distill(lctx, x, te, ti, T, y, kd, ce, tau, 4.0, in_place=in_place)
+            dx = torch.isnan(got["dx"].float())
+            assert torch.equal(torch.isnan(got["loss"]).cpu(), bad), (kd, ce, k)
+            assert torch.equal(dx.all(1).cpu(), bad) and torch.equal(dx.any(1).cpu(), bad), (kd, ce, k)
+            assert math.isnan(float(got["result"][0])) and float(got["result"][3]) == T
+            # the others are what they are without the bad rows beside them
+            ok = ~bad
+            want = R.distill(x[ok], te[ok] if k else None, ti[ok] if k else None, T, y[ok], kd, ce, tau, 4.0)
+            w = torch.full((int(ok.sum()),), 4.0 / T * (kd * tau + ce), dtype=torch.float64)
+            hot = base.hot(y[ok], V)
+            if k:
+                for i, row in enumerate(ti[ok].tolist()):
+                    for j in row:
+                        if j >= 0:
+                            hot[i, j] = True
+            base.check_dx(got["dx"][ok.cuda()], want["dx"], dtype, w, torch.full_like(w, 2 * REL + 64 * EPS), hot, "dx")
