@@ -106,10 +106,11 @@ __device__ __forceinline__ double warp_sum(double v) {
 }
 
 // Some of a row's teacher entries (a thread's, a warp's, all): their largest logit m, the sum s
-// of their exponentials, the student's logit z at m's entry, and d, the sum of the exponentials
-// times (t - m) - (x - z).  The divergence is made of d and of two logarithms of shares
-// (log_share): differences of logits only, so that an offset common to a row is not rounded
-// into its loss.  An entry that the student excludes (x of -inf) has z = 0 and d = inf.
+// of their exponentials, the student's logit z at the first of them, and d, the sum of the
+// exponentials times (t - m) - (x - z).  The divergence is made of d and of two logarithms of
+// shares (log_share): differences of logits only, so that an offset common to a row is not
+// rounded into its loss.  (z is of the first entry, not of m's: it is known before the maximum.)
+// An entry that the student excludes (x of -inf) has z = 0 and d = inf.
 // Without entries m is -inf and s 0; a NaN s makes the row NaN.
 struct __align__(16) TeacherPart {
     float m, s, d, z;
@@ -440,8 +441,9 @@ __device__ __forceinline__ float warp_max(float v) {
 // The lanes' teacher parts joined.
 __device__ __forceinline__ TeacherPart warp_join(const TeacherPart& p, float c2) {
     TeacherPart r;
+    const unsigned has = __ballot_sync(~0u, p.m > kNegInf && p.d < INFINITY);
+    r.z = __shfl_sync(~0u, p.z, has ? __ffs(has) - 1 : 0);
     r.m = warp_max(p.m);
-    r.z = __shfl_sync(~0u, p.z, __ffs(__ballot_sync(~0u, p.m == r.m)) - 1);
     const float f = rescale(p.m, part_ref(r.m), c2);
     r.s = warp_sum(p.s * f);
     r.d = warp_sum(moved(p, f, r.m, r.z));
@@ -661,7 +663,7 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
                     fac[buf4][1] = make_float4(wp, te.m, anchor(te.m, c2), 0.0f);
                 }
                 bar_arrive(3 + par, B + 32);
-                // kd = tau^2 (sum p ((t - te.m) - (x - te.z)) / tau + log p - log q at te's entry)
+                // kd = tau^2 (sum p ((t - te.m) - (x - te.z)) / tau + log p at te.m - log q at te.z)
                 const float tau = 1.0f / a.it;
                 const float logs = log_share(te.m, te.m, anchor(te.m, c2), c2, big(te.m, c2), te.s) - log_share(te.z, M, u, c2, far, S);
                 const float kd = !row_kd ? bad : te.d == INFINITY ? te.d + bad : (te.d / te.s + logs * tau) * tau + bad;
@@ -1042,8 +1044,8 @@ __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row
                         beyond = beyond || id >= a.vocab;
                         const float m = fmaxf(te.m, t), f = rescale(te.m, part_ref(m), c2);
                         const TeacherPart one = teacher_entry(t, power(t, part_ref(m), c2), z);
-                        const float mz = t > te.m ? one.z : te.z;
-                        te = {m, te.s * f + one.s, moved(te, f, m, mz) + moved(one, 1.0f, m, mz), mz};
+                        const float first = te.m > kNegInf && te.d < INFINITY ? te.z : one.z;
+                        te = {m, te.s * f + one.s, moved(te, f, m, first) + moved(one, 1.0f, m, first), first};
                     }
                     te = warp_join(te, c2);
                     if (__any_sync(~0u, beyond)) te.s = kNaN;
