@@ -170,6 +170,7 @@ __device__ __forceinline__ void finish_sums(const LossArgs& a, const LossSums& s
         last = last_group(a, ngroups);
     }
     if (!__shfl_sync(~0u, last, 0)) return;
+    __syncwarp();   // the first lane's acquire holds for all: a shuffle orders no memory
     double v[4] = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll 4
     for (int i = lane; i < ngroups; i += 32) {
