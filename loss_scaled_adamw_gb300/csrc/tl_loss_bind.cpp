@@ -153,7 +153,7 @@ int distill_loss(PyObject* const* a) {
     const tl_loss_out o = outputs(a[4], a[5], a[6], a[7], a[8], x.rows, a[9], x, device);
     tl_distill_args p{};
     p.target = longs(a[11], x.rows, device, "targets");
-    if (a[12] != Py_None) {
+    if (a[12] != Py_None || a[13] != Py_None) {   // one without the other is refused
         const Matrix t = matrix(a[12], device, "teacher_logits"), ids = matrix(a[13], device, "teacher_ids");
         if (t.rows != x.rows || ids.rows != x.rows || ids.cols != t.cols || ids.ld != t.ld)
             refuse("teacher_logits and teacher_ids", "[rows, k] with one row stride");

@@ -1,5 +1,6 @@
 """What the objectives' numbers promise beyond test_gpu_loss.py: a distillation loss made of
-differences alone, and rows without a softmax in distillation.
+differences alone, rows without a softmax in distillation, and arguments that are refused
+rather than dropped.
 
 Constants of test_gpu_loss.py: EPS = 2^-24, REL bounds the relative error of an
 exponential's share and the absolute one of the logarithm of a row's sum.
@@ -129,3 +130,18 @@ def test_distillation_of_rows_without_a_softmax(lctx, V, dtype, tau):
                         if j >= 0:
                             hot[i, j] = True
             base.check_dx(got["dx"][ok.cuda()], want["dx"], dtype, w, torch.full_like(w, 2 * REL + 64 * EPS), hot, "dx")
+
+
+# ------------------------------------------------------------------------- refusals
+
+def test_nothing_that_is_given_is_dropped(lctx):
+    T, V = 4, 64
+    x, y = torch.zeros(T, V, device="cuda"), torch.zeros(T, dtype=torch.int64, device="cuda")
+    ids, tea = torch.zeros(T, 2, dtype=torch.int32, device="cuda"), torch.zeros(T, 2, device="cuda")
+    res = torch.zeros(4, device="cuda")
+    before = tl.tl_loss_launch_count(lctx)
+    for call in (lambda: tl.tl_distill_loss(lctx, x, None, ids, 4, res, targets=y, ce_weight=1.0),
+                 lambda: tl.tl_distill_loss(lctx, x, tea, None, 4, res, targets=y, ce_weight=1.0)):
+        with pytest.raises(ValueError):
+            call()
+    assert tl.tl_loss_launch_count(lctx) == before
