@@ -93,12 +93,21 @@ tl_logits logits(PyObject* o, PyObject* temperature, long device) {
     return {m.data, m.rows, m.cols, m.ld, type, number(temperature)};
 }
 
+// A device float: its address as an integer, or a tensor of one element, or None.  0 is what
+// tl_scale_ptr gives for a destroyed context: no seed at all would scale the gradient by 1.
+const float* seed_of(PyObject* o, long device) {
+    if (!PyLong_Check(o)) return floats(o, 1, device, "seed");
+    const float* p = static_cast<const float*>(address(o));
+    if (p == nullptr) refuse("seed", "a device address other than 0, a tensor of one element or None");
+    return p;
+}
+
 // n, seed, dlogits, logp, loss (of `losses` elements), result
 tl_loss_out outputs(PyObject* n, PyObject* seed, PyObject* dlogits, PyObject* logp, PyObject* loss, int64_t losses,
                     PyObject* result, const tl_logits& x, long device) {
     tl_loss_out o{};
     o.n = whole(n);
-    o.seed = PyLong_Check(seed) ? static_cast<const float*>(address(seed)) : floats(seed, 1, device, "seed");
+    o.seed = seed_of(seed, device);
     if (dlogits != Py_None) {
         const Matrix d = matrix(dlogits, device, "dlogits");
         if (float_type(d.type) != x.dtype || d.rows != x.rows || d.cols != x.vocab)

@@ -150,7 +150,7 @@ def tl_policy_loss(lctx: LossContext, logits, targets, old_logp, advantages, n: 
                    seed=None, dlogits=None, logp=None, row_loss=None, stream=None) -> None:
     """Clipped policy objective with a KL penalty, mean over n valid targets; its gradient
     into dlogits (which may be the logits themselves).  seed: a device address (tl_scale_ptr),
-    a float32 CUDA tensor of one element, or None."""
+    a float32 CUDA tensor of one element, or None (a gradient of the plain mean)."""
     rc = _bind.policy_loss(lctx._address, lctx.device, logits, temperature, n, seed, dlogits, logp, row_loss, result,
                            _stream(lctx, stream), targets, old_logp, ref_logp, advantages, clip_low, clip_high,
                            kl_weight)

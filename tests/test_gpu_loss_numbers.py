@@ -138,10 +138,13 @@ def test_nothing_that_is_given_is_dropped(lctx):
     T, V = 4, 64
     x, y = torch.zeros(T, V, device="cuda"), torch.zeros(T, dtype=torch.int64, device="cuda")
     ids, tea = torch.zeros(T, 2, dtype=torch.int32, device="cuda"), torch.zeros(T, 2, device="cuda")
-    res = torch.zeros(4, device="cuda")
+    f, res = torch.zeros(T, device="cuda"), torch.zeros(4, device="cuda")
     before = tl.tl_loss_launch_count(lctx)
     for call in (lambda: tl.tl_distill_loss(lctx, x, None, ids, 4, res, targets=y, ce_weight=1.0),
-                 lambda: tl.tl_distill_loss(lctx, x, tea, None, 4, res, targets=y, ce_weight=1.0)):
+                 lambda: tl.tl_distill_loss(lctx, x, tea, None, 4, res, targets=y, ce_weight=1.0),
+                 lambda: tl.tl_policy_loss(lctx, x, y, f, f, 4, res, seed=0),       # the scale of a destroyed context
+                 lambda: tl.tl_preference_loss(lctx, x, y, torch.tensor([0, 2, 4], device="cuda"), 1, res, seed=0),
+                 lambda: tl.tl_distill_loss(lctx, x, tea, ids, 4, res, seed=0)):
         with pytest.raises(ValueError):
             call()
     assert tl.tl_loss_launch_count(lctx) == before
