@@ -1,6 +1,6 @@
 """What the objectives' numbers promise beyond test_gpu_loss.py: a distillation loss made of
-differences alone, rows without a softmax in distillation, and arguments that are refused
-rather than dropped.
+differences alone, rows without a softmax in distillation, the accuracy of a
+log-probability, and arguments that are refused rather than dropped.
 
 Constants of test_gpu_loss.py: EPS = 2^-24, REL bounds the relative error of an
 exponential's share and the absolute one of the logarithm of a row's sum.
@@ -14,7 +14,7 @@ torch = pytest.importorskip("torch")
 import loss_reference as R
 import loss_scaled_adamw_gb300 as tl
 import test_gpu_loss as base
-from test_gpu_loss import EPS, INF, NAN, REL, close
+from test_gpu_loss import DT, EPS, INF, NAN, REL, close
 
 pytestmark = pytest.mark.gpu
 
@@ -130,6 +130,73 @@ def test_distillation_of_rows_without_a_softmax(lctx, V, dtype, tau):
                         if j >= 0:
                             hot[i, j] = True
             base.check_dx(got["dx"][ok.cuda()], want["dx"], dtype, w, torch.full_like(w, 2 * REL + 64 * EPS), hot, "dx")
+
+
+# ------------------------------------------------------------ accuracy of log-probabilities
+
+def scored(T, V, dtype, seed, spread=2.5):
+    """Logits on the GPU, random labels, and the labels' log-probabilities in 64 bits."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    x = (torch.randn(T, V, generator=g, device="cuda") * spread).to(DT[dtype])
+    y = torch.randint(0, V, (T,), generator=g, device="cuda")
+    want = torch.cat([torch.log_softmax(x[a:a + 256].double(), 1).gather(1, y[a:a + 256, None])[:, 0]
+                      for a in range(0, T, 256)])
+    return g, x, y, want
+
+
+def with_three_roundings(x, y):
+    """log q_y formed as ((x_y log2 e - u - n) - log2 of the sum's rest) ln 2 in fp32, each step
+    rounded, from a sum that is exact: what the kernel would give if it did not carry errors along."""
+    f = lambda v: v.float().double()  # noqa: E731
+    c, ln2 = torch.tensor(1.4426950408889634).double(), torch.tensor(0.6931471805599453).double()
+    out = []
+    for a in range(0, x.shape[0], 256):
+        z = x[a:a + 256].double()
+        u = torch.round(z.amax(1) * c)
+        s = f(torch.exp2(z * c - u[:, None]).sum(1))
+        n = torch.floor(torch.log2(s))
+        rest = f(torch.log2(s * torch.exp2(-n)))
+        p = f(z.gather(1, y[a:a + 256, None])[:, 0] * c - (u + n))
+        out.append(f(f(p - rest) * ln2))
+    return torch.cat(out)
+
+
+@pytest.mark.parametrize("T,V,dtype", [(4096, 8192, "f32"), (4096, 1000, "f16"), (2048, 50001, "bf16"), (1024, 128256, "bf16")])
+def test_log_probabilities_are_rounded_once(lctx, T, V, dtype):
+    """Over many rows (temperature 1).  Rounding the result itself has the rms q of the exact
+    values.  The logarithm of the sum adds: an exponential's error of at most 2^-22, as if one
+    term made the sum and the error were uniform (1.4e-7); the roundings of partial sums, eight
+    or so on the way of a term that counts, 0.35e-7 each (1e-7); log2's last place (0.4e-7):
+    1.8e-7, taken as 2e-7.  The scale log2 e is off by 1.34e-8 of itself in fp32, which moves
+    every result by that part of x_y - E_q[x], in the mean the logits' variance 6.25: 0.84e-7;
+    with a mean error of the exponential within 2^-24 the mean is held to 1.5e-7 + 5 rms /
+    sqrt(T), and the rms is taken about the mean.  An rms of T rows strays by 5 / sqrt(2 T)."""
+    g, x, y, want = scored(T, V, dtype, 40)
+    lp = torch.zeros(T, device="cuda")
+    tl.tl_token_logprob(lctx, x, y, lp)
+    q = float((want.float().double() - want).square().mean().sqrt())
+    bound = math.sqrt(q * q + 2e-7 ** 2) * (1 + 5 / math.sqrt(2 * T))
+    rms = lambda e: float((e - e.mean()).square().mean().sqrt())  # noqa: E731
+    e = lp.double() - want
+    assert rms(with_three_roundings(x, y) - want) > bound        # the bound tells them apart
+    assert rms(e) <= bound, (rms(e), bound)
+    assert abs(float(e.mean())) <= 1.5e-7 + 5 * bound / math.sqrt(T), float(e.mean())
+
+
+def test_rewards_of_long_sequences(lctx):
+    """beta times a sum of 4,000 rows' lp - ref.  Per row the errors of the test above, rms 3.5e-7
+    and mean 1.5e-7; lp - ref (at most 2) rounds by 1.2e-7 more, unbiased."""
+    T, V, L = 8192, 2000, 4000
+    g, x, y, want = scored(T, V, "f32", 41)
+    ref = (want + 0.3 * torch.randn(T, generator=g, device="cuda").double()).float()
+    seq = torch.tensor([7, 7 + L, 7 + 2 * L], device="cuda")
+    res, rew = torch.zeros(4, device="cuda"), torch.zeros(2, device="cuda")
+    tl.tl_preference_loss(lctx, x, y, seq, 1, res, ref_logp=ref, beta=0.1, reward=rew)
+    d = want - ref.double()
+    exact = 0.1 * torch.stack([d[7:7 + L].sum(), d[7 + L:7 + 2 * L].sum()])
+    tol = 0.1 * (5 * math.sqrt(3.5e-7 ** 2 + 1.2e-7 ** 2) * math.sqrt(L) + 1.5e-7 * L) + 4 * EPS * exact.abs().cpu()
+    close(rew, exact.cpu(), tol, "reward")
 
 
 # ------------------------------------------------------------------------- refusals
