@@ -3,14 +3,17 @@
 The translation units (kernels, host C ABI, the allocation-free entry point, the
 objectives over logits) compile in parallel, then link into one shared library with
 the CUDA runtime linked statically.  The objectives' binding (_loss_bind, a CPython
-module over torch's headers) is host code of its own beside it.
+module over torch's headers) is host code of its own beside it, and nothing of the
+optimizer step needs it.
 """
 from __future__ import annotations
 
+import importlib.metadata
 import importlib.util
 import os
 import subprocess
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -44,9 +47,26 @@ def build(force: bool = False, verbose: bool = False) -> str:
     srcs = [os.path.join(CSRC, s) for s in SOURCES]
     if force or _stale(LIB, srcs + HEADERS + [__file__]):
         _build_library(srcs, verbose)
-    if force or _stale(BIND, [BIND_SOURCE, __file__] + HEADERS):
+    if force or _stale(BIND, [BIND_SOURCE, __file__] + HEADERS) or _built_key() != _binding_key():
         _build_binding(verbose)
     return LIB
+
+
+def _binding_key() -> str:
+    """What the binding is compiled against: a torch and a Python of some version."""
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        version = "unknown"
+    return f"{sysconfig.get_config_var('SOABI')} torch {version}"
+
+
+def _built_key() -> str:
+    path = os.path.join(BUILD, "_loss_bind.key")
+    if not os.path.exists(path):
+        return ""
+    with open(path) as f:
+        return f.read()
 
 
 def _run(cmd, verbose: bool, what: str) -> None:
@@ -63,12 +83,23 @@ def _build_binding(verbose: bool) -> None:
         return   # the optimizer step's binding does without torch; losses.py says what is missing
     torch = os.path.dirname(spec.origin)
     tmp = BIND + f".tmp{os.getpid()}"
-    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-I" + sysconfig.get_path("include"),
-          "-isystem", os.path.join(torch, "include"),
-          "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"), BIND_SOURCE, "-o", tmp,
-          "-L" + PKG, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(torch, "lib"),
-          "-ltorch_python", "-ltorch_cpu", "-lc10"], verbose, "g++")
+    try:
+        _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-I" + sysconfig.get_path("include"),
+              "-isystem", os.path.join(torch, "include"),
+              "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"), BIND_SOURCE, "-o", tmp,
+              "-L" + PKG, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(torch, "lib"),
+              "-ltorch_python", "-ltorch_cpu", "-lc10"], verbose, "g++")
+    except (OSError, RuntimeError) as e:
+        # no compiler, or no headers of Python or torch: the library stands without the binding, and
+        # the objectives' calls say that it is missing.  An older one may pass other structures.
+        if os.path.exists(BIND):
+            os.remove(BIND)
+        warnings.warn(f"the objectives' binding was not built; the optimizer step does not need it: {e}", RuntimeWarning)
+        return
     os.replace(tmp, BIND)
+    os.makedirs(BUILD, exist_ok=True)
+    with open(os.path.join(BUILD, "_loss_bind.key"), "w") as f:
+        f.write(_binding_key())
 
 
 def _build_library(srcs, verbose: bool) -> None:
