@@ -132,7 +132,8 @@ int tl_policy_loss(tl_loss_ctx* ctx, const tl_logits* logits, const tl_policy_ar
 /* Paired preference objective.  seq holds 2 * pairs + 1 non-decreasing row
  * offsets: rows [seq[2p], seq[2p+1]) are the chosen sequence of pair p, rows
  * [seq[2p+1], seq[2p+2]) the rejected one (a prompt's rows are ignored through
- * target < 0; rows outside every sequence are ignored too; offsets are held to
+ * target < 0; a row outside every sequence has no part in any sum and a zero
+ * gradient, and its logp is still its log-probability; offsets are held to
  * [0, rows] on the device).  With s(.) the sum over a sequence's valid rows of
  * lp - ref_logp (of lp without ref_logp), reward = beta * s, h = s(chosen) -
  * s(rejected) and sg the logistic function:

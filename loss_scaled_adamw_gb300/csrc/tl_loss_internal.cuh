@@ -13,8 +13,7 @@ enum LossOp : int {
     kLogprob = 0,     // the target's log-probability
     kPolicy = 1,      // clipped policy objective, forward (and backward when dx is set)
     kPrefStat = 2,    // preference, first pass: row statistics and log-ratios, then the pairs
-    kDistill = 3,     // distillation, forward (and backward when dx is set)
-    kLossOps = 4
+    kDistill = 3      // distillation, forward (and backward when dx is set)
 };
 
 constexpr int kMaxTeacher = 1024;      // teacher entries per row

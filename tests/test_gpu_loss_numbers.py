@@ -184,6 +184,33 @@ def test_log_probabilities_are_rounded_once(lctx, T, V, dtype):
     assert abs(float(e.mean())) <= 1.5e-7 + 5 * bound / math.sqrt(T), float(e.mean())
 
 
+@pytest.mark.parametrize("V,dtype", [(126599, "f32"), (128256, "bf16")])
+@pytest.mark.parametrize("tau", [0.7, 0.5])
+def test_small_terms_of_a_long_row_are_not_lost(lctx, V, dtype, tau):
+    """Below 1 a temperature spreads a row's exponentials over tens of bits, and most of them are
+    small against a thread's sum: added one at a time, more of them fall below half of its last
+    place than round up, and every log-probability comes out high (by 1.5e-7 and 2.4e-7 for these
+    two, from additions in fp32 alone).  The mean is held to the exponential's mean error (2^-24) and five
+    standard errors; per row an exponent of up to 32 bits rounds by up to 2^-20 (rms
+    3.8e-7 in the sum where one term makes it), beside the result's rounding q: with 5e-7 for
+    all but q.  The definition is taken at the scale that the kernel has, 1 / tau times log2 e in fp32."""
+    T = 4096
+    g = torch.Generator(device="cuda")
+    g.manual_seed(42)
+    x = (torch.randn(T, V, generator=g, device="cuda") * 2.5)
+    y = torch.randint(0, V, (T,), generator=g, device="cuda")
+    x[torch.arange(T, device="cuda"), y] += 2 + 12 * torch.rand(T, generator=g, device="cuda")
+    x = x.to(DT[dtype])
+    f = lambda v: torch.tensor(v, dtype=torch.float32)  # noqa: E731
+    scale = float((f(1.0) / f(tau)) * f(1.4426950408889634)) * math.log(2.0)
+    want = torch.cat([torch.log_softmax(x[a:a + 64].double() * scale, 1).gather(1, y[a:a + 64, None])[:, 0]
+                      for a in range(0, T, 64)])
+    lp = torch.zeros(T, device="cuda")
+    tl.tl_token_logprob(lctx, x, y, lp, temperature=tau)
+    q2 = float((want.float().double() - want).square().mean())
+    assert abs(float((lp.double() - want).mean())) <= 2.0 ** -24 + 5 * math.sqrt(q2 + 5e-7 ** 2) / math.sqrt(T)
+
+
 def test_rewards_of_long_sequences(lctx):
     """beta times a sum of 4,000 rows' lp - ref.  Per row the errors of the test above, rms 3.5e-7
     and mean 1.5e-7; lp - ref (at most 2) rounds by 1.2e-7 more, unbiased."""
