@@ -226,6 +226,21 @@ def test_rewards_of_long_sequences(lctx):
     close(rew, exact.cpu(), tol, "reward")
 
 
+# --------------------------------------------------------- rows outside every sequence
+
+def test_rows_outside_every_sequence(lctx):
+    """They are in no sum and have a zero gradient, NaN logits or not; their logp is what it is."""
+    T, V, seq = 12, 700, [2, 5, 7, 7, 10]
+    g, x, y = base.make(T, V, "f32", 33, masked=0.0)
+    x[11, 3] = NAN
+    got = base.run_preference(lctx, x, y, seq, 2, seed=4.0)
+    sane = torch.nan_to_num(x)
+    want = R.preference(sane, y, seq, 2, seed=4.0)
+    want["logp"][11] = NAN
+    base.check_preference(got, want, sane, y, seq, 2, "f32", 0.1, 1.0, 4.0, None)
+    assert float(got["dx"][[0, 1, 10, 11]].abs().max()) == 0.0
+
+
 # ------------------------------------------------------------------------- refusals
 
 def test_nothing_that_is_given_is_dropped(lctx):
