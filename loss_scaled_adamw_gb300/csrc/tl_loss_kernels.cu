@@ -543,12 +543,15 @@ struct RowShape {
 // read misses L2 (2,432 rows of 50,000: 63 % of the copy rate, one at a time 79 %).
 //
 // What bounds it: the longest rows, memory (4,096 x 128,256 bf16, one in eight ignored:
-// log-probabilities 131 us, 7.0 TB/s; policy 321 us, 6.1 TB/s, 92 % of the copy rate);
+// log-probabilities 135 us, 6.8 TB/s; policy 322 us, 6.1 TB/s, 92 % of the copy rate);
 // rows below about 10,000 entries, the chain from a row's last element to its factors, with
 // 16 instructions per element in the passes.  Ring and grid: three tiles of 32 KB per CTA of
 // 256 threads, two CTAs per SM, measured against 4 and 16 vectors per thread, two and four
 // tiles, three CTAs per SM, 64 to 512 threads, and groups of 1 to 8 CTAs.
-// POW: distillation with both terms at temperatures that differ, two sums per row (DUAL).
+// POW: distillation with both terms at temperatures that differ, two sums per row (DUAL).  4,096 x
+// 128,256 bf16, 64 entries: 398 us at temperature 2 (POW 2), 418 at 4 (POW 4), 451 at 3 (POW 0, a
+// second exponential per element), 377 at 1 (one sum).  The 16-bit
+// POW 0 forms spill 4 to 28 bytes per thread, that of POW 4 with 128 threads 8 to 12.
 template <typename T, int OP, int B, int POW>
 __global__ void __launch_bounds__(B + 32, B == 256 ? 2 : B == 128 ? 4 : 6) k_row(const LossArgs a, const int clog) {
     constexpr int N = Vec<T>::N, U = 4, tile = B * kTileVecs, ST = kStages, nw = B / 32;
@@ -1119,7 +1122,8 @@ __device__ __forceinline__ float ex2_again(float v) {
     return r;
 }
 
-// Many short rows: a warp per row, the row in its registers (NV vectors per lane), no barrier
+// Many short rows: a warp per row, the row in its registers (NV vectors per lane; policy with 17
+// vectors of 16-bit logits does not fit 128 of them and spills 328 bytes per thread), no barrier
 // at all.  What bounds it: instructions, about 300 for a row besides 11 per element, and the
 // latency of a row's loads with 16 to 24 warps per SM.  Share of the copy rate on 16,384 bf16
 // rows against k_row: policy 37 / 17 % at 1,000 entries, 39 / 25 at 2,001, 65 / 51 at 4,096;
