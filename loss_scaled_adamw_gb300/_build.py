@@ -22,6 +22,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtl_gb300.so")
 SOURCES = ["tl_kernels.cu", "tl_kernels_split.cu", "tl_api.cu", "tl_noalloc.cu", "tl_loss_kernels.cu", "tl_loss_api.cu"]
 HEADERS = [os.path.join(CSRC, "tl_internal.cuh"), os.path.join(CSRC, "tl_loss_internal.cuh"),
+           os.path.join(CSRC, "tl_loss_device.cuh"), os.path.join(CSRC, "tl_spans.h"),
            os.path.join(ROOT, "include", "tl.h"), os.path.join(ROOT, "include", "tl_loss.h")]
 BIND = os.path.join(PKG, "_loss_bind.so")
 BIND_SOURCE = os.path.join(CSRC, "tl_loss_bind.cpp")

@@ -2,6 +2,7 @@
 // context (scratch for row statistics and sums), the checks of every argument
 // before any launch, and the launches.
 #include "tl_loss_internal.cuh"
+#include "tl_spans.h"
 
 #include <cfloat>
 #include <cmath>
@@ -42,54 +43,7 @@ int cuda_fail(tl_loss_ctx* ctx, cudaError_t e, const char* what) noexcept {
     return fail(ctx, TL_ECUDA, what, cudaGetErrorString(e));
 }
 
-bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-bool float_type(int dt) { return dt == TL_F32 || dt == TL_BF16 || dt == TL_F16; }
-int64_t type_bytes(int dt) { return dt == TL_F32 ? 4 : 2; }
 bool weight(float v) { return v >= 0.0f && std::isfinite(v); }
-
-// Element offsets stay far from 2^63: rows < 2^31, ld < 2^40 would reach 2^71, so
-// the product is bounded too.
-constexpr int64_t kMaxLd = int64_t(1) << 40;
-constexpr int64_t kMaxSpan = int64_t(1) << 56;
-
-// The memory a call touches: no output may share bytes with anything else.
-struct Spans {
-    struct One {
-        uintptr_t lo, hi;
-        bool out;
-    } v[16];
-    int n = 0;
-    void add(const void* p, int64_t bytes, bool out) {
-        if (p == nullptr || bytes <= 0) return;
-        const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-        v[n++] = {lo, lo + uintptr_t(bytes), out};
-    }
-    bool clash() const {
-        for (int i = 0; i < n; ++i)
-            for (int j = i + 1; j < n; ++j)
-                if ((v[i].out || v[j].out) && v[i].lo < v[j].hi && v[j].lo < v[i].hi) return true;
-        return false;
-    }
-};
-
-int64_t span_bytes(int64_t rows, int64_t cols, int64_t ld, int64_t size) {
-    return rows < 1 || cols < 1 ? 0 : ((rows - 1) * ld + cols) * size;
-}
-
-// Whether two row-strided matrices of one shape share an element: equal strides
-// interleave when their columns stay apart, others are held to disjoint spans.
-bool rows_clash(const tl_logits& x, const void* d, int64_t ldd) {
-    const int64_t size = type_bytes(x.dtype);
-    const uintptr_t a = reinterpret_cast<uintptr_t>(x.data), b = reinterpret_cast<uintptr_t>(d);
-    const uintptr_t ahi = a + uintptr_t(span_bytes(x.rows, x.vocab, x.ld, size));
-    const uintptr_t bhi = b + uintptr_t(span_bytes(x.rows, x.vocab, ldd, size));
-    if (a >= bhi || b >= ahi) return false;
-    if (x.ld != ldd) return true;
-    if (a == b) return false;   // in place
-    const uintptr_t stride = uintptr_t(x.ld * size), width = uintptr_t(x.vocab * size);
-    const uintptr_t off = (a < b ? b - a : a - b) % stride;
-    return off < width || off + width > stride;
-}
 
 int check_device(tl_loss_ctx* ctx) {
     int dev = -1;
@@ -141,6 +95,17 @@ int check_target(tl_loss_ctx* ctx, const tl_logits* x, const int64_t* target, bo
     return TL_OK;
 }
 
+int check_dlogits(tl_loss_ctx* ctx, const tl_logits* x, const void* dlogits, int64_t ld, bool required) {
+    if (dlogits == nullptr) return required ? fail(ctx, TL_EINVAL, "dlogits must not be NULL") : TL_OK;
+    const int64_t size = type_bytes(x->dtype);
+    if (!aligned(dlogits, uintptr_t(size))) return fail(ctx, TL_EINVAL, "dlogits must be aligned to their element size");
+    if (ld < x->vocab || ld >= kMaxLd) return fail(ctx, TL_EINVAL, "ld_dlogits must be in [vocab, 2^40)");
+    if (x->rows > 0 && ld > kMaxSpan / x->rows) return fail(ctx, TL_EINVAL, "rows * ld_dlogits must be at most 2^56");
+    if (rows_clash(x->data, x->ld, dlogits, ld, x->rows, x->vocab, size))
+        return fail(ctx, TL_EINVAL, "dlogits overlap the logits without being the same tensor");
+    return TL_OK;
+}
+
 // The outputs of a loss call; `losses`: how many floats out->loss holds.
 int check_out(tl_loss_ctx* ctx, const tl_logits* x, const tl_loss_out* o, int64_t losses, LossArgs& a, Spans& sp) {
     if (o == nullptr) return fail(ctx, TL_EINVAL, "out must not be NULL");
@@ -150,16 +115,7 @@ int check_out(tl_loss_ctx* ctx, const tl_logits* x, const tl_loss_out* o, int64_
     if ((rc = check_floats(ctx, o->logp, false, "logp")) != TL_OK) return rc;
     if ((rc = check_floats(ctx, o->loss, false, "loss")) != TL_OK) return rc;
     if ((rc = check_floats(ctx, o->result, true, "result")) != TL_OK) return rc;
-    if (o->dlogits != nullptr) {
-        if (!aligned(o->dlogits, uintptr_t(type_bytes(x->dtype))))
-            return fail(ctx, TL_EINVAL, "dlogits must be aligned to their element size");
-        if (o->ld_dlogits < x->vocab || o->ld_dlogits >= kMaxLd)
-            return fail(ctx, TL_EINVAL, "ld_dlogits must be in [vocab, 2^40)");
-        if (x->rows > 0 && o->ld_dlogits > kMaxSpan / x->rows)
-            return fail(ctx, TL_EINVAL, "rows * ld_dlogits must be at most 2^56");
-        if (rows_clash(*x, o->dlogits, o->ld_dlogits))
-            return fail(ctx, TL_EINVAL, "dlogits overlap the logits without being the same tensor");
-    }
+    if ((rc = check_dlogits(ctx, x, o->dlogits, o->ld_dlogits, false)) != TL_OK) return rc;
     a.dx = o->dlogits;
     a.ldd = o->ld_dlogits;
     a.seed = o->seed;
