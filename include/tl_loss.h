@@ -19,6 +19,11 @@
  *                        rejected sequence)
  *   tl_distill_loss      distillation from a teacher's top-k logits, with or
  *                        without the cross-entropy of the labels
+ *   tl_token_stats       log-probabilities of given tokens with the entropies and
+ *                        the likeliest alternatives of their rows (among them a
+ *                        teacher's entries for tl_distill_loss)
+ *   tl_token_grad        the gradient of the logits for an objective of the
+ *                        caller's own over those log-probabilities and entropies
  *
  * Rows.  Row t of the logits is scored against target[t].  A row with
  * target[t] < 0 is ignored: it adds nothing to any sum, its gradient row is
@@ -177,6 +182,60 @@ typedef struct {
 
 int tl_distill_loss(tl_loss_ctx* ctx, const tl_logits* logits, const tl_distill_args* args, const tl_loss_out* out,
                     tl_stream stream);
+
+/* What the forward keeps of a row for the backward: log q_j = (x_j - max) /
+ * temperature - log_sum, so max / temperature + log_sum is the logarithm of the
+ * row's sum of exponentials. */
+typedef struct {
+    float max;       /* largest logit */
+    float log_sum;   /* log sum_j exp((x_j - max) / temperature) */
+    float entropy;
+} tl_token_saved;
+
+/* Log-probabilities, entropies and alternatives.  Per valid row, with log q the
+ * log-softmax of the logits / temperature:
+ *   logp     = log q_target
+ *   entropy  = -sum_j q_j log q_j
+ *   top      the k largest logits, the largest first and the lower id first among
+ *            equal ones: their ids and log q.  Excluded tokens (-inf) are never
+ *            among them; places without an entry (k above the number of others)
+ *            hold id -1 and -inf.
+ * Every output may be NULL, not all of them.  Of an ignored row the outputs are 0
+ * and its ids -1.  A target of vocab or more makes logp NaN and nothing else; a row
+ * without a softmax has NaN outputs and ids of -1.  Ids and their log-probabilities
+ * are what tl_distill_loss takes as a teacher's entries: a common offset of the
+ * logits leaves its softmax as it is, at temperature 1 here and any there. */
+typedef struct {
+    const int64_t* target;   /* NULL: every row is valid (logp must be NULL) */
+    float* logp;             /* rows floats, or NULL */
+    float* entropy;          /* rows floats, or NULL */
+    tl_token_saved* saved;   /* rows entries, or NULL */
+    void* top_id;            /* rows x k ids, row t at t * ld_top; NULL where k = 0 */
+    float* top_logp;         /* rows x k floats, row t at t * ld_top; NULL where k = 0 */
+    int64_t ld_top;          /* >= k */
+    int32_t k;               /* 0 .. 256 */
+    int32_t id_bytes;        /* 4 or 8 (k > 0) */
+} tl_token_stats_args;
+
+int tl_token_stats(tl_loss_ctx* ctx, const tl_logits* logits, const tl_token_stats_args* args, tl_stream stream);
+
+/* dlogits = d/dlogits of seed * sum_t (grad_logp[t] * logp[t] + grad_entropy[t] *
+ * entropy[t]): per valid row
+ *   seed / temperature * (grad_logp (1[j = target] - q_j) - grad_entropy q_j (log q_j + entropy))
+ * saved is what tl_token_stats wrote for these logits at this temperature; the
+ * gradients are those of the caller's objective (its own 1 / n included).  Rows
+ * whose softmax is missing, or whose target is vocab or more, are NaN. */
+typedef struct {
+    const int64_t* target;        /* NULL: every row is valid (grad_logp must be NULL) */
+    const tl_token_saved* saved;
+    const float* grad_logp;       /* rows floats, or NULL: 0 */
+    const float* grad_entropy;    /* rows floats, or NULL: 0; not both NULL */
+    const float* seed;            /* device float (S); NULL: 1 */
+    void* dlogits;                /* logits' dtype, row t at t * ld_dlogits */
+    int64_t ld_dlogits;           /* >= vocab, < 2^40 */
+} tl_token_grad_args;
+
+int tl_token_grad(tl_loss_ctx* ctx, const tl_logits* logits, const tl_token_grad_args* args, tl_stream stream);
 
 /* Kernels launched so far, and the text of the last error. */
 int64_t tl_loss_launch_count(const tl_loss_ctx* ctx);

@@ -430,13 +430,18 @@ def tl_unscale_norm_noalloc(numel: Sequence[int], accs, S: float, max_norm: floa
 
 _LOSSES = ("tl_loss_create", "tl_loss_destroy", "tl_loss_launch_count", "tl_token_logprob", "tl_policy_loss",
            "tl_preference_loss", "tl_distill_loss", "LossContext", "LOSS_EXPORTED", "tl_logits", "tl_loss_result",
-           "tl_loss_out", "tl_policy_args", "tl_preference_args", "tl_distill_args")
+           "tl_loss_out", "tl_policy_args", "tl_preference_args", "tl_distill_args", "tl_token_stats", "tl_token_grad",
+           "tl_token_saved", "tl_token_stats_args", "tl_token_grad_args")
+_DROPOUT = ("tl_dropout", "tl_dropout_args", "DROPOUT_EXPORTED")
 
 
 def __getattr__(name: str):
-    """The objectives over logits (losses.py) import torch, which the optimizer step's
-    binding does without until a stream is needed: they are loaded when first used."""
+    """The objectives over logits (losses.py) and dropout (dropout.py) import torch, which the
+    optimizer step's binding does without until a stream is needed: they are loaded when first used."""
     if name in _LOSSES:
         from . import losses
         return getattr(losses, name)
+    if name in _DROPOUT:
+        from . import dropout
+        return getattr(dropout, name)
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

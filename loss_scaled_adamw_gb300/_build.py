@@ -20,10 +20,12 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtl_gb300.so")
-SOURCES = ["tl_kernels.cu", "tl_kernels_split.cu", "tl_api.cu", "tl_noalloc.cu", "tl_loss_kernels.cu", "tl_loss_api.cu"]
+SOURCES = ["tl_kernels.cu", "tl_kernels_split.cu", "tl_api.cu", "tl_noalloc.cu", "tl_loss_kernels.cu", "tl_stats_kernels.cu",
+           "tl_loss_api.cu", "tl_dropout.cu"]
 HEADERS = [os.path.join(CSRC, "tl_internal.cuh"), os.path.join(CSRC, "tl_loss_internal.cuh"),
            os.path.join(CSRC, "tl_loss_device.cuh"), os.path.join(CSRC, "tl_spans.h"),
-           os.path.join(ROOT, "include", "tl.h"), os.path.join(ROOT, "include", "tl_loss.h")]
+           os.path.join(ROOT, "include", "tl.h"), os.path.join(ROOT, "include", "tl_loss.h"),
+           os.path.join(ROOT, "include", "tl_dropout.h")]
 BIND = os.path.join(PKG, "_loss_bind.so")
 BIND_SOURCE = os.path.join(CSRC, "tl_loss_bind.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -1,0 +1,215 @@
+// tl_dropout.cu - dropout whose mask is never stored (include/tl_dropout.h): the kernels, the checks
+// of arguments and the launch.
+//
+// Mathematics.  Eight consecutive elements share one block of Philox4x32-10, 128 bits made of the
+// block's number, the key that the device reads, and the site: 16 bits per element, compared with
+// P = round(65536 p).  The number in the high half of a word w is >= P where w >= P << 16, that in
+// the low half where w << 16 is: no number is taken out of its word.
+#include "tl_loss_device.cuh"
+#include "tl_spans.h"
+
+#include <cmath>
+
+#include "../../include/tl_dropout.h"
+
+namespace tl {
+namespace {
+
+struct DropoutArgs {
+    const void* x;
+    const void* residual;
+    void* y;
+    int64_t rows, cols, ldx, ldr, ldy;
+    const int64_t* key;
+    uint32_t site;
+    uint32_t limit;      // P << 16; kept where a number is not below it
+    bool random;         // else nothing is drawn: all numbers are 0
+    float scale;         // 1 / (1 - P / 65536)
+};
+
+struct Philox {
+    uint32_t k0, k1, ticket, above, site;
+    __device__ __forceinline__ explicit Philox(const DropoutArgs& a) {
+        const uint64_t seed = uint64_t(a.key[0]), t = uint64_t(a.key[1]);
+        k0 = uint32_t(seed);
+        k1 = uint32_t(seed >> 32);
+        ticket = uint32_t(t);
+        above = uint32_t(t >> 32) << 8;
+        site = a.site;
+    }
+    // The four words of block b: ten rounds.
+    __device__ __forceinline__ uint4 operator()(uint64_t b) const {
+        uint32_t c0 = uint32_t(b), c1 = uint32_t(b >> 32) | above, c2 = ticket, c3 = site, q0 = k0, q1 = k1;
+#pragma unroll
+        for (int i = 0; i < 10; ++i) {
+            const uint64_t p0 = uint64_t(c0) * 0xD2511F53u, p1 = uint64_t(c2) * 0xCD9E8D57u;
+            c0 = uint32_t(p1 >> 32) ^ c1 ^ q0;
+            c1 = uint32_t(p1);
+            c2 = uint32_t(p0 >> 32) ^ c3 ^ q1;
+            c3 = uint32_t(p0);
+            q0 += 0x9E3779B9u;
+            q1 += 0xBB67AE85u;
+        }
+        return make_uint4(c0, c1, c2, c3);
+    }
+};
+
+__device__ __forceinline__ uint32_t word_of(const uint4& w, int i) { return i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w; }
+
+// Element `place` of a block.
+__device__ __forceinline__ bool kept(uint32_t word, int place, uint32_t limit) {
+    return (place & 1 ? word : word << 16) >= limit;
+}
+__device__ __forceinline__ float dropped(float x, bool keep, float scale, float residual) {
+    return keep ? __fmaf_rn(x, scale, residual) : residual;
+}
+
+// Whole blocks of eight elements in 16-byte vectors.  `chunks` blocks to a row; rows without gaps are
+// one row.
+template <typename T, bool RES, int NB, int TB>
+__global__ void __launch_bounds__(TB) k_dropout(const DropoutArgs a, const int64_t blocks, const int64_t chunks) {
+    constexpr int N = Vec<T>::N, VB = 8 / N;   // vectors to a block
+    const Philox draw(a);
+    uint4 x[NB][VB], res[RES ? NB : 1][VB];
+    int64_t row[NB], col[NB];
+    const int64_t first = int64_t(blockIdx.x) * (NB * TB) + threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+        const int64_t b = first + i * TB;
+        row[i] = a.rows == 1 ? 0 : b / chunks;
+        col[i] = (b - row[i] * chunks) * 8;
+        if (b < blocks) {
+#pragma unroll
+            for (int v = 0; v < VB; ++v) {
+                x[i][v] = ld16(static_cast<const T*>(a.x) + row[i] * a.ldx + col[i] + v * N);
+                if (RES) res[i][v] = ld16(static_cast<const T*>(a.residual) + row[i] * a.ldr + col[i] + v * N);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+        const int64_t b = first + i * TB;
+        if (b >= blocks) continue;
+        const uint4 bits = a.random ? draw(uint64_t(b)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int v = 0; v < VB; ++v) {
+            float f[N], g[N];
+            Vec<T>::wide(x[i][v], f);
+            if (RES) Vec<T>::wide(res[i][v], g);
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const int e = v * N + j;
+                f[j] = dropped(f[j], kept(word_of(bits, e >> 1), e, a.limit), a.scale, RES ? g[j] : 0.0f);
+            }
+            st16(static_cast<T*>(a.y) + row[i] * a.ldy + col[i] + v * N, Vec<T>::narrow(f));
+        }
+    }
+    // the elements behind the last whole block (of the one row)
+    const int64_t n = blocks * 8 + threadIdx.x;
+    if (blockIdx.x == 0 && a.rows == 1 && n < a.cols) {
+        const uint4 bits = a.random ? draw(uint64_t(blocks)) : make_uint4(0, 0, 0, 0);
+        const float r = RES ? to_f(static_cast<const T*>(a.residual)[n]) : 0.0f;
+        const bool keep = kept(word_of(bits, int(threadIdx.x) >> 1), int(threadIdx.x), a.limit);
+        static_cast<T*>(a.y)[n] = from_f<T>(dropped(to_f(static_cast<const T*>(a.x)[n]), keep, a.scale, r));
+    }
+}
+
+// Any strides and alignment, by elements: a warp draws 32 blocks, one per lane, and takes their 256
+// elements in order, so that its accesses are of neighbouring elements.
+template <typename T, bool RES, int TB>
+__global__ void __launch_bounds__(TB) k_dropout_any(const DropoutArgs a, const int64_t numel) {
+    __shared__ uint4 bits[TB];
+    const Philox draw(a);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t first = (int64_t(blockIdx.x) * (TB / 32) + warp) * 256;
+    if (first >= numel) return;
+    bits[threadIdx.x] = a.random ? draw(uint64_t(first >> 3) + lane) : make_uint4(0, 0, 0, 0);
+    __syncwarp();
+    const uint32_t* const words = reinterpret_cast<const uint32_t*>(bits + warp * 32);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t e = first + 32 * i + lane;
+        if (e >= numel) break;
+        const int64_t row = a.rows == 1 ? 0 : e / a.cols, col = e - row * a.cols;
+        const float x = to_f(static_cast<const T*>(a.x)[row * a.ldx + col]);
+        const float r = RES ? to_f(static_cast<const T*>(a.residual)[row * a.ldr + col]) : 0.0f;
+        const bool keep = kept(words[(32 * i + lane) >> 1], lane, a.limit);
+        static_cast<T*>(a.y)[row * a.ldy + col] = from_f<T>(dropped(x, keep, a.scale, r));
+    }
+}
+
+template <typename T, bool RES>
+cudaError_t launch(DropoutArgs a, cudaStream_t s) {
+    constexpr int NB = Vec<T>::N / (RES ? 2 : 1), TB = 256;
+    const int64_t numel = a.rows * a.cols;
+    if (a.rows > 1 && a.ldx == a.cols && a.ldy == a.cols && (!RES || a.ldr == a.cols)) {   // no gaps
+        a.rows = 1;
+        a.cols = a.ldx = a.ldr = a.ldy = numel;
+    }
+    bool whole = aligned(a.x, 16) && aligned(a.y, 16) && (!RES || aligned(a.residual, 16));
+    if (a.rows > 1) whole = whole && a.cols % 8 == 0 && a.ldx % 8 == 0 && a.ldy % 8 == 0 && (!RES || a.ldr % 8 == 0);
+    const int64_t per = whole ? int64_t(NB) * TB * 8 : int64_t(TB) * 8, ctas = (numel + per - 1) / per;
+    if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
+    if (whole)
+        k_dropout<T, RES, NB, TB><<<unsigned(ctas), TB, 0, s>>>(a, numel / 8, a.cols / 8);
+    else
+        k_dropout_any<T, RES, TB><<<unsigned(ctas), TB, 0, s>>>(a, numel);
+    return cudaGetLastError();
+}
+
+template <typename T> cudaError_t launch_by(const DropoutArgs& a, cudaStream_t s) {
+    return a.residual ? launch<T, true>(a, s) : launch<T, false>(a, s);
+}
+
+// One matrix operand: its address and stride.
+bool operand(const void* p, int64_t ld, int64_t rows, int64_t cols, int64_t size) {
+    return p != nullptr && aligned(p, uintptr_t(size)) && ld >= cols && (rows == 1 || (ld < kMaxLd && ld <= kMaxSpan / rows));
+}
+
+}  // namespace
+}  // namespace tl
+
+using namespace tl;
+
+extern "C" int tl_dropout(const tl_dropout_args* args, tl_stream stream) {
+    if (args == nullptr) return TL_EINVAL;
+    const tl_dropout_args& g = *args;
+    if (!float_type(g.dtype) || !(g.p >= 0.0f && g.p <= 1.0f)) return TL_EINVAL;
+    if (g.rows < 0 || g.cols < 0 || (g.rows > 0 && g.cols > (int64_t(1) << 43) / g.rows)) return TL_EINVAL;
+    if (g.key == nullptr || !aligned(g.key, 8)) return TL_EINVAL;
+    const int64_t size = type_bytes(g.dtype);
+    if (g.rows > 0 && g.cols > 0) {
+        if (!operand(g.x, g.ldx, g.rows, g.cols, size) || !operand(g.y, g.ldy, g.rows, g.cols, size)) return TL_EINVAL;
+        if (g.residual != nullptr && !operand(g.residual, g.ldr, g.rows, g.cols, size)) return TL_EINVAL;
+        if (rows_clash(g.x, g.ldx, g.y, g.ldy, g.rows, g.cols, size)) return TL_EINVAL;
+        if (g.residual != nullptr && rows_clash(g.residual, g.ldr, g.y, g.ldy, g.rows, g.cols, size)) return TL_EINVAL;
+        Spans sp;
+        sp.add(g.key, 16, false);
+        sp.add(g.y, span_bytes(g.rows, g.cols, g.ldy, size), true);
+        if (sp.clash()) return TL_EINVAL;
+    }
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) return TL_ECUDA;
+    if (dev != g.device) return TL_ESTATE;
+    if (g.rows == 0 || g.cols == 0) return TL_OK;
+    const uint32_t P = uint32_t(std::lrint(double(g.p) * 65536.0));
+    DropoutArgs a{};
+    a.x = g.x;
+    a.residual = g.residual;
+    a.y = g.y;
+    a.rows = g.rows;
+    a.cols = g.cols;
+    a.ldx = g.ldx;
+    a.ldr = g.ldr;
+    a.ldy = g.ldy;
+    a.key = g.key;
+    a.site = g.site;
+    // where all or none are kept nothing is drawn: 0 is kept, or below the limit
+    a.random = P > 0 && P < 65536;
+    a.limit = P < 65536 ? P << 16 : 1u;
+    a.scale = P < 65536 ? float(65536.0 / (65536.0 - double(P))) : 0.0f;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = g.dtype == TL_F32 ? launch_by<float>(a, s)
+                          : g.dtype == TL_BF16 ? launch_by<__nv_bfloat16>(a, s) : launch_by<__half>(a, s);
+    return e == cudaSuccess ? TL_OK : TL_ECUDA;
+}

@@ -327,6 +327,107 @@ int tl_distill_loss(tl_loss_ctx* ctx, const tl_logits* logits, const tl_distill_
     return run_rows(ctx, kDistill, logits->dtype, a, stream);
 }
 
+int tl_token_stats(tl_loss_ctx* ctx, const tl_logits* logits, const tl_token_stats_args* args, tl_stream stream) {
+    if (ctx == nullptr) return TL_EINVAL;
+    int rc;
+    if ((rc = check_logits(ctx, logits)) != TL_OK) return rc;
+    if (args == nullptr) return fail(ctx, TL_EINVAL, "args must not be NULL");
+    const int64_t rows = logits->rows;
+    if ((rc = check_target(ctx, logits, args->target, args->logp != nullptr)) != TL_OK) return rc;
+    if ((rc = check_floats(ctx, args->logp, false, "logp")) != TL_OK) return rc;
+    if ((rc = check_floats(ctx, args->entropy, false, "entropy")) != TL_OK) return rc;
+    if ((rc = check_floats(ctx, args->saved, false, "saved")) != TL_OK) return rc;
+    if (args->k < 0 || args->k > kMaxAlternatives) return fail(ctx, TL_EINVAL, "k must be in [0, 256]");
+    if (args->k > 0) {
+        if (args->id_bytes != 4 && args->id_bytes != 8) return fail(ctx, TL_EINVAL, "id_bytes must be 4 or 8");
+        if (args->ld_top < args->k || args->ld_top >= kMaxLd || (rows > 0 && args->ld_top > kMaxSpan / rows))
+            return fail(ctx, TL_EINVAL, "ld_top must be in [k, 2^40), rows * ld_top at most 2^56");
+        if (rows > 0 && (args->top_id == nullptr || !aligned(args->top_id, uintptr_t(args->id_bytes))))
+            return fail(ctx, TL_EINVAL, "top_id", "missing or misaligned");
+        if ((rc = check_floats(ctx, args->top_logp, rows > 0, "top_logp")) != TL_OK) return rc;
+    } else if (args->top_id != nullptr || args->top_logp != nullptr) {
+        return fail(ctx, TL_EINVAL, "alternatives without k");
+    }
+    if (rows > 0 && args->k == 0 && args->logp == nullptr && args->entropy == nullptr && args->saved == nullptr)
+        return fail(ctx, TL_EINVAL, "no output is asked for");
+    StatsArgs a{};
+    a.x = logits->data;
+    a.ld = logits->ld;
+    a.rows = rows;
+    a.vocab = int32_t(logits->vocab);
+    a.it = 1.0f / logits->temperature;
+    a.target = args->target;
+    a.logp = args->logp;
+    a.entropy = args->entropy;
+    a.saved = reinterpret_cast<float*>(args->saved);
+    a.k = args->k;
+    if (a.k > 0) {
+        a.top_id = args->top_id;
+        a.top_logp = args->top_logp;
+        a.ld_top = args->ld_top;
+        a.id_bytes = args->id_bytes;
+    }
+    Spans sp;
+    sp.add(a.x, span_bytes(rows, a.vocab, a.ld, type_bytes(logits->dtype)), false);
+    sp.add(a.target, 8 * rows, false);
+    sp.add(a.logp, 4 * rows, true);
+    sp.add(a.entropy, 4 * rows, true);
+    sp.add(a.saved, 12 * rows, true);
+    sp.add(a.top_id, span_bytes(rows, a.k, a.ld_top, a.id_bytes), true);
+    sp.add(a.top_logp, span_bytes(rows, a.k, a.ld_top, 4), true);
+    if (sp.clash()) return fail(ctx, TL_EINVAL, "an output overlaps another argument");
+    if ((rc = check_device(ctx)) != TL_OK) return rc;
+    if (rows == 0) return TL_OK;
+    cudaError_t e = launch_token_stats(logits->dtype, a, ctx->sm_count, ctx->cache, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(ctx, e, "token statistics launch");
+    ctx->launches += 1;
+    return TL_OK;
+}
+
+int tl_token_grad(tl_loss_ctx* ctx, const tl_logits* logits, const tl_token_grad_args* args, tl_stream stream) {
+    if (ctx == nullptr) return TL_EINVAL;
+    int rc;
+    if ((rc = check_logits(ctx, logits)) != TL_OK) return rc;
+    if (args == nullptr) return fail(ctx, TL_EINVAL, "args must not be NULL");
+    const int64_t rows = logits->rows;
+    const bool some = rows > 0;
+    if ((rc = check_target(ctx, logits, args->target, args->grad_logp != nullptr)) != TL_OK) return rc;
+    if ((rc = check_floats(ctx, args->saved, some, "saved")) != TL_OK) return rc;
+    if ((rc = check_floats(ctx, args->grad_logp, false, "grad_logp")) != TL_OK) return rc;
+    if ((rc = check_floats(ctx, args->grad_entropy, false, "grad_entropy")) != TL_OK) return rc;
+    if ((rc = check_floats(ctx, args->seed, false, "seed")) != TL_OK) return rc;
+    if (some && args->grad_logp == nullptr && args->grad_entropy == nullptr)
+        return fail(ctx, TL_EINVAL, "grad_logp and grad_entropy are both missing");
+    if ((rc = check_dlogits(ctx, logits, args->dlogits, args->ld_dlogits, some)) != TL_OK) return rc;
+    TokenGradArgs a{};
+    a.x = logits->data;
+    a.ld = logits->ld;
+    a.rows = rows;
+    a.vocab = int32_t(logits->vocab);
+    a.it = 1.0f / logits->temperature;
+    a.target = args->target;
+    a.saved = reinterpret_cast<const float*>(args->saved);
+    a.grad_logp = args->grad_logp;
+    a.grad_entropy = args->grad_entropy;
+    a.seed = args->seed;
+    a.dx = args->dlogits;
+    a.ldd = args->ld_dlogits;
+    Spans sp;   // the logits are dlogits' own memory or have been found apart from it
+    sp.add(a.dx, span_bytes(rows, a.vocab, a.ldd, type_bytes(logits->dtype)), true);
+    sp.add(a.target, 8 * rows, false);
+    sp.add(a.saved, 12 * rows, false);
+    sp.add(a.grad_logp, 4 * rows, false);
+    sp.add(a.grad_entropy, 4 * rows, false);
+    sp.add(a.seed, 4, false);
+    if (sp.clash()) return fail(ctx, TL_EINVAL, "an output overlaps another argument");
+    if ((rc = check_device(ctx)) != TL_OK) return rc;
+    if (rows == 0) return TL_OK;
+    cudaError_t e = launch_token_grad(logits->dtype, a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(ctx, e, "token gradient launch");
+    ctx->launches += 1;
+    return TL_OK;
+}
+
 int64_t tl_loss_launch_count(const tl_loss_ctx* ctx) { return ctx == nullptr ? 0 : ctx->launches; }
 
 const char* tl_loss_last_error(const tl_loss_ctx* ctx) { return ctx == nullptr ? "" : ctx->last_error.c_str(); }

@@ -1,5 +1,5 @@
-// tl_loss_bind.cpp - the objectives' calls (include/tl_loss.h) as a CPython module that reads
-// torch tensors directly.  It checks and marshals arguments and nothing else.
+// tl_loss_bind.cpp - the objectives' calls (include/tl_loss.h) and dropout (include/tl_dropout.h) as a
+// CPython module that reads torch tensors directly.  It checks and marshals arguments and nothing else.
 //
 // Why not ctypes, as the rest of the binding: a loss call passes up to twelve tensors, and
 // asking each for its type, size, layout, device and address through Python costs about 0.4 us
@@ -14,6 +14,7 @@
 
 #include <torch/csrc/autograd/python_variable.h>
 
+#include "../../include/tl_dropout.h"
 #include "../../include/tl_loss.h"
 
 namespace {
@@ -102,19 +103,27 @@ const float* seed_of(PyObject* o, long device) {
     return p;
 }
 
+void gradient(PyObject* o, const tl_logits& x, long device, void*& data, int64_t& ld) {
+    const Matrix d = matrix(o, device, "dlogits");
+    if (float_type(d.type) != x.dtype || d.rows != x.rows || d.cols != x.vocab)
+        refuse("dlogits", "of the logits' shape and dtype");
+    data = d.data;
+    ld = d.ld;
+}
+
+// The three floats per row that the forward saves.
+tl_token_saved* saved_of(PyObject* o, int64_t rows, long device) {
+    if (o != Py_None && (tensor(o, "saved").dim() != 2 || tensor(o, "saved").size(1) != 3)) refuse("saved", "[rows, 3]");
+    return reinterpret_cast<tl_token_saved*>(floats(o, 3 * rows, device, "saved"));
+}
+
 // n, seed, dlogits, logp, loss (of `losses` elements), result
 tl_loss_out outputs(PyObject* n, PyObject* seed, PyObject* dlogits, PyObject* logp, PyObject* loss, int64_t losses,
                     PyObject* result, const tl_logits& x, long device) {
     tl_loss_out o{};
     o.n = whole(n);
     o.seed = seed_of(seed, device);
-    if (dlogits != Py_None) {
-        const Matrix d = matrix(dlogits, device, "dlogits");
-        if (float_type(d.type) != x.dtype || d.rows != x.rows || d.cols != x.vocab)
-            refuse("dlogits", "of the logits' shape and dtype");
-        o.dlogits = d.data;
-        o.ld_dlogits = d.ld;
-    }
+    if (dlogits != Py_None) gradient(dlogits, x, device, o.dlogits, o.ld_dlogits);
     o.logp = floats(logp, x.rows, device, "logp");
     o.loss = floats(loss, losses, device, "the loss output");
     o.result = reinterpret_cast<tl_loss_result*>(floats(result, 4, device, "result"));
@@ -179,6 +188,86 @@ int distill_loss(PyObject* const* a) {
     return tl_distill_loss(static_cast<tl_loss_ctx*>(address(a[0])), &x, &p, &o, address(a[10]));
 }
 
+// handle, device, logits, temperature, targets, logp, entropy, saved, top_ids, top_logp, stream
+int token_stats(PyObject* const* a) {
+    const long device = static_cast<long>(whole(a[1]));
+    const tl_logits x = logits(a[2], a[3], device);
+    tl_token_stats_args p{};
+    p.target = longs(a[4], x.rows, device, "targets");
+    p.logp = floats(a[5], x.rows, device, "logp");
+    p.entropy = floats(a[6], x.rows, device, "entropy");
+    p.saved = saved_of(a[7], x.rows, device);
+    if (a[8] != Py_None || a[9] != Py_None) {   // one without the other is refused
+        const Matrix ids = matrix(a[8], device, "top_ids"), t = matrix(a[9], device, "top_logp");
+        if (t.rows != x.rows || ids.rows != x.rows || ids.cols != t.cols || ids.ld != t.ld)
+            refuse("top_ids and top_logp", "[rows, k] with one row stride");
+        if (t.type != at::kFloat) refuse("top_logp", "float32");
+        if (t.cols > INT32_MAX) refuse("k", "below 2^31");
+        p.top_id = ids.data;
+        p.top_logp = static_cast<float*>(t.data);
+        p.ld_top = t.ld;
+        p.k = static_cast<int32_t>(t.cols);
+        p.id_bytes = ids.type == at::kInt ? 4 : ids.type == at::kLong ? 8 : -1;
+    }
+    return tl_token_stats(static_cast<tl_loss_ctx*>(address(a[0])), &x, &p, address(a[10]));
+}
+
+// handle, device, logits, temperature, saved, dlogits, targets, grad_logp, grad_entropy, seed, stream
+int token_grad(PyObject* const* a) {
+    const long device = static_cast<long>(whole(a[1]));
+    const tl_logits x = logits(a[2], a[3], device);
+    tl_token_grad_args p{};
+    p.saved = saved_of(a[4], x.rows, device);
+    if (a[5] != Py_None) gradient(a[5], x, device, p.dlogits, p.ld_dlogits);
+    p.target = longs(a[6], x.rows, device, "targets");
+    p.grad_logp = floats(a[7], x.rows, device, "grad_logp");
+    p.grad_entropy = floats(a[8], x.rows, device, "grad_entropy");
+    p.seed = seed_of(a[9], device);
+    return tl_token_grad(static_cast<tl_loss_ctx*>(address(a[0])), &x, &p, address(a[10]));
+}
+
+// x, y, residual, key, site, p, stream, device.  Tensors without gaps are one row, whatever their shape.
+int dropout(PyObject* const* a) {
+    const long device = static_cast<long>(whole(a[7]));
+    const at::Tensor &x = tensor(a[0], "x"), &y = tensor(a[1], "y");
+    const at::Tensor* const res = a[2] == Py_None ? nullptr : &tensor(a[2], "residual");
+    tl_dropout_args p{};
+    p.dtype = float_type(x.scalar_type());
+    if (p.dtype < 0) refuse("x", "float32, bfloat16 or float16");
+    for (const at::Tensor* t : {&x, &y, res}) {
+        if (t == nullptr) continue;
+        if (t->scalar_type() != x.scalar_type() || t->sizes() != x.sizes() || !on_device(*t, device))
+            refuse("y and residual", "of the shape, dtype and device of x");
+    }
+    if (x.is_contiguous() && y.is_contiguous() && (res == nullptr || res->is_contiguous())) {
+        p.x = x.data_ptr();
+        p.y = y.data_ptr();
+        p.residual = res ? res->data_ptr() : nullptr;
+        p.rows = 1;
+        p.cols = p.ldx = p.ldy = p.ldr = x.numel();
+    } else {
+        const Matrix mx = matrix(a[0], device, "x"), my = matrix(a[1], device, "y");
+        p.x = mx.data;
+        p.y = my.data;
+        p.rows = mx.rows;
+        p.cols = mx.cols;
+        p.ldx = mx.ld;
+        p.ldy = my.ld;
+        if (res) {
+            const Matrix mr = matrix(a[2], device, "residual");
+            p.residual = mr.data;
+            p.ldr = mr.ld;
+        }
+    }
+    p.key = longs(a[3], 2, device, "key");
+    const int64_t site = whole(a[4]);
+    if (site < 0 || site > UINT32_MAX) refuse("site", "in [0, 2^32)");
+    p.site = static_cast<uint32_t>(site);
+    p.p = number(a[5]);
+    p.device = static_cast<int32_t>(device);
+    return tl_dropout(&p, address(a[6]));
+}
+
 // No C++ exception leaves the module.
 template <int (*F)(PyObject* const*), Py_ssize_t N>
 PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -203,7 +292,8 @@ template <int (*F)(PyObject* const*), Py_ssize_t N> PyMethodDef method(const cha
 
 PyMethodDef methods[] = {method<token_logprob, 7>("token_logprob"), method<policy_loss, 18>("policy_loss"),
                          method<preference_loss, 17>("preference_loss"), method<distill_loss, 16>("distill_loss"),
-                         {nullptr, nullptr, 0, nullptr}};
+                         method<token_stats, 11>("token_stats"), method<token_grad, 11>("token_grad"),
+                         method<dropout, 8>("dropout"), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_loss_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

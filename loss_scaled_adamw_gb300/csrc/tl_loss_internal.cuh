@@ -1,5 +1,5 @@
-// tl_loss_internal.cuh - types shared by the objective kernels (tl_loss_kernels.cu)
-// and their host side (tl_loss_api.cu).  Not installed; the public interface is
+// tl_loss_internal.cuh - types shared by the kernels over logits (tl_loss_kernels.cu,
+// tl_stats_kernels.cu) and their host side (tl_loss_api.cu).  Not installed; the public interface is
 // include/tl_loss.h.
 #pragma once
 
@@ -69,6 +69,42 @@ struct LossArgs {
     uint32_t* ticket;
 };
 
+constexpr int kMaxAlternatives = 256;  // alternatives per row
+
+// tl_token_stats: a row's softmax statistics and its largest entries.
+struct StatsArgs {
+    const void* x;
+    int64_t ld;
+    int64_t rows;
+    int32_t vocab;
+    float it;              // 1 / temperature
+    const int64_t* target; // null: every row is valid, no logp
+    float* logp;
+    float* entropy;
+    float* saved;          // three per row: largest logit, log of the sum against it, entropy
+    void* top_id;
+    float* top_logp;
+    int64_t ld_top;
+    int32_t k;
+    int32_t id_bytes;
+};
+
+// tl_token_grad: the gradient of log-probabilities and entropies.
+struct TokenGradArgs {
+    const void* x;
+    int64_t ld;
+    int64_t rows;
+    int32_t vocab;
+    float it;
+    const int64_t* target;
+    const float* saved;
+    const float* grad_logp;
+    const float* grad_entropy;
+    const float* seed;
+    void* dx;
+    int64_t ldd;
+};
+
 // Row groups that each kernel form can have resident at once on the context's device
 // (asking the runtime for it costs more than a small launch).  A group waits for
 // nothing outside itself, so this sizes the grid and no more.
@@ -84,5 +120,9 @@ struct GroupCache {
 // Launchers (tl_loss_kernels.cu).  dt: element type of the logits.
 cudaError_t launch_loss_rows(int op, int dt, const LossArgs& a, int sm_count, GroupCache& cache, cudaStream_t s);
 cudaError_t launch_pref_grad(int dt, const LossArgs& a, cudaStream_t s);
+
+// Launchers (tl_stats_kernels.cu).
+cudaError_t launch_token_stats(int dt, const StatsArgs& a, int sm_count, GroupCache& cache, cudaStream_t s);
+cudaError_t launch_token_grad(int dt, const TokenGradArgs& a, cudaStream_t s);
 
 }  // namespace tl

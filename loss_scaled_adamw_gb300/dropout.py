@@ -1,0 +1,45 @@
+"""Dropout whose mask is never stored: Python binding of include/tl_dropout.h.
+
+The mask is a function of a key on the device ([seed, ticket], int64), of the site (which
+dropout of the model) and of an element's place in its tensor, so the backward pass, and a
+micro-batch that is computed again, see it by naming the same key::
+
+    key = torch.tensor([seed, 0], dtype=torch.int64, device="cuda")
+    tl_dropout(branch, hidden, 0.1, key, site=3, residual=hidden)    # hidden += dropout(branch)
+    ...
+    tl_dropout(d_hidden, d_branch, 0.1, key, site=3)                 # the gradient of branch
+    key[1] += 1                                                      # the next micro-batch's ticket
+
+All of it can be captured in a CUDA graph: a replay reads the key anew.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from . import TL_OK, TLError, losses
+
+DROPOUT_EXPORTED = ("tl_dropout",)
+
+_vp, _i64, _i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+
+
+class tl_dropout_args(ctypes.Structure):
+    _fields_ = [("x", _vp), ("residual", _vp), ("y", _vp), ("rows", _i64), ("cols", _i64), ("ldx", _i64), ("ldr", _i64),
+                ("ldy", _i64), ("key", _vp), ("site", ctypes.c_uint32), ("dtype", _i32), ("p", ctypes.c_float),
+                ("device", _i32)]
+
+
+def tl_dropout(x, y, p: float, key, site: int = 0, residual=None, stream=None) -> None:
+    """y = residual + (kept ? x / (1 - p) : 0), p to the nearest multiple of 2^-16.
+
+    x, y and residual: float32, bfloat16 or float16 CUDA tensors of one shape and dtype,
+    contiguous, or 2-D with contiguous rows.  y may be x or the residual itself.  The
+    gradient of x is the same call on the gradient of y, without a residual."""
+    lib = losses._load()
+    if not getattr(x, "is_cuda", False):
+        raise ValueError("x must be a CUDA tensor")
+    device = x.device.index
+    handle = losses._raw_stream(device) if stream is None else losses._any_stream(stream).value
+    rc = losses._bind.dropout(x, y, residual, key, site, p, handle, device)
+    if rc != TL_OK:
+        raise TLError("tl_dropout", rc, lib.tl_status_string(rc).decode())

@@ -25,7 +25,7 @@ from . import TL_OK, TLError, load_library
 from . import _stream as _any_stream
 
 LOSS_EXPORTED = ("tl_loss_create", "tl_loss_destroy", "tl_token_logprob", "tl_policy_loss", "tl_preference_loss",
-                 "tl_distill_loss", "tl_loss_launch_count", "tl_loss_last_error")
+                 "tl_distill_loss", "tl_token_stats", "tl_token_grad", "tl_loss_launch_count", "tl_loss_last_error")
 
 _vp, _i64, _i32, _f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
 
@@ -58,6 +58,20 @@ class tl_distill_args(ctypes.Structure):
                 ("teacher_dtype", _i32), ("id_bytes", _i32), ("kd_weight", _f32), ("ce_weight", _f32)]
 
 
+class tl_token_saved(ctypes.Structure):
+    _fields_ = [("max", _f32), ("log_sum", _f32), ("entropy", _f32)]
+
+
+class tl_token_stats_args(ctypes.Structure):
+    _fields_ = [("target", _vp), ("logp", _vp), ("entropy", _vp), ("saved", _vp), ("top_id", _vp), ("top_logp", _vp),
+                ("ld_top", _i64), ("k", _i32), ("id_bytes", _i32)]
+
+
+class tl_token_grad_args(ctypes.Structure):
+    _fields_ = [("target", _vp), ("saved", _vp), ("grad_logp", _vp), ("grad_entropy", _vp), ("seed", _vp),
+                ("dlogits", _vp), ("ld_dlogits", _i64)]
+
+
 _lib = _bind = None
 _raw_stream = torch._C._cuda_getCurrentRawStream   # current_stream() without its Stream object (3 us a call)
 
@@ -80,6 +94,8 @@ def _load():
                 ("tl_policy_loss", ctypes.c_int, [_vp, P(tl_logits), P(tl_policy_args), P(tl_loss_out), _vp]),
                 ("tl_preference_loss", ctypes.c_int, [_vp, P(tl_logits), P(tl_preference_args), P(tl_loss_out), _vp]),
                 ("tl_distill_loss", ctypes.c_int, [_vp, P(tl_logits), P(tl_distill_args), P(tl_loss_out), _vp]),
+                ("tl_token_stats", ctypes.c_int, [_vp, P(tl_logits), P(tl_token_stats_args), _vp]),
+                ("tl_token_grad", ctypes.c_int, [_vp, P(tl_logits), P(tl_token_grad_args), _vp]),
                 ("tl_loss_launch_count", _i64, [_vp]),
                 ("tl_loss_last_error", ctypes.c_char_p, [_vp])):
             fn = getattr(lib, name)
@@ -178,3 +194,27 @@ def tl_distill_loss(lctx: LossContext, logits, teacher_logits, teacher_ids, n: i
                             _stream(lctx, stream), targets, teacher_logits, teacher_ids, kd_weight, ce_weight)
     if rc != TL_OK:
         _check(lctx, "tl_distill_loss", rc)
+
+
+def tl_token_stats(lctx: LossContext, logits, targets=None, logp=None, entropy=None, top_ids=None, top_logp=None,
+                   saved=None, temperature: float = 1.0, stream=None) -> None:
+    """Log-probabilities of the targets, entropies, and the k likeliest alternatives of each
+    row ([rows, k]: ids int32 or int64, and their log-probabilities, the likeliest first and
+    the lower id first among equal logits).  saved ([rows, 3]: largest logit, log of the sum
+    of exponentials against it, entropy) is what tl_token_grad takes.  The alternatives are
+    what tl_distill_loss takes as a teacher's logits and ids."""
+    rc = _bind.token_stats(lctx._address, lctx.device, logits, temperature, targets, logp, entropy, saved, top_ids,
+                           top_logp, _stream(lctx, stream))
+    if rc != TL_OK:
+        _check(lctx, "tl_token_stats", rc)
+
+
+def tl_token_grad(lctx: LossContext, logits, saved, dlogits, targets=None, grad_logp=None, grad_entropy=None,
+                  temperature: float = 1.0, seed=None, stream=None) -> None:
+    """dlogits (which may be the logits themselves) = the gradient of seed times
+    sum_t grad_logp[t] * logp[t] + grad_entropy[t] * entropy[t], with saved of tl_token_stats
+    for the same logits and temperature.  seed as for tl_policy_loss."""
+    rc = _bind.token_grad(lctx._address, lctx.device, logits, temperature, saved, dlogits, targets, grad_logp,
+                          grad_entropy, seed, _stream(lctx, stream))
+    if rc != TL_OK:
+        _check(lctx, "tl_token_grad", rc)
