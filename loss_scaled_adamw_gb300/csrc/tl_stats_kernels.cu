@@ -39,6 +39,13 @@ __device__ __forceinline__ float exponent(float x, float m, float c2) {
     return fmaxf(big(m, c2) ? (x - m) * c2 : __fmaf_rn(x, c2, -anchor(m, c2)), kLowest);
 }
 
+// log q of an entry x of a row with a softmax.  Roundings of the sum are not let above 0, and an entry at
+// a type's lowest value, whose exponent overflows, has its distance.
+__device__ __forceinline__ float log_q(float x, float M, float u, float c2, bool far, float S, float it) {
+    const float r = log_share(x, M, u, c2, far, S);
+    return fminf(r == kNegInf ? (x - M) * it : r, 0.0f);
+}
+
 // ---------------------------------------------------------------------------
 // The largest entries
 // ---------------------------------------------------------------------------
@@ -92,8 +99,8 @@ template <typename T, int B>
 __global__ void __launch_bounds__(B) k_stats(const StatsArgs a) {
     constexpr int N = Vec<T>::N, nw = B / 32, G = kGroupsPerThread;
     __shared__ float4 parts[nw];
-    __shared__ float gmax[G][B];
-    __shared__ unsigned long long found[kCandidates];
+    extern __shared__ unsigned long long found[];                  // kCandidates
+    float(*const gmax)[B] = reinterpret_cast<float(*)[B]>(found + kCandidates);   // [G][B]
     __shared__ int sums[2][nw], nfound;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const float c2 = a.it * kLog2e, kNaN = __int_as_float(0x7fffffff);
@@ -171,10 +178,10 @@ __global__ void __launch_bounds__(B) k_stats(const StatsArgs a) {
         const bool none = !(fabsf(M) < INFINITY) || S != S;   // no softmax
         const bool far = big(M, c2);
         const float u = anchor(M, c2);
-        auto share = [&](float x) { return none ? kNaN : log_share(x, M, u, c2, far, S); };
+        auto share = [&](float x) { return none ? kNaN : log_q(x, M, u, c2, far, S, a.it); };
         if (tid == 0) {
             const float log_sum = -share(M);
-            const float H = log_sum + ((far ? 0.0f : __fmaf_rn(M, c2, -u)) - W / S) * kLn2;
+            const float H = fmaxf(log_sum + ((far ? 0.0f : __fmaf_rn(M, c2, -u)) - W / S) * kLn2, 0.0f);
             if (a.logp) a.logp[r] = y < a.vocab ? share(to_f(x[y])) : kNaN;
             if (a.entropy) a.entropy[r] = none ? kNaN : H;
             if (a.saved) {
@@ -287,6 +294,7 @@ cudaError_t stats(const StatsArgs& a, int sms, GroupCache& cache, cudaStream_t s
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(1);
     cfg.blockDim = dim3(B);
+    cfg.dynamicSmemBytes = kCandidates * 8 + kGroupsPerThread * B * 4;
     cfg.stream = s;
     int groups = 0;
     cudaError_t e = resident_groups(reinterpret_cast<const void*>(kernel), cfg, RowShape{B, 0}, sms, cache, groups);
