@@ -67,6 +67,9 @@ int check_logits(tl_loss_ctx* ctx, const tl_logits* x) {
     return TL_OK;
 }
 
+// log2(e) / temperature: a rounding of it is common to a row's exponents, and shows in its entropy.
+float exponent_scale(float temperature) { return float(1.4426950408889634 / double(temperature)); }
+
 // Fills the parts of the launch arguments that every call shares.
 void base_args(tl_loss_ctx* ctx, const tl_logits* x, const int64_t* target, LossArgs& a, Spans& sp) {
     a = LossArgs{};
@@ -356,6 +359,7 @@ int tl_token_stats(tl_loss_ctx* ctx, const tl_logits* logits, const tl_token_sta
     a.rows = rows;
     a.vocab = int32_t(logits->vocab);
     a.it = 1.0f / logits->temperature;
+    a.c2 = exponent_scale(logits->temperature);
     a.target = args->target;
     a.logp = args->logp;
     a.entropy = args->entropy;
@@ -405,6 +409,7 @@ int tl_token_grad(tl_loss_ctx* ctx, const tl_logits* logits, const tl_token_grad
     a.rows = rows;
     a.vocab = int32_t(logits->vocab);
     a.it = 1.0f / logits->temperature;
+    a.c2 = exponent_scale(logits->temperature);
     a.target = args->target;
     a.saved = reinterpret_cast<const float*>(args->saved);
     a.grad_logp = args->grad_logp;

@@ -77,7 +77,7 @@ struct StatsArgs {
     int64_t ld;
     int64_t rows;
     int32_t vocab;
-    float it;              // 1 / temperature
+    float it, c2;          // 1 / temperature, and times log2 e (rounded once)
     const int64_t* target; // null: every row is valid, no logp
     float* logp;
     float* entropy;
@@ -95,7 +95,7 @@ struct TokenGradArgs {
     int64_t ld;
     int64_t rows;
     int32_t vocab;
-    float it;
+    float it, c2;
     const int64_t* target;
     const float* saved;
     const float* grad_logp;

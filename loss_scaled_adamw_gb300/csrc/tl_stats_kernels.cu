@@ -69,6 +69,118 @@ __device__ __forceinline__ float max_nan(float v, float least) {
     return r;
 }
 
+// A thread's sums over the elements that it has seen, against a reference near its largest one.
+template <typename T> struct Running {
+    static constexpr int N = Vec<T>::N, U = 4;
+    float m = kNegInf, limit = kNegInf, s = 0.0f, w = 0.0f;
+    float u = 0.0f;      // the reference's whole number
+    bool slow = false;   // element by element, see below
+
+    // 16-bit logits are held above this one (-inf becomes it) before they are widened: one instruction to
+    // two of them, in place of two on their exponents.  That needs the lowest to be far below the
+    // reference, 2^-150 of it.
+    static constexpr float kFloor = sizeof(T) == 4 ? kNegInf : Vec<T>::kEmpty == 0xfc00fc00u ? -65504.0f : -9.9e29f;
+
+    // To a much larger element.  Smaller steps are left: exponentials up to 2^32 of the reference do no harm.
+    __device__ __forceinline__ void raise(float top, float c2) {
+        if (!(top > limit)) return;
+        move_sums(m, top, c2, s, w);
+        m = top;
+        limit = m + 32.0f / c2;
+        slow = big(m, c2) || (sizeof(T) == 2 && !((m - kFloor) * c2 > 150.0f));
+        u = slow ? 0.0f : anchor(m, c2);
+    }
+    __device__ __forceinline__ void add_one(float v, float c2) {
+        const float ref = part_ref(m);
+        const float z = max_nan(big(ref, c2) ? (v - ref) * c2 : __fmaf_rn(v, c2, -anchor(ref, c2)), kLowest), e = ex2(z);
+        s += e;
+        w = __fmaf_rn(e, z, w);
+    }
+    // U vectors, of which the largest element has been through raise().
+    __device__ __forceinline__ void add(const uint4 (&raw)[U], pair_t c2c2, float c2) {
+        if (slow || m == kNegInf) {
+#pragma unroll 1
+            for (int i = 0; i < U; ++i) {
+                const uint4 v = i == 0 ? raw[0] : i == 1 ? raw[1] : i == 2 ? raw[2] : raw[3];
+                float f[N];
+                Vec<T>::wide(v, f);
+#pragma unroll
+                for (int j = 0; j < N; ++j) add_one(f[j], c2);
+            }
+            return;
+        }
+        const pair_t uu = pair_of(-u, -u);
+        pair_t s2 = 0, w2 = 0;   // of these vectors first: see tree_sum
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            float f[N];
+            Vec<T>::wide(held(raw[i]), f);
+#pragma unroll
+            for (int j = 0; j < N; j += 2) {
+                pair_t z = fma_pair(pair_of(f[j], f[j + 1]), c2c2, uu);
+                float z0, z1;
+                apart(z, z0, z1);
+                if (sizeof(T) == 4) {
+                    z0 = max_nan(z0, kLowest);
+                    z1 = max_nan(z1, kLowest);
+                    z = pair_of(z0, z1);
+                }
+                const pair_t e = pair_of(ex2(z0), ex2(z1));
+                s2 = add_pair(s2, e);
+                w2 = fma_pair(e, z, w2);
+            }
+        }
+        float p0, p1;
+        apart(s2, p0, p1);
+        s += p0 + p1;
+        apart(w2, p0, p1);
+        w += p0 + p1;
+    }
+    static __device__ __forceinline__ uint4 held(uint4 v) {
+        if constexpr (sizeof(T) == 2) {
+            v.x = held2(v.x); v.y = held2(v.y); v.z = held2(v.z); v.w = held2(v.w);
+        }
+        return v;
+    }
+    static __device__ __forceinline__ uint32_t held2(uint32_t v) {
+        uint32_t r = v;
+        if constexpr (Vec<T>::kEmpty == 0xfc00fc00u)
+            asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0xfbfffbffu));
+        else
+            asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0xf149f149u));
+        return r;
+    }
+};
+
+// The largest element of four vectors.
+template <typename T> __device__ __forceinline__ float top_of(const uint4 (&raw)[4]) {
+    return fmaxf(fmaxf(Vec<T>::top(raw[0]), Vec<T>::top(raw[1])), fmaxf(Vec<T>::top(raw[2]), Vec<T>::top(raw[3])));
+}
+template <> __device__ __forceinline__ float top_of<__nv_bfloat16>(const uint4 (&raw)[4]) {
+    using V = Vec<__nv_bfloat16>;
+    uint4 m = raw[0];
+#pragma unroll
+    for (int i = 1; i < 4; ++i) {
+        const __nv_bfloat162 x = __hmax2(V::b2(m.x), V::b2(raw[i].x)), y = __hmax2(V::b2(m.y), V::b2(raw[i].y));
+        const __nv_bfloat162 z = __hmax2(V::b2(m.z), V::b2(raw[i].z)), w = __hmax2(V::b2(m.w), V::b2(raw[i].w));
+        m = make_uint4(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y),
+                       *reinterpret_cast<const uint32_t*>(&z), *reinterpret_cast<const uint32_t*>(&w));
+    }
+    return V::top(m);
+}
+template <> __device__ __forceinline__ float top_of<__half>(const uint4 (&raw)[4]) {
+    using V = Vec<__half>;
+    uint4 m = raw[0];
+#pragma unroll
+    for (int i = 1; i < 4; ++i) {
+        const __half2 x = __hmax2(V::h2(m.x), V::h2(raw[i].x)), y = __hmax2(V::h2(m.y), V::h2(raw[i].y));
+        const __half2 z = __hmax2(V::h2(m.z), V::h2(raw[i].z)), w = __hmax2(V::h2(m.w), V::h2(raw[i].w));
+        m = make_uint4(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y),
+                       *reinterpret_cast<const uint32_t*>(&z), *reinterpret_cast<const uint32_t*>(&w));
+    }
+    return V::top(m);
+}
+
 // ---------------------------------------------------------------------------
 // The largest entries
 // ---------------------------------------------------------------------------
@@ -95,8 +207,119 @@ __device__ __forceinline__ unsigned long long candidate(uint32_t order, int id) 
     return (static_cast<unsigned long long>(order) << 32) | uint32_t(~id);
 }
 
-constexpr int kGroups = 8;          // of vectors, per thread, over all CTAs of a row
 constexpr int kCandidates = 1024;
+
+// Barriers of the first SB threads that take part (barrier ID).
+template <int SB, int ID> __device__ __forceinline__ void sync() {
+    if constexpr (SB == 32) __syncwarp(); else bar_sync(ID, SB);
+}
+// The sum of v over them; `sh` holds 2 x 8 numbers, used in turns (`turn` flips).
+template <int SB, int ID> __device__ __forceinline__ int sum_over(int v, int (*sh)[8], int& turn, int tid) {
+    v = __reduce_add_sync(~0u, v);
+    if constexpr (SB == 32) return v;
+    if ((tid & 31) == 0) sh[turn][tid >> 5] = v;
+    sync<SB, ID>();
+    v = 0;
+#pragma unroll
+    for (int i = 0; i < SB / 32; ++i) v += sh[turn][i];
+    turn ^= 1;
+    return v;
+}
+
+// More candidates than fit: the k-th largest entry itself.  At least k entries are >= lo, M is the
+// largest.  Every count is a pass over the row, out of L2.  Gives the number of candidates, at most k.
+template <typename T, int SB, int ID>
+__device__ __noinline__ int exact_candidates(const T* x, int vocab, int k, uint32_t lo, float M, unsigned long long* found,
+                                             int* nfound, int (*sh)[8], int turn, int tid) {
+    const int warp = tid >> 5, lane = tid & 31;
+    uint32_t hi = rank_of<T>(M) + 1;   // fewer than k are >= hi
+    bool first = true;                 // thousands of equal entries: the next rank already has fewer than k
+    while (hi - lo > 1) {
+        const uint32_t mid = first ? lo + 1 : lo + (hi - lo) / 2;
+        first = false;
+        int c = 0;
+        for (int j = tid; j < vocab; j += SB) c += rank_of<T>(to_f(x[j])) >= mid;
+        if (sum_over<SB, ID>(c, sh, turn, tid) >= k) lo = mid; else hi = mid;
+    }
+    sync<SB, ID>();
+    if (tid == 0) *nfound = 0;
+    sync<SB, ID>();
+    for (int j = tid; j < vocab; j += SB) {   // fewer than k
+        const uint32_t o = order_of(to_f(x[j]));
+        if (o >> Order<T>::kShift > lo) found[atomicAdd(nfound, 1)] = candidate(o, j);
+    }
+    sync<SB, ID>();
+    int n = *nfound;
+    // of those equal to the k-th the first ones
+    for (int base = 0; n < k && base < vocab; base += SB) {
+        const int j = base + tid;
+        const uint32_t o = j < vocab ? order_of(to_f(x[j])) : 0u;
+        const bool equal = j < vocab && o >> Order<T>::kShift == lo;
+        const unsigned ones = __ballot_sync(~0u, equal);
+        int before = __popc(ones & ((1u << lane) - 1)), all = __popc(ones);
+        if constexpr (SB > 32) {
+            if (lane == 0) sh[turn][warp] = all;
+            sync<SB, ID>();
+            all = 0;
+#pragma unroll
+            for (int v = 0; v < SB / 32; ++v) {
+                before += v < warp ? sh[turn][v] : 0;
+                all += sh[turn][v];
+            }
+            turn ^= 1;
+        }
+        if (equal && n + before < k) found[n + before] = candidate(o, j);
+        n += all;
+    }
+    sync<SB, ID>();
+    return min(n, k);
+}
+
+// A candidate's place is the number of candidates before it.  settle(candidate, place) by one thread.
+template <int SB, int ID, typename F>
+__device__ __forceinline__ void place_candidates(unsigned long long* found, int n, int tid, F settle) {
+    const int warp = tid >> 5, lane = tid & 31;
+    if (n <= 128) {   // counted; several lanes to a candidate where that keeps all of them busy at once
+        const int ls = 4 * n <= SB ? 2 : 2 * n <= SB ? 1 : 0, part = tid & ((1 << ls) - 1);
+        for (int i = tid >> ls; i < ((n + 31) & ~31); i += SB >> ls) {
+            const unsigned long long c = i < n ? found[i] : 0;
+            int place = 0;
+#pragma unroll 4
+            for (int j = part; j < n; j += 1 << ls) place += found[j] > c;
+            if (ls > 0) place += __shfl_xor_sync(~0u, place, 1);
+            if (ls > 1) place += __shfl_xor_sync(~0u, place, 2);
+            if (part == 0 && i < n) settle(c, place);
+        }
+        return;
+    }
+    // 32 at a time in order first, then looked up among the others
+    for (int base = warp * 32; base < n; base += SB) {
+        unsigned long long c = base + lane < n ? found[base + lane] : 0;
+#pragma unroll
+        for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+            for (int d = size / 2; d > 0; d /= 2) {
+                const unsigned long long o = __shfl_xor_sync(~0u, c, d);
+                const bool larger = ((lane & size) == 0) == ((lane & d) == 0);
+                c = larger == (c > o) ? c : o;
+            }
+        if (base + lane < n) found[base + lane] = c;
+    }
+    sync<SB, ID>();
+    for (int i = tid; i < n; i += SB) {
+        const unsigned long long c = found[i];
+        int place = 0;
+        for (int base = 0; base < n; base += 32) {
+            int before = 0;
+#pragma unroll
+            for (int d = 16; d > 0; d /= 2)
+                if (base + before + d - 1 < n && found[base + before + d - 1] > c) before += d;
+            if (base + before < n && found[base + before] > c) before += 1;
+            place += before;
+        }
+        settle(c, place);
+    }
+}
 
 // Other CTAs' shared memory.
 __device__ __forceinline__ uint32_t remote_address(const void* smem, uint32_t rank) {
@@ -135,56 +358,84 @@ __device__ __forceinline__ RowSums join_parts(float4 p, float c2) {
     r.W = __shfl_sync(~0u, p.z, 0);
     return r;
 }
+// The warp's part of them, its edge elements (-inf: none) included.
+template <typename T> __device__ __forceinline__ float4 warp_part(Running<T>& t, float top, float xe, bool edge, float c2) {
+    const float wt = warp_max(fmaxf(top, xe)), ref = part_ref(wt), least = -warp_max(-top);
+    move_sums(t.m, ref, c2, t.s, t.w);
+    t.m = ref;
+    if (edge) t.add_one(xe, c2);
+    return make_float4(wt, warp_sum(t.s), warp_sum(t.w), least);
+}
+
+// A row's softmax, and its outputs.
+struct RowSoftmax {
+    float M, S, W, u, c2, it;
+    bool none, far;   // none: no softmax
+    __device__ __forceinline__ RowSoftmax(const RowSums& r, const StatsArgs& a)
+        : M(r.M), S(r.S), W(r.W), u(anchor(r.M, a.c2)), c2(a.c2), it(a.it), none(!(fabsf(r.M) < INFINITY) || r.S != r.S),
+          far(big(r.M, a.c2)) {}
+    __device__ __forceinline__ float share(float x) const {
+        return none ? __int_as_float(0x7fffffff) : log_q(x, M, u, c2, far, S, it);
+    }
+    // By a warp; xy: the label's logit.
+    __device__ __forceinline__ void finish(const StatsArgs& a, int64_t r, int64_t y, float xy) const {
+        const float kNaN = __int_as_float(0x7fffffff), log_sum = -share(M), lp = share(xy);
+        const float H = fmaxf(log_sum + ((far ? 0.0f : __fmaf_rn(M, c2, -u)) - W / S) * kLn2, 0.0f);
+        if ((threadIdx.x & 31) != 0) return;
+        if (a.logp) a.logp[r] = y < a.vocab ? lp : kNaN;
+        if (a.entropy) a.entropy[r] = none ? kNaN : H;
+        if (a.saved) {
+            a.saved[3 * r] = none ? kNaN : M;
+            a.saved[3 * r + 1] = log_sum;
+            a.saved[3 * r + 2] = none ? kNaN : H;
+        }
+    }
+};
+__device__ __forceinline__ void put_entry(const StatsArgs& a, int64_t r, int i, int id, float lp) {
+    const int64_t at = r * a.ld_top + i;
+    if (a.id_bytes == 8) static_cast<int64_t*>(a.top_id)[at] = id; else static_cast<int32_t*>(a.top_id)[at] = id;
+    a.top_logp[at] = lp;
+}
+// An ignored row's outputs, by n threads.
+__device__ __forceinline__ void ignored_row(const StatsArgs& a, int64_t r, int tid, int n) {
+    for (int i = tid; i < a.k; i += n) put_entry(a, r, i, -1, 0.0f);
+    if (tid == 0) {
+        if (a.logp) a.logp[r] = 0.0f;
+        if (a.entropy) a.entropy[r] = 0.0f;
+    }
+    if (tid < 3 && a.saved) a.saved[3 * r + tid] = 0.0f;
+}
 
 // ---------------------------------------------------------------------------
-// A group of CTAs per row
+// Rows through shared memory
 // ---------------------------------------------------------------------------
 
-constexpr int kTileVecs = 8, kStages = 3;
+// The rows of a group, in tiles of TV vectors per thread, ST of them in shared memory, copied
+// asynchronously ahead of their use in the order of it.  A thread copies the vectors that it will itself
+// use, so a tile needs no barrier.
+template <typename T, int B, int TV, int ST> struct Feed {
+    static constexpr int N = Vec<T>::N, tile = B * TV;
+    const StatsArgs& a;
+    uint4* const ring;
+    const int ngroups, rank, clog, tid;
+    const bool alike;   // all rows lie alike where their stride is a multiple of 128 bytes
+    const Place<T> first;
+    int64_t fr, fynext;
+    const T* fat = nullptr;    // this thread's next vector
+    int fleft = 0, foff = 0;   // places left of the share, empty ones before the next vector
+    int slot = -1;             // of the tile last taken
 
-// A group of 2^clog CTAs takes one row at a time, each CTA a contiguous share of the row's vectors,
-// which come through shared memory in tiles, copied asynchronously ahead of their use, the next row's
-// too.  A thread copies the vectors that it will itself use.
-//
-// The largest k entries without a second pass over the row.  The row's vectors fall into groups (a
-// thread's consecutive ones, eight groups to the threads of one place in the row's CTAs) whose maxima
-// the softmax's pass gives for nothing.  Let t be the k-th largest of these maxima: k groups have an
-// entry >= t each, so every one of the k largest entries is >= t, and lies in a group whose maximum is.
-// Those groups (k, and a few that the search for t leaves) are read again, out of L2, their entries
-// >= t are the candidates, and a candidate's place is the number of candidates before it.
-//
-// Where more candidates come together than fit (thousands of equal entries, or the largest ones side by
-// side in a few groups), the exact k-th entry is searched for in the row itself: every count is a pass
-// out of L2.
-template <typename T, int B, bool TOP>
-__global__ void __launch_bounds__(B, 512 / B) k_stats(const StatsArgs a, const int clog) {
-    constexpr int N = Vec<T>::N, U = 4, tile = B * kTileVecs, ST = kStages, nw = B / 32, G = kGroups;
-    __shared__ float4 wparts[2][8], cparts[2][kMaxCluster];   // by row parity: of the warps, of the CTAs
-    __shared__ int counts[2][3][8], nfound[2], nlist[2];
-    extern __shared__ __align__(128) uint4 ring[];   // [ST][tile]
-    unsigned long long* const found = reinterpret_cast<unsigned long long*>(ring + ST * tile);   // [kCandidates]
-    float(*const gmax)[B] = reinterpret_cast<float(*)[B]>(found + kCandidates);                   // [G][B]
-    uint16_t* const list = reinterpret_cast<uint16_t*>(gmax);   // [G * B], where the maxima have been
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int cluster = 1 << clog, rank = cluster > 1 ? int(cluster_rank()) : 0;
-    const int group = int(blockIdx.x) >> clog, ngroups = int(gridDim.x) >> clog;
-    const int own = G >> clog;   // groups of this CTA's threads
-    const float c2 = a.it * kLog2e, kNaN = __int_as_float(0x7fffffff);
-    const pair_t c2c2 = pair_of(c2, c2);
-    const uint4 empty = make_uint4(Vec<T>::kEmpty, Vec<T>::kEmpty, Vec<T>::kEmpty, Vec<T>::kEmpty);
-    const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + 16u * uint32_t(tid);
-    auto row_at = [&](int64_t r) { return static_cast<const T*>(a.x) + r * a.ld; };
-    // all rows lie alike where their stride is a multiple of 128 bytes
-    const bool alike = (a.ld * int(sizeof(T))) % 128 == 0;
-    const Place<T> first_place(static_cast<const T*>(a.x), a.vocab, rank, clog);
-    auto place_of = [&](const T* x) { return alike ? first_place : Place<T>(x, a.vocab, rank, clog); };
-
-    // The copies run ahead in the order of their use: the next vector of this thread, places left of the
-    // share, empty places before the next vector.
-    int64_t fr = group - ngroups, fynext = a.target && group < a.rows ? a.target[group] : 0;
-    const T* fat = nullptr;
-    int fleft = 0, foff = 0;
-    auto fetch = [&](int slot) {
+    __device__ __forceinline__ Feed(const StatsArgs& args, uint4* smem, int group, int groups, int r, int c, int t)
+        : a(args), ring(smem), ngroups(groups), rank(r), clog(c), tid(t), alike((args.ld * int(sizeof(T))) % 128 == 0),
+          first(static_cast<const T*>(args.x), args.vocab, r, c), fr(group - groups),
+          fynext(args.target && group < args.rows ? args.target[group] : 0) {
+#pragma unroll
+        for (int i = 0; i < ST - 1; ++i) fetch(i);
+    }
+    __device__ __forceinline__ const T* row_at(int64_t r) const { return static_cast<const T*>(a.x) + r * a.ld; }
+    __device__ __forceinline__ Place<T> place_of(const T* x) const { return alike ? first : Place<T>(x, a.vocab, rank, clog); }
+    static __device__ __forceinline__ uint4 empty() { return make_uint4(Vec<T>::kEmpty, Vec<T>::kEmpty, Vec<T>::kEmpty, Vec<T>::kEmpty); }
+    __device__ __forceinline__ void fetch(int to_slot) {
         while (fleft <= 0) {   // the next row that is not ignored and of which this CTA has a share
             fr += ngroups;
             if (fr >= a.rows) break;
@@ -197,176 +448,391 @@ __global__ void __launch_bounds__(B, 512 / B) k_stats(const StatsArgs a, const i
             fleft = pl.hi > pl.lo ? pl.hi - pl.lo + pl.off : 0;
             fat = x + pl.head + int64_t(pl.lo + tid - pl.off) * N;
         }
-        const uint32_t to = ring_at + 16u * uint32_t(slot * tile);
+        const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + 16u * uint32_t(to_slot * tile + tid);
         if (fleft >= tile && foff == 0) {
 #pragma unroll
-            for (int i = 0; i < kTileVecs; ++i) copy_async(to + 16u * B * i, fat + B * N * i);
-        } else {   // behind the last row a group is empty
+            for (int i = 0; i < TV; ++i) copy_async(to + 16u * B * i, fat + B * N * i);
+        } else {   // behind the last row a copy group is empty
 #pragma unroll
-            for (int i = 0; i < kTileVecs; ++i)
+            for (int i = 0; i < TV; ++i)
                 if (tid + B * i < fleft && (i > 0 || tid >= foff)) copy_async(to + 16u * B * i, fat + B * N * i);
-            if (tid < foff) ring[slot * tile + tid] = empty;
+            if (tid < foff) ring[to_slot * tile + tid] = empty();
             foff = 0;
         }
         fat += tile * N;
         fleft -= tile;
         copy_commit();
-    };
-    int slot = -1;   // of the tile last taken
-    auto take_tile = [&]() {   // the tile before is done with; its slot is the next to fill
+    }
+    // The next tile; the one before is done with, its slot is the next to fill.
+    __device__ __forceinline__ const uint4* take() {
         const int before = slot;
         slot = slot + 1 == ST ? 0 : slot + 1;
         fetch(before < 0 ? ST - 1 : before);
         copy_wait<ST - 1>();
-    };
+        return ring + slot * tile + tid;
+    }
+};
+// Four of a tile's vectors, from the g-th on, for a thread that has `mine` places left in it.
+template <typename T, int B> __device__ __forceinline__ void load_four(const uint4* buf, int g, int mine, uint4 (&raw)[4]) {
+    if (B * (g + 3) < mine) {
 #pragma unroll
-    for (int i = 0; i < ST - 1; ++i) fetch(i);
+        for (int i = 0; i < 4; ++i) raw[i] = buf[B * (g + i)];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            raw[i] = make_uint4(Vec<T>::kEmpty, Vec<T>::kEmpty, Vec<T>::kEmpty, Vec<T>::kEmpty);
+            if (B * (g + i) < mine) raw[i] = buf[B * (g + i)];
+        }
+    }
+}
+
+// The largest k entries without a second pass over the row.  The row's vectors fall into groups (a
+// thread's consecutive ones) whose maxima the softmax's pass gives for nothing.  Let t be the k-th
+// largest of these maxima: k groups have an entry >= t each, so every one of the k largest entries is
+// >= t, and lies in a group whose maximum is.  Those groups (k, and a few that the search for t leaves)
+// are read again, out of L2, their entries >= t are the candidates, and a candidate's place is the number
+// of candidates before it.  Where more candidates come together than fit (thousands of equal entries, or
+// the largest ones side by side in a few groups), the exact k-th entry is searched for in the row itself.
+
+// Vectors in a group: the least power of two with which `most` of them are at most `groups` groups.
+__device__ __forceinline__ int group_shift(int most, int groups) {
+    int gs = 0;
+    while (groups << gs < most) ++gs;
+    return gs;
+}
+// The maxima of a thread's groups, from four vectors at a time: those from vector `at` on.
+template <typename T, int B>
+__device__ __forceinline__ float keep_maxima(float (*gm)[B], int gs, int at, const uint4 (&raw)[4], float& run, int tid) {
+    if (gs >= 2) {
+        const float t = top_of<T>(raw);
+        run = (at & ((1 << gs) - 1)) == 0 ? t : fmaxf(run, t);
+        gm[at >> gs][tid] = run;
+        return t;
+    }
+    float tops[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) tops[i] = Vec<T>::top(raw[i]);
+    const float t01 = fmaxf(tops[0], tops[1]), t23 = fmaxf(tops[2], tops[3]);
+    if (gs == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) gm[at + i][tid] = tops[i];
+    } else {
+        gm[at >> 1][tid] = t01;
+        gm[(at >> 1) + 1][tid] = t23;
+    }
+    return fmaxf(t01, t23);
+}
+// Among `sets` of maxima at least k of which are >= lo, and fewer than k above M: lo raised until few
+// more than k are.  count(value): how many are >= it.
+template <typename T, typename F> __device__ __forceinline__ uint32_t search_rank(uint32_t lo, float M, int k, F count) {
+    const int enough = k + k / 8 + 4;
+    uint32_t hi = rank_of<T>(M) + 1;
+    while (hi - lo > 1) {
+        const uint32_t mid = lo + (hi - lo) / 2;
+        const int n = count(logit_of(mid << Order<T>::kShift));
+        if (n < k) { hi = mid; continue; }
+        lo = mid;
+        if (n <= enough) break;
+    }
+    return lo;
+}
+// The entries >= least of up to four vectors (at[i] < 0: none) to `add(count)`, which gives the place of the
+// first, and `store(place, candidate)`.
+template <typename T, typename A, typename S>
+__device__ __forceinline__ void offer_vectors(const uint4 (&raw)[4], const int (&at)[4], int head, float least, A add, S store) {
+    constexpr int N = Vec<T>::N;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (at[i] < 0 || !(Vec<T>::top(raw[i]) >= least)) continue;
+        float f[N];
+        Vec<T>::wide(raw[i], f);
+        int n = 0;
+#pragma unroll
+        for (int j = 0; j < N; ++j) n += f[j] >= least;
+        int to = add(n);
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (f[j] >= least) store(to++, candidate(order_of(f[j]), head + at[i] * N + j));
+    }
+}
+
+// ---------------------------------------------------------------------------
+// A CTA per row: warps that read rows, and warps that choose entries
+// ---------------------------------------------------------------------------
+
+constexpr int kSlots = 16;    // groups of vectors per thread
+constexpr int kList = 1024;   // groups that are read again; more: the exact search
+
+template <int B> constexpr size_t top_smem(int tv, int st) {
+    return size_t(16) * st * tv * B + size_t(8) * kCandidates + size_t(4) * 2 * (kSlots + 1) * B + size_t(2) * kList;
+}
+
+// B threads read rows and leave the maxima of groups, SB others choose the entries of a row while the
+// former are in the next one.  Named barriers 1 and 2 (by row parity): a row's maxima and sums are there;
+// 3 and 4: they have been used; 5: the choosing warps alone.
+template <typename T, int B, int TV, int ST, int PER_SM>
+__global__ void __launch_bounds__(B + B / 2, PER_SM) k_top(const StatsArgs a) {
+    constexpr int SB = B / 2, nw = B / 32, G = kSlots, KEYS = 16;
+    __shared__ float4 wparts[2][8];
+    __shared__ int counts[2][8], nfound[2], nlist[2];
+    extern __shared__ __align__(128) uint4 ring[];   // [ST][TV * B]
+    unsigned long long* const found = reinterpret_cast<unsigned long long*>(ring + ST * TV * B);   // [kCandidates]
+    float(*const gmax)[B] = reinterpret_cast<float(*)[B]>(found + kCandidates);   // [2][G + 1][B]: of the groups, of all
+    uint16_t* const list = reinterpret_cast<uint16_t*>(gmax + 2 * (G + 1));       // [kList]
+    const int lane = threadIdx.x & 31;
+    const float c2 = a.c2;
+    const int group = blockIdx.x, ngroups = gridDim.x;
+    int par = 0;
+    int64_t ynext = a.target && group < a.rows ? a.target[group] : 0;
+    auto label = [&](int64_t r) {
+        const int64_t y = ynext;
+        if (a.target && r + ngroups < a.rows) ynext = a.target[r + ngroups];
+        return y;
+    };
+    if (threadIdx.x < B) {
+        // ------------------------------------------------------------ the rows
+        const int tid = threadIdx.x, warp = tid >> 5;
+        Feed<T, B, TV, ST> feed(a, ring, group, ngroups, 0, 0, tid);
+        const pair_t c2c2 = pair_of(c2, c2);
+        int done = 0;   // rows so far, up to 2
+        for (int64_t r = group; r < a.rows; r += ngroups) {
+            if (label(r) < 0) continue;
+            const T* const x = feed.row_at(r);
+            const Place<T> pl = feed.place_of(x);
+            const bool edge = tid < pl.edges;
+            const float xe = edge ? to_f(x[pl.edge_at(tid)]) : kNegInf;
+            const int places = pl.hi > pl.lo ? pl.hi - pl.lo + pl.off : 0;
+            const int gs = group_shift((places + TV * B - 1) / (TV * B) * TV, G);
+            if (done == 2) bar_sync(3 + par, B + SB); else ++done;
+            float(*const gm)[B] = gmax + par * (G + 1);
+#pragma unroll
+            for (int g = 0; g < G; ++g) gm[g][tid] = kNegInf;
+            Running<T> sum;
+            float top = kNegInf, run = kNegInf;
+            for (int base = 0; base * B < places; base += TV) {
+                const uint4* const buf = feed.take();
+                const int mine = places - base * B - tid;
+#pragma unroll 1
+                for (int g = 0; g < TV; g += 4) {
+                    if (B * g >= mine) break;
+                    uint4 raw[4];
+                    load_four<T, B>(buf, g, mine, raw);
+                    const float t = keep_maxima<T, B>(gm, gs, base + g, raw, run, tid);
+                    top = fmaxf(top, t);
+                    sum.raise(t, c2);
+                    sum.add(raw, c2c2, c2);
+                }
+            }
+            gm[G][tid] = top;
+            const float4 part = warp_part(sum, top, xe, edge, c2);
+            if (lane == 0) wparts[par][warp] = part;
+            bar_arrive(1 + par, B + SB);
+            par ^= 1;
+        }
+        if (done == 2) bar_sync(3 + par, B + SB);
+        if (done > 0) bar_sync(3 + (done == 2 ? par ^ 1 : 0), B + SB);
+        copy_wait<0>();
+        return;
+    }
+    // ---------------------------------------------------------------- the entries
+    const int tid = threadIdx.x - B, warp = tid >> 5;
+    const bool alike = (a.ld * int(sizeof(T))) % 128 == 0;
+    const Place<T> first(static_cast<const T*>(a.x), a.vocab, 0, 0);
+    int turn = 0;
+    for (int64_t r = group; r < a.rows; r += ngroups) {
+        const int64_t y = label(r);
+        if (y < 0) {
+            ignored_row(a, r, tid, SB);
+            continue;
+        }
+        const T* const x = static_cast<const T*>(a.x) + r * a.ld;
+        const Place<T> pl = alike ? first : Place<T>(x, a.vocab, 0, 0);
+        const bool edge = tid < pl.edges;
+        const float xe = edge ? to_f(x[pl.edge_at(tid)]) : kNegInf;
+        const float xy = warp == 0 && a.logp && y < a.vocab ? to_f(x[y]) : 0.0f;
+        const int places = pl.hi > pl.lo ? pl.hi - pl.lo + pl.off : 0;
+        const int gs = group_shift((places + TV * B - 1) / (TV * B) * TV, G);
+        const float(*const gm)[B] = gmax + par * (G + 1);
+        if (tid == 0) nfound[par] = nlist[par] = 0;
+        bar_sync(1 + par, B + SB);
+        const RowSums sums = join_parts(lane < nw ? wparts[par][lane] : make_float4(kNegInf, 0.0f, 0.0f, INFINITY), c2);
+        const RowSoftmax row(sums, a);
+        if (warp == 0) row.finish(a, r, y, xy);
+        if (row.none) {
+            for (int i = tid; i < a.k; i += SB) put_entry(a, r, i, -1, row.share(0.0f));
+            bar_arrive(3 + par, B + SB);
+            par ^= 1;
+            continue;
+        }
+        // The sets among which t is searched: the threads' vectors as wholes while there are twice as many
+        // as k (the k largest of 4 k sets have 1.15 k entries >= t, of 2 k 1.39 k), else 2, 4 or 8 to a thread.
+        const int ss = 2 * a.k <= B ? 0 : a.k <= B ? 1 : a.k <= 2 * B ? 2 : 3;   // log2 of that
+        float key[KEYS];   // of two threads
+        if (ss == 0) {
+            key[0] = gm[G][tid];
+            key[1] = gm[G][tid + SB];
+        } else {
+#pragma unroll
+            for (int i = 0; i < KEYS; ++i) {
+                key[i] = kNegInf;
+                const int width = G >> ss;   // slots of a set
+                if (i < 2 << ss)
+                    for (int g = 0; g < width; ++g) key[i] = fmaxf(key[i], gm[(i >> 1) * width + g][tid + (i & 1) * SB]);
+            }
+        }
+        auto count = [&](float v) {
+            int c = 0;
+            if (ss == 0) {
+                c = (key[0] >= v) + (key[1] >= v);
+            } else {
+#pragma unroll
+                for (int i = 0; i < KEYS; ++i) c += i < 2 << ss && key[i] >= v ? 1 : 0;
+            }
+            return sum_over<SB, 5>(c, counts, turn, tid);
+        };
+        uint32_t lo = kLeast<T>;
+        const bool full = a.k <= B && sums.least > kNegInf;   // each thread has a set from the least of their tops on
+        if (full) lo = rank_of<T>(sums.least);
+        if (full || count(logit_of(lo << Order<T>::kShift)) > a.k) lo = search_rank<T>(lo, row.M, a.k, count);
+        const float least = logit_of(lo << Order<T>::kShift);
+        // the groups from there on
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int t = tid + h * SB;
+            if (gm[G][t] >= least)
+                for (int g = 0; g < G; ++g)
+                    if (gm[g][t] >= least) {
+                        const int i = atomicAdd(&nlist[par], 1);
+                        if (i < kList) list[i] = uint16_t(g * B + t);
+                    }
+        }
+        if (edge && xe >= least) found[atomicAdd(&nfound[par], 1)] = candidate(order_of(xe), pl.edge_at(tid));
+        sync<SB, 5>();
+        bar_arrive(3 + par, B + SB);   // the maxima have been used
+        const int groups = nlist[par], items = groups > kList ? 0 : groups << gs;
+        for (int from = tid; from < items; from += 4 * SB) {
+            uint4 raw[4];
+            int at[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int item = from + SB * i;
+                at[i] = -1;
+                if (item < items) {
+                    const int e = list[item >> gs], t = e & (B - 1);
+                    const int place = t + B * (((e / B) << gs) + (item & ((1 << gs) - 1)));
+                    if (place >= pl.off && place < places) at[i] = pl.lo + place - pl.off;
+                }
+                if (at[i] >= 0) raw[i] = ld16(x + pl.head + int64_t(at[i]) * Vec<T>::N);
+            }
+            offer_vectors<T>(raw, at, pl.head, least, [&](int n) { return atomicAdd(&nfound[par], n); },
+                             [&](int i, unsigned long long c) { if (i < kCandidates) found[i] = c; });
+        }
+        sync<SB, 5>();
+        int n = nfound[par];
+        if (n > kCandidates || groups > kList)
+            n = exact_candidates<T, SB, 5>(x, a.vocab, a.k, lo, row.M, found, &nfound[par], counts, turn, tid);
+        place_candidates<SB, 5>(found, n, tid, [&](unsigned long long c, int place) {
+            if (place < a.k) put_entry(a, r, place, int(~uint32_t(c)), row.share(logit_of(uint32_t(c >> 32))));
+        });
+        for (int i = n + tid; i < a.k; i += SB) put_entry(a, r, i, -1, kNegInf);
+        sync<SB, 5>();   // before the next row's candidates
+        par ^= 1;
+    }
+}
+
+template <typename T, int B, int TV, int ST, int PER_SM>
+cudaError_t top_launch(const StatsArgs& a, int sms, GroupCache& cache, cudaStream_t s) {
+    auto* kernel = k_top<T, B, TV, ST, PER_SM>;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(B + B / 2);
+    cfg.dynamicSmemBytes = top_smem<B>(TV, ST);
+    cfg.stream = s;
+    int groups = 0;
+    cudaError_t e = resident_groups(reinterpret_cast<const void*>(kernel), cfg, RowShape{B + B / 2, 0}, sms, cache, groups);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim.x = unsigned(groups < a.rows ? groups : a.rows);
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+// ---------------------------------------------------------------------------
+// A group of CTAs per row
+// ---------------------------------------------------------------------------
+
+constexpr int kGroups = 8;   // groups of vectors to the threads of one place in the row's CTAs
+
+// A group of 2^clog CTAs takes one row at a time, each CTA a contiguous share of the row's vectors.  With
+// alternatives (TOP) for few rows alone, where a row is spread over CTAs: each CTA hands its groups'
+// maxima to all others, all of them search for t alike, and the first one collects the candidates.
+template <typename T, int B, bool TOP>
+__global__ void __launch_bounds__(B, (TOP ? 256 : 512) / B) k_stats(const StatsArgs a, const int clog) {
+    constexpr int TV = 8, ST = 3, nw = B / 32, G = kGroups;
+    __shared__ float4 wparts[2][8], cparts[2][kMaxCluster];   // by row parity: of the warps, of the CTAs
+    __shared__ int counts[2][8], nfound[2], nlist[2];
+    extern __shared__ __align__(128) uint4 ring[];   // [ST][TV * B]
+    unsigned long long* const found = reinterpret_cast<unsigned long long*>(ring + ST * TV * B);   // [kCandidates]
+    float(*const gmax)[B] = reinterpret_cast<float(*)[B]>(found + kCandidates);                     // [G][B]
+    uint16_t* const list = reinterpret_cast<uint16_t*>(gmax + G);                                   // [G * B]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int cluster = 1 << clog, rank = cluster > 1 ? int(cluster_rank()) : 0;
+    const int group = int(blockIdx.x) >> clog, ngroups = int(gridDim.x) >> clog;
+    const int own = G >> clog;   // groups of this CTA's threads
+    const float c2 = a.c2;
+    const pair_t c2c2 = pair_of(c2, c2);
+    Feed<T, B, TV, ST> feed(a, ring, group, ngroups, rank, clog, tid);
     if (cluster > 1) {   // every CTA of the group runs before any writes into another
         cluster_arrive();
         cluster_wait();
     }
-
     int par = 0, turn = 0, finisher = 0;
     int64_t ynext = a.target && group < a.rows ? a.target[group] : 0;
     for (int64_t r = group; r < a.rows; r += ngroups) {
         const int64_t y = ynext;
         if (a.target && r + ngroups < a.rows) ynext = a.target[r + ngroups];
-        auto put = [&](int i, int id, float lp) {
-            const int64_t at = r * a.ld_top + i;
-            if (a.id_bytes == 8) static_cast<int64_t*>(a.top_id)[at] = id; else static_cast<int32_t*>(a.top_id)[at] = id;
-            a.top_logp[at] = lp;
-        };
         if (y < 0) {
-            if (rank == 0) {
-                if (TOP)
-                    for (int i = tid; i < a.k; i += B) put(i, -1, 0.0f);
-                if (tid == 0) {
-                    if (a.logp) a.logp[r] = 0.0f;
-                    if (a.entropy) a.entropy[r] = 0.0f;
-                }
-                if (tid < 3 && a.saved) a.saved[3 * r + tid] = 0.0f;
-            }
+            if (rank == 0) ignored_row(a, r, tid, B);
             continue;
         }
-        const T* const x = row_at(r);
-        const Place<T> pl = place_of(x);
+        const T* const x = feed.row_at(r);
+        const Place<T> pl = feed.place_of(x);
         const bool edge = rank == 0 && tid < pl.edges;
         const float xe = edge ? to_f(x[pl.edge_at(tid)]) : kNegInf;
         // the warps take the rows' ends in turns
         const bool finishes = rank == 0 && warp == finisher;
-        float xy = 0.0f;
-        if (finishes && a.logp && y < a.vocab) xy = to_f(x[y]);
-        // vectors of a group: the least power of two with which a thread's vectors are at most `own` groups
+        const float xy = finishes && a.logp && y < a.vocab ? to_f(x[y]) : 0.0f;
         const int places = pl.hi > pl.lo ? pl.hi - pl.lo + pl.off : 0;
         int gs = 0;
         if (TOP) {
-            const int most = (places + tile - 1) / tile * kTileVecs;
-            while (own << gs < most) ++gs;
-#pragma unroll
-            for (int g = 0; g < G; ++g)
-                if (g < own) gmax[rank * own + g][tid] = kNegInf;
+            gs = group_shift((places + TV * B - 1) / (TV * B) * TV, own);
+            for (int g = 0; g < own; ++g) gmax[rank * own + g][tid] = kNegInf;
         }
-        // one pass: the largest entry, and the sums against a reference near it, U vectors at a time
-        float top = kNegInf, m = kNegInf, s = 0.0f, w = 0.0f, run = kNegInf;
-        for (int base = 0; base * B < places; base += kTileVecs) {
-            take_tile();
-            const uint4* const buf = ring + slot * tile + tid;
+        Running<T> sum;
+        float top = kNegInf, run = kNegInf;
+        for (int base = 0; base * B < places; base += TV) {
+            const uint4* const buf = feed.take();
             const int mine = places - base * B - tid;
 #pragma unroll 1
-            for (int g = 0; g < kTileVecs; g += U) {
+            for (int g = 0; g < TV; g += 4) {
                 if (B * g >= mine) break;
-                uint4 raw[U];
-                float tops[U];
-                if (B * (g + U - 1) < mine) {
-#pragma unroll
-                    for (int i = 0; i < U; ++i) raw[i] = buf[B * (g + i)];
-                } else {
-#pragma unroll
-                    for (int i = 0; i < U; ++i) {
-                        raw[i] = empty;
-                        if (B * (g + i) < mine) raw[i] = buf[B * (g + i)];
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < U; ++i) tops[i] = Vec<T>::top(raw[i]);
-                const float t01 = fmaxf(tops[0], tops[1]), t23 = fmaxf(tops[2], tops[3]), t = fmaxf(t01, t23);
-                if (TOP) {
-                    float(*const gm)[B] = gmax + rank * own;
-                    const int at = base + g;
-                    if (gs == 0) {
-#pragma unroll
-                        for (int i = 0; i < U; ++i) gm[at + i][tid] = tops[i];
-                    } else if (gs == 1) {
-                        gm[at >> 1][tid] = t01;
-                        gm[(at >> 1) + 1][tid] = t23;
-                    } else {
-                        run = (at & ((1 << gs) - 1)) == 0 ? t : fmaxf(run, t);
-                        gm[at >> gs][tid] = run;
-                    }
-                }
+                uint4 raw[4];
+                load_four<T, B>(buf, g, mine, raw);
+                const float t = TOP ? keep_maxima<T, B>(gmax + rank * own, gs, base + g, raw, run, tid) : top_of<T>(raw);
                 top = fmaxf(top, t);
-                // smaller steps are left: m is a reference, and exponentials up to 2^32 of it do no harm
-                if ((t - m) * c2 > 32.0f) {
-                    move_sums(m, t, c2, s, w);
-                    m = t;
-                }
-                const float ref = part_ref(m);
-                if (big(ref, c2)) {
-#pragma unroll 1
-                    for (int i = 0; i < U * N && B * (g + i / N) < mine; ++i) {
-                        const float v = to_f(reinterpret_cast<const T*>(buf + B * (g + i / N))[i % N]);
-                        const float z = max_nan((v - ref) * c2, kLowest), e = ex2(z);
-                        s += e;
-                        w = __fmaf_rn(e, z, w);
-                    }
-                } else {
-                    const float u = anchor(ref, c2);
-                    const pair_t uu = pair_of(-u, -u);
-                    pair_t s2 = 0, w2 = 0;   // of these vectors first: see tree_sum
-#pragma unroll
-                    for (int i = 0; i < U; ++i) {
-                        float f[N];
-                        Vec<T>::wide(raw[i], f);
-#pragma unroll
-                        for (int j = 0; j < N; j += 2) {
-                            float z0, z1;
-                            apart(fma_pair(pair_of(f[j], f[j + 1]), c2c2, uu), z0, z1);
-                            z0 = max_nan(z0, kLowest);
-                            z1 = max_nan(z1, kLowest);
-                            const pair_t e = pair_of(ex2(z0), ex2(z1));
-                            s2 = add_pair(s2, e);
-                            w2 = fma_pair(e, pair_of(z0, z1), w2);
-                        }
-                    }
-                    float p0, p1;
-                    apart(s2, p0, p1);
-                    s += p0 + p1;
-                    apart(w2, p0, p1);
-                    w += p0 + p1;
-                }
+                sum.raise(t, c2);
+                sum.add(raw, c2c2, c2);
             }
         }
         {
-            // the warp's part, edges included
-            const float wt = warp_max(fmaxf(top, xe)), ref = part_ref(wt), least = -warp_max(-top);
-            move_sums(m, ref, c2, s, w);
-            if (edge) {
-                const float z = max_nan(big(ref, c2) ? (xe - ref) * c2 : __fmaf_rn(xe, c2, -anchor(ref, c2)), kLowest), e = ex2(z);
-                s += e;
-                w = __fmaf_rn(e, z, w);
-            }
-            s = warp_sum(s);
-            w = warp_sum(w);
-            if (lane == 0) wparts[par][warp] = make_float4(wt, s, w, least);
+            const float4 part = warp_part(sum, top, xe, edge, c2);
+            if (lane == 0) wparts[par][warp] = part;
             if (tid == 0) nfound[par] = nlist[par] = 0;
         }
         const float4 none_part = make_float4(kNegInf, 0.0f, 0.0f, INFINITY);
-        RowSums row;
         __syncthreads();
         if (cluster > 1) {
             if (warp == 0) {
-                row = join_parts(lane < nw ? wparts[par][lane] : none_part, c2);
-                if (lane < cluster) store_remote(&cparts[par][rank], uint32_t(lane), make_float4(row.M, row.S, row.W, row.least));
+                const RowSums p = join_parts(lane < nw ? wparts[par][lane] : none_part, c2);
+                if (lane < cluster) store_remote(&cparts[par][rank], uint32_t(lane), make_float4(p.M, p.S, p.W, p.least));
             }
             if (TOP)
                 for (int c = 0; c < cluster; ++c) {
@@ -379,190 +845,67 @@ __global__ void __launch_bounds__(B, 512 / B) k_stats(const StatsArgs a, const i
         }
         const int was = par;
         par ^= 1;
-        if (TOP || finishes) {
-            row = cluster > 1 ? join_parts(lane < cluster ? cparts[was][lane] : none_part, c2)
-                              : join_parts(lane < nw ? wparts[was][lane] : none_part, c2);
-        }
         finisher = finisher + 1 == nw ? 0 : finisher + 1;
         if (!TOP && !finishes) continue;
-        const float M = row.M, S = row.S;
-        const bool none = !(fabsf(M) < INFINITY) || S != S;   // no softmax
-        const bool far = big(M, c2);
-        const float u = anchor(M, c2);
-        auto share = [&](float x) { return none ? kNaN : log_q(x, M, u, c2, far, S, a.it); };
-        if (finishes) {
-            const float log_sum = -share(M), lp = share(xy);
-            const float H = fmaxf(log_sum + ((far ? 0.0f : __fmaf_rn(M, c2, -u)) - row.W / S) * kLn2, 0.0f);
-            if (lane == 0) {
-                if (a.logp) a.logp[r] = y < a.vocab ? lp : kNaN;
-                if (a.entropy) a.entropy[r] = none ? kNaN : H;
-                if (a.saved) {
-                    a.saved[3 * r] = none ? kNaN : M;
-                    a.saved[3 * r + 1] = log_sum;
-                    a.saved[3 * r + 2] = none ? kNaN : H;
-                }
-            }
-        }
+        const RowSums sums = cluster > 1 ? join_parts(lane < cluster ? cparts[was][lane] : none_part, c2)
+                                         : join_parts(lane < nw ? wparts[was][lane] : none_part, c2);
+        const RowSoftmax row(sums, a);
+        if (finishes) row.finish(a, r, y, xy);
         if (!TOP) continue;
-        if (none) {
+        if (row.none) {
             if (rank == 0)
-                for (int i = tid; i < a.k; i += B) put(i, -1, kNaN);
+                for (int i = tid; i < a.k; i += B) put_entry(a, r, i, -1, row.share(0.0f));
             continue;
         }
-        // t: at least k groups are >= lo (or lo is the least), fewer than k are >= hi
-        uint32_t key[G];
+        float key[G];
 #pragma unroll
-        for (int g = 0; g < G; ++g) key[g] = rank_of<T>(gmax[g][tid]);
-        // how many groups are >= each of three ranks
-        auto groups_from = [&](uint32_t t0, uint32_t t1, uint32_t t2, int (&n)[3]) {
-            int c = 0;   // at most 8 per thread, 256 per warp: ten bits each
+        for (int g = 0; g < G; ++g) key[g] = gmax[g][tid];
+        auto count = [&](float v) {
+            int c = 0;
 #pragma unroll
-            for (int g = 0; g < G; ++g) c += (key[g] >= t0 ? 1 : 0) + (key[g] >= t1 ? 1 << 10 : 0) + (key[g] >= t2 ? 1 << 20 : 0);
-            c = __reduce_add_sync(~0u, c);
-            if (lane < 3) counts[turn][lane][warp] = (c >> (10 * lane)) & 0x3ff;
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < 3; ++i) {
-                n[i] = 0;
-#pragma unroll
-                for (int v = 0; v < nw; ++v) n[i] += counts[turn][i][v];
-            }
-            turn ^= 1;
+            for (int g = 0; g < G; ++g) c += key[g] >= v;
+            return sum_over<B, 0>(c, counts, turn, tid);
         };
-        // every thread that has a vector has a group from the least of their largest entries on
-        const int enough = a.k + a.k / 2 + 16;
-        uint32_t lo = kLeast<T>, hi = rank_of<T>(M) + 1;
-        int over = G * B, n3[3];
-        if (a.k <= B && row.least > kNegInf) {
-            lo = rank_of<T>(row.least);
-        } else {
-            groups_from(lo, lo, lo, n3);
-            over = n3[0];
-        }
-        while (over > enough && hi - lo > 1) {
-            const uint32_t d = hi - lo, q = d >> 2, m0 = lo + q, m1 = lo + (d >> 1), m2 = hi - (q > 0 ? q : 1);
-            groups_from(m0, m1, m2, n3);
-            if (n3[2] >= a.k) { lo = m2; over = n3[2]; }
-            else if (n3[1] >= a.k) { lo = m1; hi = m2; over = n3[1]; }
-            else if (n3[0] >= a.k) { lo = m0; hi = m1; over = n3[0]; }
-            else hi = m0;
-        }
-        // the groups from lo on, each CTA its own, and their entries from lo on, to the first CTA
+        uint32_t lo = kLeast<T>;
+        const bool full = a.k <= B && sums.least > kNegInf;   // each thread has a group from the least of their tops on
+        if (full) lo = rank_of<T>(sums.least);
+        if (full || count(logit_of(lo << Order<T>::kShift)) > a.k) lo = search_rank<T>(lo, row.M, a.k, count);
+        const float least = logit_of(lo << Order<T>::kShift);
+        // the groups from there on, each CTA its own, and their entries, to the first CTA
+        if (top >= least)
+            for (int g = 0; g < own; ++g)
+                if (gmax[rank * own + g][tid] >= least) list[atomicAdd(&nlist[was], 1)] = uint16_t(g * B + tid);
         __syncthreads();
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-            const int i = g - rank * own;
-            if (i >= 0 && i < own && key[g] >= lo) list[atomicAdd(&nlist[was], 1)] = uint16_t(i * B + tid);
-        }
-        __syncthreads();
-        const uint32_t far_found = cluster > 1 ? remote_address(found, 0) : 0, far_count = cluster > 1 ? remote_address(&nfound[was], 0) : 0;
-        auto offer = [&](float v, int id) {
-            const uint32_t o = order_of(v);
-            if (o >> Order<T>::kShift < lo) return;
-            if (cluster > 1) {
-                const int i = add_remote(far_count, 1);
-                if (i < kCandidates) store_remote(far_found + 8u * uint32_t(i), candidate(o, id));
-            } else {
-                const int i = atomicAdd(&nfound[was], 1);
-                if (i < kCandidates) found[i] = candidate(o, id);
-            }
-        };
-        if (edge) offer(xe, pl.edge_at(tid));
+        const uint32_t far_found = remote_address(found, 0), far_count = remote_address(&nfound[was], 0);
+        auto add = [&](int n) { return add_remote(far_count, n); };
+        auto store = [&](int i, unsigned long long c) { if (i < kCandidates) store_remote(far_found + 8u * uint32_t(i), c); };
+        if (edge && xe >= least) store(add(1), candidate(order_of(xe), pl.edge_at(tid)));
         const int items = nlist[was] << gs;
-        for (int first = tid; first < items; first += B * U) {
-            uint4 raw[U];
-            int at[U];
+        for (int from = tid; from < items; from += 4 * B) {
+            uint4 raw[4];
+            int at[4];
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const int item = first + B * i;
+            for (int i = 0; i < 4; ++i) {
+                const int item = from + B * i;
                 at[i] = -1;
                 if (item < items) {
                     const int e = list[item >> gs], t = e & (B - 1);
                     const int place = t + B * (((e / B) << gs) + (item & ((1 << gs) - 1)));
                     if (place >= pl.off && place < places) at[i] = pl.lo + place - pl.off;
                 }
-                if (at[i] >= 0) raw[i] = ld16(x + pl.head + int64_t(at[i]) * N);
+                if (at[i] >= 0) raw[i] = ld16(x + pl.head + int64_t(at[i]) * Vec<T>::N);
             }
-#pragma unroll
-            for (int i = 0; i < U; ++i) {
-                if (at[i] < 0 || rank_of<T>(Vec<T>::top(raw[i])) < lo) continue;
-                float f[N];
-                Vec<T>::wide(raw[i], f);
-#pragma unroll
-                for (int j = 0; j < N; ++j) offer(f[j], pl.head + at[i] * N + j);
-            }
+            offer_vectors<T>(raw, at, pl.head, least, add, store);
         }
-        if (cluster > 1) {
-            cluster_arrive();
-            cluster_wait();
-            if (rank != 0) continue;
-        } else {
-            __syncthreads();
-        }
+        cluster_arrive();
+        cluster_wait();
+        if (rank != 0) continue;
         int n = nfound[was];
-        if (n > kCandidates) {
-            // the k-th largest entry itself: at least k entries are >= lo, fewer than k are >= hi
-            auto entries_from = [&](uint32_t t) {
-                int c = 0;
-                for (int j = tid; j < a.vocab; j += B) c += rank_of<T>(to_f(x[j])) >= t;
-                c = __reduce_add_sync(~0u, c);
-                if (lane == 0) counts[turn][0][warp] = c;
-                __syncthreads();
-                c = 0;
-#pragma unroll
-                for (int v = 0; v < nw; ++v) c += counts[turn][0][v];
-                turn ^= 1;
-                return c;
-            };
-            hi = rank_of<T>(M) + 1;
-            bool first = true;   // thousands of equal entries: the next rank already has fewer than k
-            while (hi - lo > 1) {
-                const uint32_t mid = first ? lo + 1 : lo + (hi - lo) / 2;
-                first = false;
-                if (entries_from(mid) >= a.k) lo = mid; else hi = mid;
-            }
-            __syncthreads();
-            if (tid == 0) nfound[was] = 0;
-            __syncthreads();
-            for (int j = tid; j < a.vocab; j += B) {   // fewer than k
-                const uint32_t o = order_of(to_f(x[j]));
-                if (o >> Order<T>::kShift > lo) found[atomicAdd(&nfound[was], 1)] = candidate(o, j);
-            }
-            __syncthreads();
-            n = nfound[was];
-            // of those equal to the k-th the first ones
-            for (int base = 0; n < a.k && base < a.vocab; base += B) {
-                const int j = base + tid;
-                const uint32_t o = j < a.vocab ? order_of(to_f(x[j])) : 0u;
-                const bool equal = j < a.vocab && o >> Order<T>::kShift == lo;
-                const unsigned ones = __ballot_sync(~0u, equal);
-                if (lane == 0) counts[turn][0][warp] = __popc(ones);
-                __syncthreads();
-                int before = __popc(ones & ((1u << lane) - 1)), all = 0;
-#pragma unroll
-                for (int v = 0; v < nw; ++v) {
-                    before += v < warp ? counts[turn][0][v] : 0;
-                    all += counts[turn][0][v];
-                }
-                turn ^= 1;
-                if (equal && n + before < a.k) found[n + before] = candidate(o, j);
-                n += all;
-            }
-            n = min(n, a.k);
-            __syncthreads();
-        }
-        // places: L lanes to a candidate where that keeps all of them busy at once
-        const int ls = 4 * n <= B ? 2 : 2 * n <= B ? 1 : 0, part = tid & ((1 << ls) - 1);
-        for (int i = tid >> ls; i < (n + 31 & ~31); i += B >> ls) {
-            const unsigned long long c = i < n ? found[i] : 0;
-            int place = 0;
-#pragma unroll 4
-            for (int j = part; j < n; j += 1 << ls) place += found[j] > c;
-            if (ls > 0) place += __shfl_xor_sync(~0u, place, 1);
-            if (ls > 1) place += __shfl_xor_sync(~0u, place, 2);
-            if (part == 0 && i < n && place < a.k) put(place, int(~uint32_t(c)), share(logit_of(uint32_t(c >> 32))));
-        }
-        for (int i = n + tid; i < a.k; i += B) put(i, -1, kNegInf);
+        if (n > kCandidates) n = exact_candidates<T, B, 0>(x, a.vocab, a.k, lo, row.M, found, &nfound[was], counts, turn, tid);
+        place_candidates<B, 0>(found, n, tid, [&](unsigned long long c, int place) {
+            if (place < a.k) put_entry(a, r, place, int(~uint32_t(c)), row.share(logit_of(uint32_t(c >> 32))));
+        });
+        for (int i = n + tid; i < a.k; i += B) put_entry(a, r, i, -1, kNegInf);
     }
     copy_wait<0>();
 }
@@ -573,7 +916,7 @@ cudaError_t stats_launch(const StatsArgs& a, int clog, int sms, GroupCache& cach
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(1u << clog);
     cfg.blockDim = dim3(B);
-    cfg.dynamicSmemBytes = size_t(16) * kStages * kTileVecs * B + (TOP ? size_t(8) * kCandidates + size_t(4) * kGroups * B : 0);
+    cfg.dynamicSmemBytes = size_t(16) * 3 * 8 * B + (TOP ? size_t(8) * kCandidates + size_t(6) * kGroups * B : 0);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -590,15 +933,24 @@ cudaError_t stats_launch(const StatsArgs& a, int clog, int sms, GroupCache& cach
     return cudaLaunchKernelEx(&cfg, kernel, a, clog);
 }
 
-template <typename T, bool TOP>
+template <typename T>
 cudaError_t stats(const StatsArgs& a, int sms, GroupCache& cache, cudaStream_t s) {
     const int vecs = (a.vocab + Vec<T>::N - 1) / Vec<T>::N, threads = vecs < 512 ? 64 : vecs <= 8192 ? 128 : 256;
     // few rows: spread each over more CTAs while the GPU has idle SMs and the share is over a tile
     int clog = 0;
-    while (clog < kMaxClusterLog && a.rows << (clog + 1) <= sms && (threads * kTileVecs) << clog < vecs) clog += 1;
-    if (threads == 64) return stats_launch<T, 64, TOP>(a, clog, sms, cache, s);
-    if (threads == 128) return stats_launch<T, 128, TOP>(a, clog, sms, cache, s);
-    return stats_launch<T, 256, TOP>(a, clog, sms, cache, s);
+    while (clog < kMaxClusterLog && a.rows << (clog + 1) <= sms && (threads * 8) << clog < vecs) clog += 1;
+    if (a.k == 0) {
+        if (threads == 64) return stats_launch<T, 64, false>(a, clog, sms, cache, s);
+        if (threads == 128) return stats_launch<T, 128, false>(a, clog, sms, cache, s);
+        return stats_launch<T, 256, false>(a, clog, sms, cache, s);
+    }
+    if (clog > 0) {   // more than a tile: never 64 threads
+        if (threads == 128) return stats_launch<T, 128, true>(a, clog, sms, cache, s);
+        return stats_launch<T, 256, true>(a, clog, sms, cache, s);
+    }
+    if (threads == 64) return top_launch<T, 64, 4, 4, 6>(a, sms, cache, s);
+    if (threads == 128) return top_launch<T, 128, 4, 4, 3>(a, sms, cache, s);
+    return top_launch<T, 256, 4, 4, 2>(a, sms, cache, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -637,7 +989,7 @@ __global__ void __launch_bounds__(TB) k_token_grad(const TokenGradArgs a, const 
         if (v >= 0 && v < hi) raw[i] = ld16(body + int64_t(v) * N);
     }
     const float xe = edge ? to_f(x[row.edge_at(tid)]) : 0.0f;
-    const float c2 = a.it * kLog2e, kNaN = __int_as_float(0x7fffffff);
+    const float c2 = a.c2, kNaN = __int_as_float(0x7fffffff);
     const float M = a.saved[3 * r], H = a.saved[3 * r + 2];
     const bool far = big(M, c2);
     const float u = far ? 0.0f : anchor(M, c2), base = far ? M : 0.0f;
@@ -690,9 +1042,9 @@ template <typename T> cudaError_t token_grad(const TokenGradArgs& a, cudaStream_
 }  // namespace
 
 cudaError_t launch_token_stats(int dt, const StatsArgs& a, int sm_count, GroupCache& cache, cudaStream_t s) {
-    if (dt == kF32) return a.k > 0 ? stats<float, true>(a, sm_count, cache, s) : stats<float, false>(a, sm_count, cache, s);
-    if (dt == kBF16) return a.k > 0 ? stats<__nv_bfloat16, true>(a, sm_count, cache, s) : stats<__nv_bfloat16, false>(a, sm_count, cache, s);
-    return a.k > 0 ? stats<__half, true>(a, sm_count, cache, s) : stats<__half, false>(a, sm_count, cache, s);
+    if (dt == kF32) return stats<float>(a, sm_count, cache, s);
+    if (dt == kBF16) return stats<__nv_bfloat16>(a, sm_count, cache, s);
+    return stats<__half>(a, sm_count, cache, s);
 }
 
 cudaError_t launch_token_grad(int dt, const TokenGradArgs& a, cudaStream_t s) {
