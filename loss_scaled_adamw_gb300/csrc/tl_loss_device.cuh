@@ -74,9 +74,8 @@ __device__ __forceinline__ float sum_parts(float a, float b, float& left) {
 }
 // log(exponential of x / s) in a part whose largest element is m, with anchor u; c: the scale
 // of x times log2(e).
-__device__ __forceinline__ float log_share(float x, float m, float u, float c, bool far, float s) {
-    float n, rest;
-    log2_parts(s, n, rest);
+// n, rest: log2_parts of s.
+__device__ __forceinline__ float log_share(float x, float m, float u, float c, bool far, float n, float rest) {
     const float plain = ((far ? (x - m) * c - n : __fmaf_rn(x, c, -(u + n))) - rest) * kLn2;
     // The same with the error of each step carried along, so that the log-probability is rounded
     // once at its own size: of the 3.7e-7 rms that three roundings left on 128,256 entries a
@@ -91,6 +90,11 @@ __device__ __forceinline__ float log_share(float x, float m, float u, float c, b
     const float r = __fmul_rn(h, kLn2), re = __fmaf_rn(h, kLn2, -r);
     const float lp = __fadd_rn(r, __fadd_rn(re, __fmaf_rn(low, kLn2, __fmul_rn(h, kLn2Low))));
     return fabsf(lp) < INFINITY ? lp : plain;   // infinities leave no error to carry
+}
+__device__ __forceinline__ float log_share(float x, float m, float u, float c, bool far, float s) {
+    float n, rest;
+    log2_parts(s, n, rest);
+    return log_share(x, m, u, c, far, n, rest);
 }
 
 __device__ __forceinline__ float warp_sum(float v) {

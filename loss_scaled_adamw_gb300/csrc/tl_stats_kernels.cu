@@ -34,13 +34,6 @@ __device__ __forceinline__ void move_sums(float m, float to, float c2, float& s,
 // own exponent is -inf, and 0 times that is not).
 constexpr float kLowest = -200.0f;
 
-// log q of an entry x of a row with a softmax.  Roundings of the sum are not let above 0, and an entry at
-// a type's lowest value, whose exponent overflows, has its distance.
-__device__ __forceinline__ float log_q(float x, float M, float u, float c2, bool far, float S, float it) {
-    const float r = log_share(x, M, u, c2, far, S);
-    return fminf(r == kNegInf ? (x - M) * it : r, 0.0f);
-}
-
 // ---------------------------------------------------------------------------
 // Pairs of fp32 in one register pair: two multiply-adds or additions to an instruction
 // ---------------------------------------------------------------------------
@@ -275,50 +268,70 @@ __device__ __noinline__ int exact_candidates(const T* x, int vocab, int k, uint3
     return min(n, k);
 }
 
-// A candidate's place is the number of candidates before it.  settle(candidate, place) by one thread.
-template <int SB, int ID, typename F>
-__device__ __forceinline__ void place_candidates(unsigned long long* found, int n, int tid, F settle) {
-    const int warp = tid >> 5, lane = tid & 31;
-    if (n <= 128) {   // counted; several lanes to a candidate where that keeps all of them busy at once
-        const int ls = 4 * n <= SB ? 2 : 2 * n <= SB ? 1 : 0, part = tid & ((1 << ls) - 1);
-        for (int i = tid >> ls; i < ((n + 31) & ~31); i += SB >> ls) {
-            const unsigned long long c = i < n ? found[i] : 0;
-            int place = 0;
-#pragma unroll 4
-            for (int j = part; j < n; j += 1 << ls) place += found[j] > c;
-            if (ls > 0) place += __shfl_xor_sync(~0u, place, 1);
-            if (ls > 1) place += __shfl_xor_sync(~0u, place, 2);
-            if (part == 0 && i < n) settle(c, place);
-        }
-        return;
-    }
-    // 32 at a time in order first, then looked up among the others
-    for (int base = warp * 32; base < n; base += SB) {
-        unsigned long long c = base + lane < n ? found[base + lane] : 0;
+// The n candidates in order, each thread E of them in registers: candidate (warp E + e) 32 + lane of the
+// sorted list is settled by that lane.  A bitonic network: neighbours up to 16 apart by shuffles, up to
+// 32 E / 2 apart in registers, further ones through shared memory.
+template <int SB, int ID, int E, typename F>
+__device__ __forceinline__ void sort_by(unsigned long long* found, int n, int tid, F settle) {
+    const int warp = tid >> 5, lane = tid & 31, base = warp * E * 32 + lane;
+    unsigned long long c[E];
 #pragma unroll
-        for (int size = 2; size <= 32; size *= 2)
+    for (int e = 0; e < E; ++e) c[e] = base + 32 * e < n ? found[base + 32 * e] : 0;
+    auto keep = [](unsigned long long mine, unsigned long long other, bool larger) { return larger == (mine > other) ? mine : other; };
+    if (SB > 32) sync<SB, ID>();   // the list has been read
+#pragma unroll 1
+    for (int size = 2; size < 2 * n; size *= 2) {   // the largest candidates first where `size` is not in the index
+        if (SB > 32) {
+#pragma unroll 1
+            for (int d = size / 2; d >= 32 * E; d /= 2) {
 #pragma unroll
-            for (int d = size / 2; d > 0; d /= 2) {
-                const unsigned long long o = __shfl_xor_sync(~0u, c, d);
-                const bool larger = ((lane & size) == 0) == ((lane & d) == 0);
-                c = larger == (c > o) ? c : o;
+                for (int e = 0; e < E; ++e) found[base + 32 * e] = c[e];
+                sync<SB, ID>();
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const int i = base + 32 * e;
+                    c[e] = keep(c[e], found[i ^ d], ((i & size) == 0) == ((i & d) == 0));
+                }
+                sync<SB, ID>();
             }
-        if (base + lane < n) found[base + lane] = c;
-    }
-    sync<SB, ID>();
-    for (int i = tid; i < n; i += SB) {
-        const unsigned long long c = found[i];
-        int place = 0;
-        for (int base = 0; base < n; base += 32) {
-            int before = 0;
-#pragma unroll
-            for (int d = 16; d > 0; d /= 2)
-                if (base + before + d - 1 < n && found[base + before + d - 1] > c) before += d;
-            if (base + before < n && found[base + before] > c) before += 1;
-            place += before;
         }
-        settle(c, place);
+#pragma unroll
+        for (int de = E / 2; de > 0; de /= 2) {
+            if (32 * de < size) {
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if ((e & de) == 0) {
+                        const unsigned long long x = c[e], y = c[e + de];
+                        const bool first = (((base + 32 * e) & size) == 0) == (x > y);
+                        c[e] = first ? x : y;
+                        c[e + de] = first ? y : x;
+                    }
+            }
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2) {
+            if (d < size) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const int i = base + 32 * e;
+                    c[e] = keep(c[e], __shfl_xor_sync(~0u, c[e], d), ((i & size) == 0) == ((lane & d) == 0));
+                }
+            }
+        }
     }
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        if (base + 32 * e < n) settle(c[e], base + 32 * e);
+}
+// CAP: the list's length, at most 16 per thread.
+template <int SB, int ID, int CAP, typename F>
+__device__ __forceinline__ void place_candidates(unsigned long long* found, int n, int tid, F settle) {
+    if (n <= SB) return sort_by<SB, ID, 1>(found, n, tid, settle);
+    if (n <= 2 * SB) return sort_by<SB, ID, 2>(found, n, tid, settle);
+    if (n <= 4 * SB || CAP <= 4 * SB) return sort_by<SB, ID, 4>(found, n, tid, settle);
+    if constexpr (CAP > 4 * SB)
+        if (n <= 8 * SB || CAP <= 8 * SB) return sort_by<SB, ID, 8>(found, n, tid, settle);
+    if constexpr (CAP > 8 * SB) sort_by<SB, ID, 16>(found, n, tid, settle);
 }
 
 // Other CTAs' shared memory.
@@ -369,13 +382,19 @@ template <typename T> __device__ __forceinline__ float4 warp_part(Running<T>& t,
 
 // A row's softmax, and its outputs.
 struct RowSoftmax {
-    float M, S, W, u, c2, it;
+    float M, S, W, u, c2, it, n, rest;
     bool none, far;   // none: no softmax
     __device__ __forceinline__ RowSoftmax(const RowSums& r, const StatsArgs& a)
         : M(r.M), S(r.S), W(r.W), u(anchor(r.M, a.c2)), c2(a.c2), it(a.it), none(!(fabsf(r.M) < INFINITY) || r.S != r.S),
-          far(big(r.M, a.c2)) {}
+          far(big(r.M, a.c2)) {
+        log2_parts(S, n, rest);
+    }
+    // log q of an entry x.  Roundings of the sum are not let above 0, and an entry at a type's lowest value,
+    // whose exponent overflows, has its distance.
     __device__ __forceinline__ float share(float x) const {
-        return none ? __int_as_float(0x7fffffff) : log_q(x, M, u, c2, far, S, it);
+        if (none) return __int_as_float(0x7fffffff);
+        const float r = log_share(x, M, u, c2, far, n, rest);
+        return fminf(r == kNegInf ? (x - M) * it : r, 0.0f);
     }
     // By a warp; xy: the label's logit.
     __device__ __forceinline__ void finish(const StatsArgs& a, int64_t r, int64_t y, float xy) const {
@@ -490,8 +509,8 @@ template <typename T, int B> __device__ __forceinline__ void load_four(const uin
 // thread's consecutive ones) whose maxima the softmax's pass gives for nothing.  Let t be the k-th
 // largest of these maxima: k groups have an entry >= t each, so every one of the k largest entries is
 // >= t, and lies in a group whose maximum is.  Those groups (k, and a few that the search for t leaves)
-// are read again, out of L2, their entries >= t are the candidates, and a candidate's place is the number
-// of candidates before it.  Where more candidates come together than fit (thousands of equal entries, or
+// are read again, out of L2, their entries >= t are the candidates, which are put in
+// order.  Where more candidates come together than fit (thousands of equal entries, or
 // the largest ones side by side in a few groups), the exact k-th entry is searched for in the row itself.
 
 // Vectors in a group: the least power of two with which `most` of them are at most `groups` groups.
@@ -522,37 +541,125 @@ __device__ __forceinline__ float keep_maxima(float (*gm)[B], int gs, int at, con
     }
     return fmaxf(t01, t23);
 }
-// Among `sets` of maxima at least k of which are >= lo, and fewer than k above M: lo raised until few
-// more than k are.  count(value): how many are >= it.
-template <typename T, typename F> __device__ __forceinline__ uint32_t search_rank(uint32_t lo, float M, int k, F count) {
+__device__ __forceinline__ float lg2(float v) {
+    float r;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+// Of `sets` numbers at least k are >= the value of rank lo, and M is the largest: lo raised until few more
+// than k are.  count(value): how many are >= it.  The logarithm of that count falls about evenly towards
+// the largest ones: two steps of three go where it would be just above k, the third halves the ranks.
+template <typename T, typename F>
+__device__ __forceinline__ uint32_t search_rank(uint32_t lo, int sets, float M, int k, F count) {
+    constexpr int SH = Order<T>::kShift;
     const int enough = k + k / 8 + 4;
+    const float aim = lg2(float(k) + 0.06f * float(k) + 1.0f);
     uint32_t hi = rank_of<T>(M) + 1;
-    while (hi - lo > 1) {
-        const uint32_t mid = lo + (hi - lo) / 2;
-        const int n = count(logit_of(mid << Order<T>::kShift));
-        if (n < k) { hi = mid; continue; }
+    float from = logit_of(lo << SH), to = M, lfrom = lg2(float(sets)), lto = 0.0f;   // the ends, and log2 of their counts
+    for (int step = 0; hi - lo > 1; step = step == 2 ? 0 : step + 1) {
+        uint32_t mid = lo + (hi - lo) / 2;
+        if (step < 2) {
+            const uint32_t guess = rank_of<T>(__fmaf_rn(to - from, (lfrom - aim) / (lfrom - lto), from));
+            mid = guess > lo && guess < hi ? guess : mid;
+        }
+        const float v = logit_of(mid << SH);
+        const int n = count(v);
+        if (n < k) {
+            hi = mid;
+            to = v;
+            lto = lg2(fmaxf(float(n), 1.0f));
+            continue;
+        }
         lo = mid;
+        from = v;
+        lfrom = lg2(float(n));
         if (n <= enough) break;
     }
     return lo;
 }
-// The entries >= least of up to four vectors (at[i] < 0: none) to `add(count)`, which gives the place of the
-// first, and `store(place, candidate)`.
-template <typename T, typename A, typename S>
-__device__ __forceinline__ void offer_vectors(const uint4 (&raw)[4], const int (&at)[4], int head, float least, A add, S store) {
+// The entries >= least of NV vectors (at(i): the first element's id, below 0 for none) to the list:
+// add(count) gives the place of a thread's first one, store(place, candidate) puts it there.
+template <typename T, int NV, typename At, typename A, typename S>
+__device__ __forceinline__ void offer_vectors(const uint4 (&raw)[NV], float least, At at, A add, S store) {
     constexpr int N = Vec<T>::N;
+    int n = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (at[i] < 0 || !(Vec<T>::top(raw[i]) >= least)) continue;
+    for (int i = 0; i < NV; ++i) {
+        if (at(i) < 0 || !(Vec<T>::top(raw[i]) >= least)) continue;
         float f[N];
         Vec<T>::wide(raw[i], f);
-        int n = 0;
 #pragma unroll
         for (int j = 0; j < N; ++j) n += f[j] >= least;
-        int to = add(n);
+    }
+    if (n == 0) return;
+    int to = add(n);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if (at(i) < 0 || !(Vec<T>::top(raw[i]) >= least)) continue;
+        float f[N];
+        Vec<T>::wide(raw[i], f);
 #pragma unroll
         for (int j = 0; j < N; ++j)
-            if (f[j] >= least) store(to++, candidate(order_of(f[j]), head + at[i] * N + j));
+            if (f[j] >= least) store(to++, candidate(order_of(f[j]), at(i) + j));
+    }
+}
+
+// Vectors with an entry to be offered, side by side in shared memory, so that the threads share their
+// entries evenly.
+struct Stage {
+    uint4* raw;
+    int *id, *count;   // of a vector's first element
+};
+__device__ __forceinline__ int warp_before(int n, int& all) {   // the sum over the lanes below, and over all
+    int to = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int below = __shfl_up_sync(~0u, to, o);
+        if ((threadIdx.x & 31) >= o) to += below;
+    }
+    all = __shfl_sync(~0u, to, 31);
+    return to - n;
+}
+// Places for the n of each lane of a warp, behind those that *count has already.
+__device__ __forceinline__ int warp_places(int n, int* count) {
+    int all;
+    const int before = warp_before(n, all);
+    int first = 0;
+    if ((threadIdx.x & 31) == 0 && all > 0) first = atomicAdd(count, all);
+    return __shfl_sync(~0u, first, 0) + before;
+}
+// A thread's vectors `pass` (a bit each), of the first element's id id(i).
+template <int NV, typename Id>
+__device__ __forceinline__ void stage_vectors(const uint4 (&raw)[NV], unsigned pass, Id id, const Stage& st) {
+    int to = warp_places(__popc(pass), st.count);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if (pass >> i & 1) {
+            st.raw[to] = raw[i];
+            st.id[to] = id(i);
+            ++to;
+        }
+}
+// The staged vectors' entries >= least to the list, by SB threads.
+template <typename T, int SB, int CAP>
+__device__ __forceinline__ void offer_staged(const Stage& st, int m, float least, unsigned long long* found, int* nfound, int tid) {
+    constexpr int N = Vec<T>::N;
+    for (int base = tid & ~31; base < m; base += SB) {
+        const int i = base + (tid & 31);
+        unsigned some = 0;
+        int id = 0;
+        if (i < m) {
+            float f[N];
+            Vec<T>::wide(st.raw[i], f);
+            id = st.id[i];
+#pragma unroll
+            for (int j = 0; j < N; ++j) some |= f[j] >= least ? 1u << j : 0u;
+        }
+        int to = warp_places(__popc(some), nfound);
+        for (; some != 0 && to < CAP; some &= some - 1) {
+            const int j = __ffs(some) - 1;
+            found[to++] = candidate(order_of(to_f(reinterpret_cast<const T*>(st.raw + i)[j])), id + j);
+        }
     }
 }
 
@@ -574,7 +681,7 @@ template <typename T, int B, int TV, int ST, int PER_SM>
 __global__ void __launch_bounds__(B + B / 2, PER_SM) k_top(const StatsArgs a) {
     constexpr int SB = B / 2, nw = B / 32, G = kSlots, KEYS = 16;
     __shared__ float4 wparts[2][8];
-    __shared__ int counts[2][8], nfound[2], nlist[2];
+    __shared__ int counts[2][8], nfound[2], nlist[2], nstage;
     extern __shared__ __align__(128) uint4 ring[];   // [ST][TV * B]
     unsigned long long* const found = reinterpret_cast<unsigned long long*>(ring + ST * TV * B);   // [kCandidates]
     float(*const gmax)[B] = reinterpret_cast<float(*)[B]>(found + kCandidates);   // [2][G + 1][B]: of the groups, of all
@@ -693,45 +800,54 @@ __global__ void __launch_bounds__(B + B / 2, PER_SM) k_top(const StatsArgs a) {
         uint32_t lo = kLeast<T>;
         const bool full = a.k <= B && sums.least > kNegInf;   // each thread has a set from the least of their tops on
         if (full) lo = rank_of<T>(sums.least);
-        if (full || count(logit_of(lo << Order<T>::kShift)) > a.k) lo = search_rank<T>(lo, row.M, a.k, count);
+        const int from = full ? B << ss : count(logit_of(lo << Order<T>::kShift));
+        if (from > a.k) lo = search_rank<T>(lo, from, row.M, a.k, count);
         const float least = logit_of(lo << Order<T>::kShift);
         // the groups from there on
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int t = tid + h * SB;
-            if (gm[G][t] >= least)
-                for (int g = 0; g < G; ++g)
-                    if (gm[g][t] >= least) {
-                        const int i = atomicAdd(&nlist[par], 1);
-                        if (i < kList) list[i] = uint16_t(g * B + t);
-                    }
+            if (!(gm[G][t] >= least)) continue;
+            unsigned some = 0;
+#pragma unroll
+            for (int g = 0; g < G; ++g) some |= gm[g][t] >= least ? 1u << g : 0u;
+            int i = atomicAdd(&nlist[par], __popc(some));
+            for (; some != 0 && i < kList; some &= some - 1) list[i++] = uint16_t((__ffs(some) - 1) * B + t);
         }
         if (edge && xe >= least) found[atomicAdd(&nfound[par], 1)] = candidate(order_of(xe), pl.edge_at(tid));
         sync<SB, 5>();
-        bar_arrive(3 + par, B + SB);   // the maxima have been used
         const int groups = nlist[par], items = groups > kList ? 0 : groups << gs;
-        for (int from = tid; from < items; from += 4 * SB) {
+        const Stage stage{reinterpret_cast<uint4*>(gmax + par * (G + 1)),   // where the maxima have been
+                          reinterpret_cast<int*>(gmax + par * (G + 1) + G / 2), &nstage};
+        for (int base = 0; base < items; base += 4 * SB) {
+            if (tid == 0) nstage = 0;
             uint4 raw[4];
             int at[4];
+            unsigned pass = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int item = from + SB * i;
+                const int item = base + tid + SB * i;
                 at[i] = -1;
                 if (item < items) {
                     const int e = list[item >> gs], t = e & (B - 1);
                     const int place = t + B * (((e / B) << gs) + (item & ((1 << gs) - 1)));
-                    if (place >= pl.off && place < places) at[i] = pl.lo + place - pl.off;
+                    if (place >= pl.off && place < places) at[i] = pl.head + (pl.lo + place - pl.off) * Vec<T>::N;
                 }
-                if (at[i] >= 0) raw[i] = ld16(x + pl.head + int64_t(at[i]) * Vec<T>::N);
+                if (at[i] >= 0) raw[i] = ld16(x + at[i]);
             }
-            offer_vectors<T>(raw, at, pl.head, least, [&](int n) { return atomicAdd(&nfound[par], n); },
-                             [&](int i, unsigned long long c) { if (i < kCandidates) found[i] = c; });
+#pragma unroll
+            for (int i = 0; i < 4; ++i) pass |= at[i] >= 0 && Vec<T>::top(raw[i]) >= least ? 1u << i : 0u;
+            sync<SB, 5>();
+            stage_vectors<4>(raw, pass, [&](int i) { return at[i]; }, stage);
+            sync<SB, 5>();
+            offer_staged<T, SB, kCandidates>(stage, nstage, least, found, &nfound[par], tid);
+            sync<SB, 5>();
         }
-        sync<SB, 5>();
+        bar_arrive(3 + par, B + SB);   // the maxima have been used
         int n = nfound[par];
         if (n > kCandidates || groups > kList)
             n = exact_candidates<T, SB, 5>(x, a.vocab, a.k, lo, row.M, found, &nfound[par], counts, turn, tid);
-        place_candidates<SB, 5>(found, n, tid, [&](unsigned long long c, int place) {
+        place_candidates<SB, 5, kCandidates>(found, n, tid, [&](unsigned long long c, int place) {
             if (place < a.k) put_entry(a, r, place, int(~uint32_t(c)), row.share(logit_of(uint32_t(c >> 32))));
         });
         for (int i = n + tid; i < a.k; i += SB) put_entry(a, r, i, -1, kNegInf);
@@ -753,6 +869,160 @@ cudaError_t top_launch(const StatsArgs& a, int sms, GroupCache& cache, cudaStrea
     if (e != cudaSuccess) return e;
     cfg.gridDim.x = unsigned(groups < a.rows ? groups : a.rows);
     return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+// ---------------------------------------------------------------------------
+// Short rows, held in registers
+// ---------------------------------------------------------------------------
+
+// A warp per row (W = 1, four rows to a CTA) or a CTA of W warps, NV vectors per thread.  The row is
+// read once; the entries are chosen where it is.
+template <typename T, int W, int NV, bool TOP>
+__global__ void __launch_bounds__(128, NV > 8 ? 3 : NV > 4 ? 4 : 6) k_held(const StatsArgs a) {
+    constexpr int N = Vec<T>::N, SB = 32 * W, TEAMS = 4 / W, CAP = W == 1 ? 512 : kCandidates;
+    __shared__ float4 wparts[W == 1 ? 1 : 2][4];
+    __shared__ float2 wtops[W == 1 ? 1 : 2][4];
+    __shared__ int counts[2][8], nfound[TEAMS], nstage[TEAMS];
+    extern __shared__ __align__(128) uint4 ring[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, team = warp / W, tid = threadIdx.x % SB;
+    // per team: the staged vectors and their ids, and the candidates
+    const Stage stage{ring + team * (SB * NV), reinterpret_cast<int*>(ring + TEAMS * SB * NV) + team * (SB * NV), &nstage[team]};
+    unsigned long long* const found = reinterpret_cast<unsigned long long*>(reinterpret_cast<int*>(ring + TEAMS * SB * NV) + TEAMS * SB * NV) + team * CAP;
+    const float c2 = a.c2;
+    const pair_t c2c2 = pair_of(c2, c2);
+    const int64_t step = int64_t(gridDim.x) * TEAMS, start = int64_t(blockIdx.x) * TEAMS + team;
+    int64_t ynext = a.target && start < a.rows ? a.target[start] : 0;
+    int turn = 0, par = 0;
+    for (int64_t r = start; r < a.rows; r += step) {
+        const int64_t y = ynext;
+        if (a.target && r + step < a.rows) ynext = a.target[r + step];
+        if (y < 0) {
+            ignored_row(a, r, tid, SB);
+            continue;
+        }
+        const T* const x = static_cast<const T*>(a.x) + r * a.ld;
+        const Place<T> pl(x, a.vocab, 0, 0);
+        const T* const body = x + pl.head;
+        const bool edge = tid < pl.edges;
+        uint4 raw[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v = i * SB + tid - pl.off;
+            raw[i] = make_uint4(Vec<T>::kEmpty, Vec<T>::kEmpty, Vec<T>::kEmpty, Vec<T>::kEmpty);
+            if (v >= 0 && v < pl.body) raw[i] = ld16(body + v * N);
+        }
+        const float xe = edge ? to_f(x[pl.edge_at(tid)]) : kNegInf;
+        const float xy = a.logp && y < a.vocab ? to_f(x[y]) : 0.0f;
+        float tops[NV], top = xe, low = INFINITY;   // low: the least of the vectors' largest entries
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            top = fmaxf(top, tops[i] = Vec<T>::top(raw[i]));
+            const int v = i * SB + tid - pl.off;
+            if (TOP && v >= 0 && v < pl.body) low = fminf(low, tops[i]);
+        }
+        float M = warp_max(top);
+        if (TOP) low = -warp_max(-low);
+        if (W > 1) {
+            if (lane == 0) wtops[par][warp] = make_float2(M, low);
+            if (TOP && tid == 0) nfound[0] = nstage[0] = 0;
+            __syncthreads();
+            M = fmaxf(fmaxf(wtops[par][0].x, wtops[par][1].x), fmaxf(wtops[par][2].x, wtops[par][3].x));
+            low = fminf(fminf(wtops[par][0].y, wtops[par][1].y), fminf(wtops[par][2].y, wtops[par][3].y));
+        } else if (TOP) {
+            if (lane == 0) nfound[team] = nstage[team] = 0;
+            __syncwarp();
+        }
+        Running<T> sum;
+        sum.raise(M, c2);
+#pragma unroll
+        for (int i = 0; i < NV; i += 4) {
+            const uint4 four[4] = {raw[i], raw[i + 1], raw[i + 2], raw[i + 3]};
+            sum.add(four, c2c2, c2);
+        }
+        if (edge) sum.add_one(xe, c2);
+        RowSums sums{M, warp_sum(sum.s), warp_sum(sum.w), kNegInf};
+        if (W > 1) {
+            if (lane == 0) wparts[par][warp] = make_float4(0.0f, sums.S, sums.W, 0.0f);
+            __syncthreads();
+            sums.S = (wparts[par][0].y + wparts[par][1].y) + (wparts[par][2].y + wparts[par][3].y);
+            sums.W = (wparts[par][0].z + wparts[par][1].z) + (wparts[par][2].z + wparts[par][3].z);
+            par ^= 1;
+        }
+        const RowSoftmax row(sums, a);
+        if (W == 1 || warp == 0) row.finish(a, r, y, xy);
+        if (!TOP) continue;
+        if (row.none) {
+            for (int i = tid; i < a.k; i += SB) put_entry(a, r, i, -1, row.share(0.0f));
+            continue;
+        }
+        // t among the vectors' maxima while there are twice as many as k, else among the entries themselves
+        uint32_t lo = kLeast<T>;
+        if (2 * a.k <= pl.body) {
+            auto count = [&](float v) {
+                int c = 0;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) c += tops[i] >= v;
+                return sum_over<SB, 5>(c, counts, turn, tid);
+            };
+            const bool full = low > kNegInf;
+            if (full) lo = rank_of<T>(low);
+            const int from = full ? pl.body : count(logit_of(lo << Order<T>::kShift));
+            if (from > a.k) lo = search_rank<T>(lo, from, M, a.k, count);
+        } else {
+            auto count = [&](float v) {
+                int c = xe >= v;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    float f[N];
+                    Vec<T>::wide(raw[i], f);
+#pragma unroll
+                    for (int j = 0; j < N; ++j) c += f[j] >= v;
+                }
+                return sum_over<SB, 5>(c, counts, turn, tid);
+            };
+            const int from = count(logit_of(lo << Order<T>::kShift));
+            if (from > a.k) lo = search_rank<T>(lo, from, M, a.k, count);
+        }
+        const float least = logit_of(lo << Order<T>::kShift);
+        if (edge && xe >= least) found[atomicAdd(&nfound[team], 1)] = candidate(order_of(xe), pl.edge_at(tid));
+        unsigned pass = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) pass |= tops[i] >= least ? 1u << i : 0u;
+        stage_vectors<NV>(raw, pass, [&](int i) { return pl.head + (i * SB + tid - pl.off) * N; }, stage);
+        sync<SB, 5>();
+        offer_staged<T, SB, CAP>(stage, nstage[team], least, found, &nfound[team], tid);
+        sync<SB, 5>();
+        int n = nfound[team];
+        if (n > CAP) n = exact_candidates<T, SB, 5>(x, a.vocab, a.k, lo, M, found, &nfound[team], counts, turn, tid);
+        place_candidates<SB, 5, CAP>(found, n, tid, [&](unsigned long long c, int place) {
+            if (place < a.k) put_entry(a, r, place, int(~uint32_t(c)), row.share(logit_of(uint32_t(c >> 32))));
+        });
+        for (int i = n + tid; i < a.k; i += SB) put_entry(a, r, i, -1, kNegInf);
+        sync<SB, 5>();   // before the next row's candidates
+    }
+}
+
+template <typename T, int W, int NV, bool TOP>
+cudaError_t held_launch(const StatsArgs& a, int sms, GroupCache& cache, cudaStream_t s) {
+    auto* kernel = k_held<T, W, NV, TOP>;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = TOP ? size_t(8) * (W == 1 ? 4 * 512 : kCandidates) + size_t(20) * NV * 128 : 0;
+    cfg.stream = s;
+    int groups = 0;
+    cudaError_t e = resident_groups(reinterpret_cast<const void*>(kernel), cfg, RowShape{128, 0}, sms, cache, groups);
+    if (e != cudaSuccess) return e;
+    const int64_t want = (a.rows + 4 / W - 1) / (4 / W);
+    cfg.gridDim.x = unsigned(groups < want ? groups : want);
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+template <typename T, bool TOP> cudaError_t held(const StatsArgs& a, int places, int sms, GroupCache& cache, cudaStream_t s) {
+    if (places <= 128) return held_launch<T, 1, 4, TOP>(a, sms, cache, s);
+    if (places <= 256) return held_launch<T, 1, 8, TOP>(a, sms, cache, s);
+    if (places <= 512) return held_launch<T, 4, 4, TOP>(a, sms, cache, s);
+    if (places <= 1024) return held_launch<T, 4, 8, TOP>(a, sms, cache, s);
+    return held_launch<T, 4, 16, TOP>(a, sms, cache, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -869,7 +1139,8 @@ __global__ void __launch_bounds__(B, (TOP ? 256 : 512) / B) k_stats(const StatsA
         uint32_t lo = kLeast<T>;
         const bool full = a.k <= B && sums.least > kNegInf;   // each thread has a group from the least of their tops on
         if (full) lo = rank_of<T>(sums.least);
-        if (full || count(logit_of(lo << Order<T>::kShift)) > a.k) lo = search_rank<T>(lo, row.M, a.k, count);
+        const int from = full ? B * G : count(logit_of(lo << Order<T>::kShift));
+        if (from > a.k) lo = search_rank<T>(lo, from, row.M, a.k, count);
         const float least = logit_of(lo << Order<T>::kShift);
         // the groups from there on, each CTA its own, and their entries, to the first CTA
         if (top >= least)
@@ -881,28 +1152,28 @@ __global__ void __launch_bounds__(B, (TOP ? 256 : 512) / B) k_stats(const StatsA
         auto store = [&](int i, unsigned long long c) { if (i < kCandidates) store_remote(far_found + 8u * uint32_t(i), c); };
         if (edge && xe >= least) store(add(1), candidate(order_of(xe), pl.edge_at(tid)));
         const int items = nlist[was] << gs;
-        for (int from = tid; from < items; from += 4 * B) {
+        for (int first = tid; first < items; first += 4 * B) {
             uint4 raw[4];
             int at[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int item = from + B * i;
+                const int item = first + B * i;
                 at[i] = -1;
                 if (item < items) {
                     const int e = list[item >> gs], t = e & (B - 1);
                     const int place = t + B * (((e / B) << gs) + (item & ((1 << gs) - 1)));
-                    if (place >= pl.off && place < places) at[i] = pl.lo + place - pl.off;
+                    if (place >= pl.off && place < places) at[i] = pl.head + (pl.lo + place - pl.off) * Vec<T>::N;
                 }
-                if (at[i] >= 0) raw[i] = ld16(x + pl.head + int64_t(at[i]) * Vec<T>::N);
+                if (at[i] >= 0) raw[i] = ld16(x + at[i]);
             }
-            offer_vectors<T>(raw, at, pl.head, least, add, store);
+            offer_vectors<T, 4>(raw, least, [&](int i) { return at[i]; }, add, store);
         }
         cluster_arrive();
         cluster_wait();
         if (rank != 0) continue;
         int n = nfound[was];
         if (n > kCandidates) n = exact_candidates<T, B, 0>(x, a.vocab, a.k, lo, row.M, found, &nfound[was], counts, turn, tid);
-        place_candidates<B, 0>(found, n, tid, [&](unsigned long long c, int place) {
+        place_candidates<B, 0, kCandidates>(found, n, tid, [&](unsigned long long c, int place) {
             if (place < a.k) put_entry(a, r, place, int(~uint32_t(c)), row.share(logit_of(uint32_t(c >> 32))));
         });
         for (int i = n + tid; i < a.k; i += B) put_entry(a, r, i, -1, kNegInf);
@@ -935,20 +1206,19 @@ cudaError_t stats_launch(const StatsArgs& a, int clog, int sms, GroupCache& cach
 
 template <typename T>
 cudaError_t stats(const StatsArgs& a, int sms, GroupCache& cache, cudaStream_t s) {
-    const int vecs = (a.vocab + Vec<T>::N - 1) / Vec<T>::N, threads = vecs < 512 ? 64 : vecs <= 8192 ? 128 : 256;
+    const int vecs = (a.vocab + Vec<T>::N - 1) / Vec<T>::N, threads = vecs <= 8192 ? 128 : 256;
+    if (vecs + 7 <= 2048) return a.k > 0 ? held<T, true>(a, vecs + 7, sms, cache, s) : held<T, false>(a, vecs + 7, sms, cache, s);
     // few rows: spread each over more CTAs while the GPU has idle SMs and the share is over a tile
     int clog = 0;
     while (clog < kMaxClusterLog && a.rows << (clog + 1) <= sms && (threads * 8) << clog < vecs) clog += 1;
     if (a.k == 0) {
-        if (threads == 64) return stats_launch<T, 64, false>(a, clog, sms, cache, s);
         if (threads == 128) return stats_launch<T, 128, false>(a, clog, sms, cache, s);
         return stats_launch<T, 256, false>(a, clog, sms, cache, s);
     }
-    if (clog > 0) {   // more than a tile: never 64 threads
+    if (clog > 0) {
         if (threads == 128) return stats_launch<T, 128, true>(a, clog, sms, cache, s);
         return stats_launch<T, 256, true>(a, clog, sms, cache, s);
     }
-    if (threads == 64) return top_launch<T, 64, 4, 4, 6>(a, sms, cache, s);
     if (threads == 128) return top_launch<T, 128, 4, 4, 3>(a, sms, cache, s);
     return top_launch<T, 256, 4, 4, 2>(a, sms, cache, s);
 }
