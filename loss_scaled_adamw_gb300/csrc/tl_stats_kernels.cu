@@ -69,8 +69,8 @@ template <typename T> struct Running {
     float u = 0.0f;      // the reference's whole number
     bool slow = false;   // element by element, see below
 
-    // 16-bit logits are held above this one (-inf becomes it) before they are widened: one instruction to
-    // two of them, in place of two on their exponents.  That needs the lowest to be far below the
+    // Vectors with an excluded entry (-inf) are summed again, their 16-bit logits held above this one before
+    // they are widened (32-bit ones: their exponents).  That needs the lowest to be far below the
     // reference, 2^-150 of it.
     static constexpr float kFloor = sizeof(T) == 4 ? kNegInf : Vec<T>::kEmpty == 0xfc00fc00u ? -65504.0f : -9.9e29f;
 
@@ -89,31 +89,20 @@ template <typename T> struct Running {
         s += e;
         w = __fmaf_rn(e, z, w);
     }
-    // U vectors, of which the largest element has been through raise().
-    __device__ __forceinline__ void add(const uint4 (&raw)[U], pair_t c2c2, float c2) {
-        if (slow || m == kNegInf) {
-#pragma unroll 1
-            for (int i = 0; i < U; ++i) {
-                const uint4 v = i == 0 ? raw[0] : i == 1 ? raw[1] : i == 2 ? raw[2] : raw[3];
-                float f[N];
-                Vec<T>::wide(v, f);
-#pragma unroll
-                for (int j = 0; j < N; ++j) add_one(f[j], c2);
-            }
-            return;
-        }
+    // The sums of U vectors; HOLD: with elements held above kFloor.
+    template <bool HOLD> __device__ __forceinline__ void sums_of(const uint4 (&raw)[U], pair_t c2c2, float& s_, float& w_) const {
         const pair_t uu = pair_of(-u, -u);
         pair_t s2 = 0, w2 = 0;   // of these vectors first: see tree_sum
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             float f[N];
-            Vec<T>::wide(held(raw[i]), f);
+            Vec<T>::wide(HOLD ? held(raw[i]) : raw[i], f);
 #pragma unroll
             for (int j = 0; j < N; j += 2) {
                 pair_t z = fma_pair(pair_of(f[j], f[j + 1]), c2c2, uu);
                 float z0, z1;
                 apart(z, z0, z1);
-                if (sizeof(T) == 4) {
+                if (HOLD && sizeof(T) == 4) {
                     z0 = max_nan(z0, kLowest);
                     z1 = max_nan(z1, kLowest);
                     z = pair_of(z0, z1);
@@ -125,9 +114,28 @@ template <typename T> struct Running {
         }
         float p0, p1;
         apart(s2, p0, p1);
-        s += p0 + p1;
+        s_ = p0 + p1;
         apart(w2, p0, p1);
-        w += p0 + p1;
+        w_ = p0 + p1;
+    }
+    // U vectors, of which the largest element has been through raise(); whole: none of them is empty.
+    __device__ __forceinline__ void add(const uint4 (&raw)[U], bool whole, pair_t c2c2, float c2) {
+        if (slow || m == kNegInf) {
+#pragma unroll 1
+            for (int i = 0; i < U; ++i) {
+                const uint4 v = i == 0 ? raw[0] : i == 1 ? raw[1] : i == 2 ? raw[2] : raw[3];
+                float f[N];
+                Vec<T>::wide(v, f);
+#pragma unroll
+                for (int j = 0; j < N; ++j) add_one(f[j], c2);
+            }
+            return;
+        }
+        float ds = 0.0f, dw = __int_as_float(0x7fffffff);
+        if (whole) sums_of<false>(raw, c2c2, ds, dw);
+        if (dw != dw) sums_of<true>(raw, c2c2, ds, dw);   // 0 times an excluded entry's exponent, or a NaN entry
+        s += ds;
+        w += dw;
     }
     static __device__ __forceinline__ uint4 held(uint4 v) {
         if constexpr (sizeof(T) == 2) {
@@ -202,16 +210,16 @@ __device__ __forceinline__ unsigned long long candidate(uint32_t order, int id) 
 
 constexpr int kCandidates = 1024;
 
-// Barriers of the first SB threads that take part (barrier ID).
-template <int SB, int ID> __device__ __forceinline__ void sync() {
-    if constexpr (SB == 32) __syncwarp(); else bar_sync(ID, SB);
+// Barrier `bar` of the SB threads that choose a row's entries.
+template <int SB> __device__ __forceinline__ void sync(int bar) {
+    if constexpr (SB == 32) __syncwarp(); else bar_sync(bar, SB);
 }
 // The sum of v over them; `sh` holds 2 x 8 numbers, used in turns (`turn` flips).
-template <int SB, int ID> __device__ __forceinline__ int sum_over(int v, int (*sh)[8], int& turn, int tid) {
+template <int SB> __device__ __forceinline__ int sum_over(int v, int (*sh)[8], int& turn, int tid, int bar) {
     v = __reduce_add_sync(~0u, v);
     if constexpr (SB == 32) return v;
     if ((tid & 31) == 0) sh[turn][tid >> 5] = v;
-    sync<SB, ID>();
+    sync<SB>(bar);
     v = 0;
 #pragma unroll
     for (int i = 0; i < SB / 32; ++i) v += sh[turn][i];
@@ -221,9 +229,9 @@ template <int SB, int ID> __device__ __forceinline__ int sum_over(int v, int (*s
 
 // More candidates than fit: the k-th largest entry itself.  At least k entries are >= lo, M is the
 // largest.  Every count is a pass over the row, out of L2.  Gives the number of candidates, at most k.
-template <typename T, int SB, int ID>
+template <typename T, int SB>
 __device__ __noinline__ int exact_candidates(const T* x, int vocab, int k, uint32_t lo, float M, unsigned long long* found,
-                                             int* nfound, int (*sh)[8], int turn, int tid) {
+                                             int* nfound, int (*sh)[8], int turn, int tid, int bar) {
     const int warp = tid >> 5, lane = tid & 31;
     uint32_t hi = rank_of<T>(M) + 1;   // fewer than k are >= hi
     bool first = true;                 // thousands of equal entries: the next rank already has fewer than k
@@ -232,16 +240,16 @@ __device__ __noinline__ int exact_candidates(const T* x, int vocab, int k, uint3
         first = false;
         int c = 0;
         for (int j = tid; j < vocab; j += SB) c += rank_of<T>(to_f(x[j])) >= mid;
-        if (sum_over<SB, ID>(c, sh, turn, tid) >= k) lo = mid; else hi = mid;
+        if (sum_over<SB>(c, sh, turn, tid, bar) >= k) lo = mid; else hi = mid;
     }
-    sync<SB, ID>();
+    sync<SB>(bar);
     if (tid == 0) *nfound = 0;
-    sync<SB, ID>();
+    sync<SB>(bar);
     for (int j = tid; j < vocab; j += SB) {   // fewer than k
         const uint32_t o = order_of(to_f(x[j]));
         if (o >> Order<T>::kShift > lo) found[atomicAdd(nfound, 1)] = candidate(o, j);
     }
-    sync<SB, ID>();
+    sync<SB>(bar);
     int n = *nfound;
     // of those equal to the k-th the first ones
     for (int base = 0; n < k && base < vocab; base += SB) {
@@ -252,7 +260,7 @@ __device__ __noinline__ int exact_candidates(const T* x, int vocab, int k, uint3
         int before = __popc(ones & ((1u << lane) - 1)), all = __popc(ones);
         if constexpr (SB > 32) {
             if (lane == 0) sh[turn][warp] = all;
-            sync<SB, ID>();
+            sync<SB>(bar);
             all = 0;
 #pragma unroll
             for (int v = 0; v < SB / 32; ++v) {
@@ -264,21 +272,21 @@ __device__ __noinline__ int exact_candidates(const T* x, int vocab, int k, uint3
         if (equal && n + before < k) found[n + before] = candidate(o, j);
         n += all;
     }
-    sync<SB, ID>();
+    sync<SB>(bar);
     return min(n, k);
 }
 
 // The n candidates in order, each thread E of them in registers: candidate (warp E + e) 32 + lane of the
 // sorted list is settled by that lane.  A bitonic network: neighbours up to 16 apart by shuffles, up to
 // 32 E / 2 apart in registers, further ones through shared memory.
-template <int SB, int ID, int E, typename F>
-__device__ __forceinline__ void sort_by(unsigned long long* found, int n, int tid, F settle) {
+template <int SB, int E, typename F>
+__device__ __forceinline__ void sort_by(unsigned long long* found, int n, int tid, int bar, F settle) {
     const int warp = tid >> 5, lane = tid & 31, base = warp * E * 32 + lane;
     unsigned long long c[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) c[e] = base + 32 * e < n ? found[base + 32 * e] : 0;
     auto keep = [](unsigned long long mine, unsigned long long other, bool larger) { return larger == (mine > other) ? mine : other; };
-    if (SB > 32) sync<SB, ID>();   // the list has been read
+    if (SB > 32) sync<SB>(bar);   // the list has been read
 #pragma unroll 1
     for (int size = 2; size < 2 * n; size *= 2) {   // the largest candidates first where `size` is not in the index
         if (SB > 32) {
@@ -286,13 +294,13 @@ __device__ __forceinline__ void sort_by(unsigned long long* found, int n, int ti
             for (int d = size / 2; d >= 32 * E; d /= 2) {
 #pragma unroll
                 for (int e = 0; e < E; ++e) found[base + 32 * e] = c[e];
-                sync<SB, ID>();
+                sync<SB>(bar);
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
                     const int i = base + 32 * e;
                     c[e] = keep(c[e], found[i ^ d], ((i & size) == 0) == ((i & d) == 0));
                 }
-                sync<SB, ID>();
+                sync<SB>(bar);
             }
         }
 #pragma unroll
@@ -323,15 +331,19 @@ __device__ __forceinline__ void sort_by(unsigned long long* found, int n, int ti
     for (int e = 0; e < E; ++e)
         if (base + 32 * e < n) settle(c[e], base + 32 * e);
 }
-// CAP: the list's length, at most 16 per thread.
-template <int SB, int ID, int CAP, typename F>
-__device__ __forceinline__ void place_candidates(unsigned long long* found, int n, int tid, F settle) {
-    if (n <= SB) return sort_by<SB, ID, 1>(found, n, tid, settle);
-    if (n <= 2 * SB) return sort_by<SB, ID, 2>(found, n, tid, settle);
-    if (n <= 4 * SB || CAP <= 4 * SB) return sort_by<SB, ID, 4>(found, n, tid, settle);
+// CAP: the list's length, at most 16 per thread.  Short lists are one warp's work: no barrier.
+template <int SB, int CAP, typename F>
+__device__ __forceinline__ void place_candidates(unsigned long long* found, int n, int tid, int bar, F settle) {
+    if (n <= 128) {
+        if (tid >= 32) return;
+        if (n <= 32) return sort_by<32, 1>(found, n, tid, bar, settle);
+        if (n <= 64) return sort_by<32, 2>(found, n, tid, bar, settle);
+        return sort_by<32, 4>(found, n, tid, bar, settle);
+    }
+    if (n <= 4 * SB || CAP <= 4 * SB) return sort_by<SB, 4>(found, n, tid, bar, settle);
     if constexpr (CAP > 4 * SB)
-        if (n <= 8 * SB || CAP <= 8 * SB) return sort_by<SB, ID, 8>(found, n, tid, settle);
-    if constexpr (CAP > 8 * SB) sort_by<SB, ID, 16>(found, n, tid, settle);
+        if (n <= 8 * SB || CAP <= 8 * SB) return sort_by<SB, 8>(found, n, tid, bar, settle);
+    if constexpr (CAP > 8 * SB) sort_by<SB, 16>(found, n, tid, bar, settle);
 }
 
 // Other CTAs' shared memory.
@@ -352,18 +364,18 @@ __device__ __forceinline__ int add_remote(uint32_t to, int v) {
     return r;
 }
 
-// What a row's sums amount to; by every lane of a warp, whose lanes 0 .. n - 1 (n <= 8) hold the parts
+// What a row's sums amount to; by every lane of a warp, whose lanes 0 .. n - 1 (n <= PARTS) hold the parts
 // (largest entry, S, W, and the least of the threads' largest entries).
 struct RowSums {
     float M, S, W, least;
 };
-__device__ __forceinline__ RowSums join_parts(float4 p, float c2) {
+template <int PARTS> __device__ __forceinline__ RowSums join_parts(float4 p, float c2) {
     RowSums r;
     r.M = warp_max(p.x);
     r.least = -warp_max(-p.w);
     move_sums(p.x, part_ref(r.M), c2, p.y, p.z);
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) {
+    for (int o = PARTS / 2; o > 0; o >>= 1) {
         p.y += __shfl_xor_sync(~0u, p.y, o);
         p.z += __shfl_xor_sync(~0u, p.z, o);
     }
@@ -435,29 +447,33 @@ __device__ __forceinline__ void ignored_row(const StatsArgs& a, int64_t r, int t
 template <typename T, int B, int TV, int ST> struct Feed {
     static constexpr int N = Vec<T>::N, tile = B * TV;
     const StatsArgs& a;
-    uint4* const ring;
     const int ngroups, rank, clog, tid;
     const bool alike;   // all rows lie alike where their stride is a multiple of 128 bytes
     const Place<T> first;
     int64_t fr, fynext;
-    const T* fat = nullptr;    // this thread's next vector
+    uint4* const ring;         // this thread's first place
+    const T* fat = nullptr;    // its next vector
     int fleft = 0, foff = 0;   // places left of the share, empty ones before the next vector
-    int slot = -1;             // of the tile last taken
+    uint32_t put;              // this thread's place in the slot that is filled next, and in the tile last taken
+    uint32_t got;
+    const uint32_t begin, end;
 
     __device__ __forceinline__ Feed(const StatsArgs& args, uint4* smem, int group, int groups, int r, int c, int t)
-        : a(args), ring(smem), ngroups(groups), rank(r), clog(c), tid(t), alike((args.ld * int(sizeof(T))) % 128 == 0),
+        : a(args), ngroups(groups), rank(r), clog(c), tid(t), alike((args.ld * int(sizeof(T))) % 128 == 0),
           first(static_cast<const T*>(args.x), args.vocab, r, c), fr(group - groups),
-          fynext(args.target && group < args.rows ? args.target[group] : 0) {
+          fynext(args.target && group < args.rows ? args.target[group] : 0), ring(smem + t),
+          begin(static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + 16u * uint32_t(t)), end(begin + 16u * ST * tile) {
+        put = begin;
+        got = end - 16u * tile;
 #pragma unroll
-        for (int i = 0; i < ST - 1; ++i) fetch(i);
+        for (int i = 0; i < ST - 1; ++i) fetch();
     }
     __device__ __forceinline__ const T* row_at(int64_t r) const { return static_cast<const T*>(a.x) + r * a.ld; }
     __device__ __forceinline__ Place<T> place_of(const T* x) const { return alike ? first : Place<T>(x, a.vocab, rank, clog); }
-    static __device__ __forceinline__ uint4 empty() { return make_uint4(Vec<T>::kEmpty, Vec<T>::kEmpty, Vec<T>::kEmpty, Vec<T>::kEmpty); }
-    __device__ __forceinline__ void fetch(int to_slot) {
+    __device__ __forceinline__ void edge_tile() {   // a row's first or last tile
         while (fleft <= 0) {   // the next row that is not ignored and of which this CTA has a share
             fr += ngroups;
-            if (fr >= a.rows) break;
+            if (fr >= a.rows) return;   // behind the last row a copy group is empty
             const int64_t y = fynext;
             if (a.target && fr + ngroups < a.rows) fynext = a.target[fr + ngroups];
             if (y < 0) continue;
@@ -467,28 +483,32 @@ template <typename T, int B, int TV, int ST> struct Feed {
             fleft = pl.hi > pl.lo ? pl.hi - pl.lo + pl.off : 0;
             fat = x + pl.head + int64_t(pl.lo + tid - pl.off) * N;
         }
-        const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + 16u * uint32_t(to_slot * tile + tid);
-        if (fleft >= tile && foff == 0) {
 #pragma unroll
-            for (int i = 0; i < TV; ++i) copy_async(to + 16u * B * i, fat + B * N * i);
-        } else {   // behind the last row a copy group is empty
+        for (int i = 0; i < TV; ++i)
+            if (tid + B * i < fleft && (i > 0 || tid >= foff)) copy_async(put + 16u * B * i, fat + B * N * i);
+        if (tid < foff) ring[(put - begin) / 16] = make_uint4(Vec<T>::kEmpty, Vec<T>::kEmpty, Vec<T>::kEmpty, Vec<T>::kEmpty);
+        foff = 0;
+    }
+    __device__ __forceinline__ void fetch() {
+        if (fleft >= tile) {
 #pragma unroll
-            for (int i = 0; i < TV; ++i)
-                if (tid + B * i < fleft && (i > 0 || tid >= foff)) copy_async(to + 16u * B * i, fat + B * N * i);
-            if (tid < foff) ring[to_slot * tile + tid] = empty();
-            foff = 0;
+            for (int i = 0; i < TV; ++i) copy_async(put + 16u * B * i, fat + B * N * i);
+        } else {
+            edge_tile();
         }
+        copy_commit();
         fat += tile * N;
         fleft -= tile;
-        copy_commit();
+        put += 16u * tile;
+        if (put == end) put = begin;
     }
     // The next tile; the one before is done with, its slot is the next to fill.
     __device__ __forceinline__ const uint4* take() {
-        const int before = slot;
-        slot = slot + 1 == ST ? 0 : slot + 1;
-        fetch(before < 0 ? ST - 1 : before);
+        fetch();
         copy_wait<ST - 1>();
-        return ring + slot * tile + tid;
+        got += 16u * tile;
+        if (got == end) got = begin;
+        return ring + (got - begin) / 16;
     }
 };
 // Four of a tile's vectors, from the g-th on, for a thread that has `mine` places left in it.
@@ -667,29 +687,33 @@ __device__ __forceinline__ void offer_staged(const Stage& st, int m, float least
 // A CTA per row: warps that read rows, and warps that choose entries
 // ---------------------------------------------------------------------------
 
-constexpr int kSlots = 16;    // groups of vectors per thread
+constexpr int kSlots = 8;     // groups of vectors per thread
 constexpr int kList = 1024;   // groups that are read again; more: the exact search
 
-template <int B> constexpr size_t top_smem(int tv, int st) {
-    return size_t(16) * st * tv * B + size_t(8) * kCandidates + size_t(4) * 2 * (kSlots + 1) * B + size_t(2) * kList;
-}
+template <int B, int NT, int TV, int ST> struct TopShared {   // dynamic shared memory of a CTA
+    uint4 ring[ST][TV * B];
+    unsigned long long found[NT][kCandidates];
+    float gmax[NT + 1][kSlots + 1][B];   // per row: of a thread's groups, of all its vectors
+    uint16_t list[NT][kList];
+};
 
-// B threads read rows and leave the maxima of groups, SB others choose the entries of a row while the
-// former are in the next one.  Named barriers 1 and 2 (by row parity): a row's maxima and sums are there;
-// 3 and 4: they have been used; 5: the choosing warps alone.
-template <typename T, int B, int TV, int ST, int PER_SM>
-__global__ void __launch_bounds__(B + B / 2, PER_SM) k_top(const StatsArgs a) {
-    constexpr int SB = B / 2, nw = B / 32, G = kSlots, KEYS = 16;
-    __shared__ float4 wparts[2][8];
-    __shared__ int counts[2][8], nfound[2], nlist[2], nstage;
-    extern __shared__ __align__(128) uint4 ring[];   // [ST][TV * B]
-    unsigned long long* const found = reinterpret_cast<unsigned long long*>(ring + ST * TV * B);   // [kCandidates]
-    float(*const gmax)[B] = reinterpret_cast<float(*)[B]>(found + kCandidates);   // [2][G + 1][B]: of the groups, of all
-    uint16_t* const list = reinterpret_cast<uint16_t*>(gmax + 2 * (G + 1));       // [kList]
+// B threads read rows and leave the maxima of groups; NT teams of SB threads take rows in turns and
+// choose their entries while the former are in the next rows.  NT + 1 rows' maxima are kept (`buffer`).
+// Named barriers 1 + buffer: a row's maxima and sums are there; 1 + NT + 1 + buffer: they have been used;
+// then one per team.
+template <typename T, int B, int SB, int NT, int TV, int ST, int PER_SM>
+__global__ void __launch_bounds__(B + NT * SB, PER_SM) k_top(const StatsArgs a) {
+    constexpr int N = Vec<T>::N, nw = B / 32, G = kSlots, NB = NT + 1, HELD = B / SB, KEYS = HELD * 4;
+    static_assert(nw <= 16 && 2 * NB + NT < 16, "parts of a row for half a warp, 16 named barriers");
+    __shared__ float4 wparts[NB][nw];
+    __shared__ int counts[NT][2][8], nfound[NT], nlist[NT], nstage[NT];
+    extern __shared__ __align__(128) uint4 ring[];
+    TopShared<B, NT, TV, ST>& sh = *reinterpret_cast<TopShared<B, NT, TV, ST>*>(ring);
     const int lane = threadIdx.x & 31;
     const float c2 = a.c2;
     const int group = blockIdx.x, ngroups = gridDim.x;
-    int par = 0;
+    int buffer = 0;
+    auto next = [&]() { buffer = buffer + 1 == NB ? 0 : buffer + 1; };
     int64_t ynext = a.target && group < a.rows ? a.target[group] : 0;
     auto label = [&](int64_t r) {
         const int64_t y = ynext;
@@ -701,7 +725,7 @@ __global__ void __launch_bounds__(B + B / 2, PER_SM) k_top(const StatsArgs a) {
         const int tid = threadIdx.x, warp = tid >> 5;
         Feed<T, B, TV, ST> feed(a, ring, group, ngroups, 0, 0, tid);
         const pair_t c2c2 = pair_of(c2, c2);
-        int done = 0;   // rows so far, up to 2
+        int done = 0;   // rows so far, up to NB
         for (int64_t r = group; r < a.rows; r += ngroups) {
             if (label(r) < 0) continue;
             const T* const x = feed.row_at(r);
@@ -710,8 +734,8 @@ __global__ void __launch_bounds__(B + B / 2, PER_SM) k_top(const StatsArgs a) {
             const float xe = edge ? to_f(x[pl.edge_at(tid)]) : kNegInf;
             const int places = pl.hi > pl.lo ? pl.hi - pl.lo + pl.off : 0;
             const int gs = group_shift((places + TV * B - 1) / (TV * B) * TV, G);
-            if (done == 2) bar_sync(3 + par, B + SB); else ++done;
-            float(*const gm)[B] = gmax + par * (G + 1);
+            if (done == NB) bar_sync(1 + NB + buffer, B + SB); else ++done;
+            float(*const gm)[B] = sh.gmax[buffer];
 #pragma unroll
             for (int g = 0; g < G; ++g) gm[g][tid] = kNegInf;
             Running<T> sum;
@@ -727,31 +751,37 @@ __global__ void __launch_bounds__(B + B / 2, PER_SM) k_top(const StatsArgs a) {
                     const float t = keep_maxima<T, B>(gm, gs, base + g, raw, run, tid);
                     top = fmaxf(top, t);
                     sum.raise(t, c2);
-                    sum.add(raw, c2c2, c2);
+                    sum.add(raw, B * (g + 3) < mine, c2c2, c2);
                 }
             }
             gm[G][tid] = top;
             const float4 part = warp_part(sum, top, xe, edge, c2);
-            if (lane == 0) wparts[par][warp] = part;
-            bar_arrive(1 + par, B + SB);
-            par ^= 1;
+            if (lane == 0) wparts[buffer][warp] = part;
+            bar_arrive(1 + buffer, B + SB);
+            next();
         }
-        if (done == 2) bar_sync(3 + par, B + SB);
-        if (done > 0) bar_sync(3 + (done == 2 ? par ^ 1 : 0), B + SB);
+        // the teams' last rows
+        for (int i = 0; i < done; ++i) {
+            buffer = buffer == 0 ? NB - 1 : buffer - 1;
+            bar_sync(1 + NB + buffer, B + SB);
+        }
         copy_wait<0>();
         return;
     }
     // ---------------------------------------------------------------- the entries
-    const int tid = threadIdx.x - B, warp = tid >> 5;
+    const int team = (threadIdx.x - B) / SB, tid = (threadIdx.x - B) % SB, warp = tid >> 5, bar = 1 + 2 * NB + team;
     const bool alike = (a.ld * int(sizeof(T))) % 128 == 0;
     const Place<T> first(static_cast<const T*>(a.x), a.vocab, 0, 0);
-    int turn = 0;
-    for (int64_t r = group; r < a.rows; r += ngroups) {
-        const int64_t y = label(r);
-        if (y < 0) {
-            ignored_row(a, r, tid, SB);
-            continue;
-        }
+    unsigned long long* const found = sh.found[team];
+    uint16_t* const list = sh.list[team];
+    int turn = 0, whose = NT - 1;
+    for (int64_t r = group; r < a.rows; r += ngroups, next()) {
+        int64_t y = label(r);
+        for (; y < 0 && r < a.rows; r += ngroups, y = r < a.rows ? label(r) : 0)
+            if (team == 0) ignored_row(a, r, tid, SB);
+        if (r >= a.rows) break;
+        whose = whose + 1 == NT ? 0 : whose + 1;
+        if (whose != team) continue;
         const T* const x = static_cast<const T*>(a.x) + r * a.ld;
         const Place<T> pl = alike ? first : Place<T>(x, a.vocab, 0, 0);
         const bool edge = tid < pl.edges;
@@ -759,43 +789,46 @@ __global__ void __launch_bounds__(B + B / 2, PER_SM) k_top(const StatsArgs a) {
         const float xy = warp == 0 && a.logp && y < a.vocab ? to_f(x[y]) : 0.0f;
         const int places = pl.hi > pl.lo ? pl.hi - pl.lo + pl.off : 0;
         const int gs = group_shift((places + TV * B - 1) / (TV * B) * TV, G);
-        const float(*const gm)[B] = gmax + par * (G + 1);
-        if (tid == 0) nfound[par] = nlist[par] = 0;
-        bar_sync(1 + par, B + SB);
-        const RowSums sums = join_parts(lane < nw ? wparts[par][lane] : make_float4(kNegInf, 0.0f, 0.0f, INFINITY), c2);
+        const float(*const gm)[B] = sh.gmax[buffer];
+        if (tid == 0) nfound[team] = nlist[team] = 0;
+        bar_sync(1 + buffer, B + SB);
+        const RowSums sums = join_parts<nw>(lane < nw ? wparts[buffer][lane] : make_float4(kNegInf, 0.0f, 0.0f, INFINITY), c2);
         const RowSoftmax row(sums, a);
         if (warp == 0) row.finish(a, r, y, xy);
         if (row.none) {
             for (int i = tid; i < a.k; i += SB) put_entry(a, r, i, -1, row.share(0.0f));
-            bar_arrive(3 + par, B + SB);
-            par ^= 1;
+            bar_arrive(1 + NB + buffer, B + SB);
             continue;
         }
         // The sets among which t is searched: the threads' vectors as wholes while there are twice as many
-        // as k (the k largest of 4 k sets have 1.15 k entries >= t, of 2 k 1.39 k), else 2, 4 or 8 to a thread.
-        const int ss = 2 * a.k <= B ? 0 : a.k <= B ? 1 : a.k <= 2 * B ? 2 : 3;   // log2 of that
-        float key[KEYS];   // of two threads
+        // as k (the k largest of 4 k sets have 1.15 k entries >= t, of 2 k 1.39 k), else 2 or 4 to a thread.
+        const int ss = 2 * a.k <= B ? 0 : a.k <= B ? 1 : 2;   // log2 of that
+        float key[KEYS];   // of HELD threads
+#pragma unroll
+        for (int i = 0; i < KEYS; ++i) key[i] = kNegInf;
         if (ss == 0) {
-            key[0] = gm[G][tid];
-            key[1] = gm[G][tid + SB];
+#pragma unroll
+            for (int i = 0; i < HELD; ++i) key[i] = gm[G][tid + i * SB];
         } else {
 #pragma unroll
-            for (int i = 0; i < KEYS; ++i) {
-                key[i] = kNegInf;
-                const int width = G >> ss;   // slots of a set
-                if (i < 2 << ss)
-                    for (int g = 0; g < width; ++g) key[i] = fmaxf(key[i], gm[(i >> 1) * width + g][tid + (i & 1) * SB]);
-            }
+            for (int i = 0; i < HELD; ++i)
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    const float v = gm[g][tid + i * SB];
+                    if (ss == 1) key[4 * i + g / 4] = fmaxf(key[4 * i + g / 4], v);
+                    else key[4 * i + g / 2] = fmaxf(key[4 * i + g / 2], v);
+                }
         }
         auto count = [&](float v) {
             int c = 0;
             if (ss == 0) {
-                c = (key[0] >= v) + (key[1] >= v);
+#pragma unroll
+                for (int i = 0; i < HELD; ++i) c += key[i] >= v;
             } else {
 #pragma unroll
-                for (int i = 0; i < KEYS; ++i) c += i < 2 << ss && key[i] >= v ? 1 : 0;
+                for (int i = 0; i < KEYS; ++i) c += key[i] >= v;
             }
-            return sum_over<SB, 5>(c, counts, turn, tid);
+            return sum_over<SB>(c, counts[team], turn, tid, bar);
         };
         uint32_t lo = kLeast<T>;
         const bool full = a.k <= B && sums.least > kNegInf;   // each thread has a set from the least of their tops on
@@ -805,22 +838,24 @@ __global__ void __launch_bounds__(B + B / 2, PER_SM) k_top(const StatsArgs a) {
         const float least = logit_of(lo << Order<T>::kShift);
         // the groups from there on
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < HELD; ++h) {
             const int t = tid + h * SB;
             if (!(gm[G][t] >= least)) continue;
             unsigned some = 0;
 #pragma unroll
             for (int g = 0; g < G; ++g) some |= gm[g][t] >= least ? 1u << g : 0u;
-            int i = atomicAdd(&nlist[par], __popc(some));
+            int i = atomicAdd(&nlist[team], __popc(some));
             for (; some != 0 && i < kList; some &= some - 1) list[i++] = uint16_t((__ffs(some) - 1) * B + t);
         }
-        if (edge && xe >= least) found[atomicAdd(&nfound[par], 1)] = candidate(order_of(xe), pl.edge_at(tid));
-        sync<SB, 5>();
-        const int groups = nlist[par], items = groups > kList ? 0 : groups << gs;
-        const Stage stage{reinterpret_cast<uint4*>(gmax + par * (G + 1)),   // where the maxima have been
-                          reinterpret_cast<int*>(gmax + par * (G + 1) + G / 2), &nstage};
+        if (edge && xe >= least) found[atomicAdd(&nfound[team], 1)] = candidate(order_of(xe), pl.edge_at(tid));
+        sync<SB>(bar);
+        const int groups = nlist[team], items = groups > kList ? 0 : groups << gs;
+        // where the maxima have been: 4 SB vectors and their ids
+        static_assert(80 * SB <= int(sizeof(sh.gmax[0])), "a round's vectors take the place of a row's maxima");
+        uint4* const staged = reinterpret_cast<uint4*>(sh.gmax[buffer]);
+        const Stage stage{staged, reinterpret_cast<int*>(staged + 4 * SB), &nstage[team]};
         for (int base = 0; base < items; base += 4 * SB) {
-            if (tid == 0) nstage = 0;
+            if (tid == 0) nstage[team] = 0;
             uint4 raw[4];
             int at[4];
             unsigned pass = 0;
@@ -831,41 +866,40 @@ __global__ void __launch_bounds__(B + B / 2, PER_SM) k_top(const StatsArgs a) {
                 if (item < items) {
                     const int e = list[item >> gs], t = e & (B - 1);
                     const int place = t + B * (((e / B) << gs) + (item & ((1 << gs) - 1)));
-                    if (place >= pl.off && place < places) at[i] = pl.head + (pl.lo + place - pl.off) * Vec<T>::N;
+                    if (place >= pl.off && place < places) at[i] = pl.head + (pl.lo + place - pl.off) * N;
                 }
                 if (at[i] >= 0) raw[i] = ld16(x + at[i]);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) pass |= at[i] >= 0 && Vec<T>::top(raw[i]) >= least ? 1u << i : 0u;
-            sync<SB, 5>();
+            sync<SB>(bar);
             stage_vectors<4>(raw, pass, [&](int i) { return at[i]; }, stage);
-            sync<SB, 5>();
-            offer_staged<T, SB, kCandidates>(stage, nstage, least, found, &nfound[par], tid);
-            sync<SB, 5>();
+            sync<SB>(bar);
+            offer_staged<T, SB, kCandidates>(stage, nstage[team], least, found, &nfound[team], tid);
+            sync<SB>(bar);
         }
-        bar_arrive(3 + par, B + SB);   // the maxima have been used
-        int n = nfound[par];
+        bar_arrive(1 + NB + buffer, B + SB);   // the maxima have been used
+        int n = nfound[team];
         if (n > kCandidates || groups > kList)
-            n = exact_candidates<T, SB, 5>(x, a.vocab, a.k, lo, row.M, found, &nfound[par], counts, turn, tid);
-        place_candidates<SB, 5, kCandidates>(found, n, tid, [&](unsigned long long c, int place) {
+            n = exact_candidates<T, SB>(x, a.vocab, a.k, lo, row.M, found, &nfound[team], counts[team], turn, tid, bar);
+        place_candidates<SB, kCandidates>(found, n, tid, bar, [&](unsigned long long c, int place) {
             if (place < a.k) put_entry(a, r, place, int(~uint32_t(c)), row.share(logit_of(uint32_t(c >> 32))));
         });
         for (int i = n + tid; i < a.k; i += SB) put_entry(a, r, i, -1, kNegInf);
-        sync<SB, 5>();   // before the next row's candidates
-        par ^= 1;
+        sync<SB>(bar);   // before the next row's candidates
     }
 }
 
-template <typename T, int B, int TV, int ST, int PER_SM>
+template <typename T, int B, int SB, int NT, int TV, int ST, int PER_SM>
 cudaError_t top_launch(const StatsArgs& a, int sms, GroupCache& cache, cudaStream_t s) {
-    auto* kernel = k_top<T, B, TV, ST, PER_SM>;
+    auto* kernel = k_top<T, B, SB, NT, TV, ST, PER_SM>;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(1);
-    cfg.blockDim = dim3(B + B / 2);
-    cfg.dynamicSmemBytes = top_smem<B>(TV, ST);
+    cfg.blockDim = dim3(B + NT * SB);
+    cfg.dynamicSmemBytes = sizeof(TopShared<B, NT, TV, ST>);
     cfg.stream = s;
     int groups = 0;
-    cudaError_t e = resident_groups(reinterpret_cast<const void*>(kernel), cfg, RowShape{B + B / 2, 0}, sms, cache, groups);
+    cudaError_t e = resident_groups(reinterpret_cast<const void*>(kernel), cfg, RowShape{B + NT * SB, 0}, sms, cache, groups);
     if (e != cudaSuccess) return e;
     cfg.gridDim.x = unsigned(groups < a.rows ? groups : a.rows);
     return cudaLaunchKernelEx(&cfg, kernel, a);
@@ -937,7 +971,7 @@ __global__ void __launch_bounds__(128, NV > 8 ? 3 : NV > 4 ? 4 : 6) k_held(const
 #pragma unroll
         for (int i = 0; i < NV; i += 4) {
             const uint4 four[4] = {raw[i], raw[i + 1], raw[i + 2], raw[i + 3]};
-            sum.add(four, c2c2, c2);
+            sum.add(four, (i + 3) * SB + tid - pl.off < pl.body && (i > 0 || tid >= pl.off), c2c2, c2);
         }
         if (edge) sum.add_one(xe, c2);
         RowSums sums{M, warp_sum(sum.s), warp_sum(sum.w), kNegInf};
@@ -962,7 +996,7 @@ __global__ void __launch_bounds__(128, NV > 8 ? 3 : NV > 4 ? 4 : 6) k_held(const
                 int c = 0;
 #pragma unroll
                 for (int i = 0; i < NV; ++i) c += tops[i] >= v;
-                return sum_over<SB, 5>(c, counts, turn, tid);
+                return sum_over<SB>(c, counts, turn, tid, 1);
             };
             const bool full = low > kNegInf;
             if (full) lo = rank_of<T>(low);
@@ -978,7 +1012,7 @@ __global__ void __launch_bounds__(128, NV > 8 ? 3 : NV > 4 ? 4 : 6) k_held(const
 #pragma unroll
                     for (int j = 0; j < N; ++j) c += f[j] >= v;
                 }
-                return sum_over<SB, 5>(c, counts, turn, tid);
+                return sum_over<SB>(c, counts, turn, tid, 1);
             };
             const int from = count(logit_of(lo << Order<T>::kShift));
             if (from > a.k) lo = search_rank<T>(lo, from, M, a.k, count);
@@ -989,16 +1023,16 @@ __global__ void __launch_bounds__(128, NV > 8 ? 3 : NV > 4 ? 4 : 6) k_held(const
 #pragma unroll
         for (int i = 0; i < NV; ++i) pass |= tops[i] >= least ? 1u << i : 0u;
         stage_vectors<NV>(raw, pass, [&](int i) { return pl.head + (i * SB + tid - pl.off) * N; }, stage);
-        sync<SB, 5>();
+        sync<SB>(1);
         offer_staged<T, SB, CAP>(stage, nstage[team], least, found, &nfound[team], tid);
-        sync<SB, 5>();
+        sync<SB>(1);
         int n = nfound[team];
-        if (n > CAP) n = exact_candidates<T, SB, 5>(x, a.vocab, a.k, lo, M, found, &nfound[team], counts, turn, tid);
-        place_candidates<SB, 5, CAP>(found, n, tid, [&](unsigned long long c, int place) {
+        if (n > CAP) n = exact_candidates<T, SB>(x, a.vocab, a.k, lo, M, found, &nfound[team], counts, turn, tid, 1);
+        place_candidates<SB, CAP>(found, n, tid, 1, [&](unsigned long long c, int place) {
             if (place < a.k) put_entry(a, r, place, int(~uint32_t(c)), row.share(logit_of(uint32_t(c >> 32))));
         });
         for (int i = n + tid; i < a.k; i += SB) put_entry(a, r, i, -1, kNegInf);
-        sync<SB, 5>();   // before the next row's candidates
+        sync<SB>(1);   // before the next row's candidates
     }
 }
 
@@ -1089,7 +1123,7 @@ __global__ void __launch_bounds__(B, (TOP ? 256 : 512) / B) k_stats(const StatsA
                 const float t = TOP ? keep_maxima<T, B>(gmax + rank * own, gs, base + g, raw, run, tid) : top_of<T>(raw);
                 top = fmaxf(top, t);
                 sum.raise(t, c2);
-                sum.add(raw, c2c2, c2);
+                sum.add(raw, B * (g + 3) < mine, c2c2, c2);
             }
         }
         {
@@ -1101,7 +1135,7 @@ __global__ void __launch_bounds__(B, (TOP ? 256 : 512) / B) k_stats(const StatsA
         __syncthreads();
         if (cluster > 1) {
             if (warp == 0) {
-                const RowSums p = join_parts(lane < nw ? wparts[par][lane] : none_part, c2);
+                const RowSums p = join_parts<8>(lane < nw ? wparts[par][lane] : none_part, c2);
                 if (lane < cluster) store_remote(&cparts[par][rank], uint32_t(lane), make_float4(p.M, p.S, p.W, p.least));
             }
             if (TOP)
@@ -1117,8 +1151,8 @@ __global__ void __launch_bounds__(B, (TOP ? 256 : 512) / B) k_stats(const StatsA
         par ^= 1;
         finisher = finisher + 1 == nw ? 0 : finisher + 1;
         if (!TOP && !finishes) continue;
-        const RowSums sums = cluster > 1 ? join_parts(lane < cluster ? cparts[was][lane] : none_part, c2)
-                                         : join_parts(lane < nw ? wparts[was][lane] : none_part, c2);
+        const RowSums sums = cluster > 1 ? join_parts<8>(lane < cluster ? cparts[was][lane] : none_part, c2)
+                                         : join_parts<8>(lane < nw ? wparts[was][lane] : none_part, c2);
         const RowSoftmax row(sums, a);
         if (finishes) row.finish(a, r, y, xy);
         if (!TOP) continue;
@@ -1134,7 +1168,7 @@ __global__ void __launch_bounds__(B, (TOP ? 256 : 512) / B) k_stats(const StatsA
             int c = 0;
 #pragma unroll
             for (int g = 0; g < G; ++g) c += key[g] >= v;
-            return sum_over<B, 0>(c, counts, turn, tid);
+            return sum_over<B>(c, counts, turn, tid, 0);
         };
         uint32_t lo = kLeast<T>;
         const bool full = a.k <= B && sums.least > kNegInf;   // each thread has a group from the least of their tops on
@@ -1172,8 +1206,8 @@ __global__ void __launch_bounds__(B, (TOP ? 256 : 512) / B) k_stats(const StatsA
         cluster_wait();
         if (rank != 0) continue;
         int n = nfound[was];
-        if (n > kCandidates) n = exact_candidates<T, B, 0>(x, a.vocab, a.k, lo, row.M, found, &nfound[was], counts, turn, tid);
-        place_candidates<B, 0, kCandidates>(found, n, tid, [&](unsigned long long c, int place) {
+        if (n > kCandidates) n = exact_candidates<T, B>(x, a.vocab, a.k, lo, row.M, found, &nfound[was], counts, turn, tid, 0);
+        place_candidates<B, kCandidates>(found, n, tid, 0, [&](unsigned long long c, int place) {
             if (place < a.k) put_entry(a, r, place, int(~uint32_t(c)), row.share(logit_of(uint32_t(c >> 32))));
         });
         for (int i = n + tid; i < a.k; i += B) put_entry(a, r, i, -1, kNegInf);
@@ -1219,8 +1253,7 @@ cudaError_t stats(const StatsArgs& a, int sms, GroupCache& cache, cudaStream_t s
         if (threads == 128) return stats_launch<T, 128, true>(a, clog, sms, cache, s);
         return stats_launch<T, 256, true>(a, clog, sms, cache, s);
     }
-    if (threads == 128) return top_launch<T, 128, 4, 4, 3>(a, sms, cache, s);
-    return top_launch<T, 256, 4, 4, 2>(a, sms, cache, s);
+    return top_launch<T, 256, 64, 2, 4, 4, 2>(a, sms, cache, s);
 }
 
 // ---------------------------------------------------------------------------
