@@ -276,74 +276,62 @@ __device__ __noinline__ int exact_candidates(const T* x, int vocab, int k, uint3
     return min(n, k);
 }
 
-// The n candidates in order, each thread E of them in registers: candidate (warp E + e) 32 + lane of the
-// sorted list is settled by that lane.  A bitonic network: neighbours up to 16 apart by shuffles, up to
-// 32 E / 2 apart in registers, further ones through shared memory.
-template <int SB, int E, typename F>
-__device__ __forceinline__ void sort_by(unsigned long long* found, int n, int tid, int bar, F settle) {
-    const int warp = tid >> 5, lane = tid & 31, base = warp * E * 32 + lane;
-    unsigned long long c[E];
+__device__ __forceinline__ int warp_before(int n, int& all) {   // the sum over the lanes below, and over all
+    int to = n;
 #pragma unroll
-    for (int e = 0; e < E; ++e) c[e] = base + 32 * e < n ? found[base + 32 * e] : 0;
-    auto keep = [](unsigned long long mine, unsigned long long other, bool larger) { return larger == (mine > other) ? mine : other; };
-    if (SB > 32) sync<SB>(bar);   // the list has been read
-#pragma unroll 1
-    for (int size = 2; size < 2 * n; size *= 2) {   // the largest candidates first where `size` is not in the index
-        if (SB > 32) {
-#pragma unroll 1
-            for (int d = size / 2; d >= 32 * E; d /= 2) {
-#pragma unroll
-                for (int e = 0; e < E; ++e) found[base + 32 * e] = c[e];
-                sync<SB>(bar);
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const int i = base + 32 * e;
-                    c[e] = keep(c[e], found[i ^ d], ((i & size) == 0) == ((i & d) == 0));
-                }
-                sync<SB>(bar);
-            }
-        }
-#pragma unroll
-        for (int de = E / 2; de > 0; de /= 2) {
-            if (32 * de < size) {
-#pragma unroll
-                for (int e = 0; e < E; ++e)
-                    if ((e & de) == 0) {
-                        const unsigned long long x = c[e], y = c[e + de];
-                        const bool first = (((base + 32 * e) & size) == 0) == (x > y);
-                        c[e] = first ? x : y;
-                        c[e + de] = first ? y : x;
-                    }
-            }
-        }
-#pragma unroll
-        for (int d = 16; d > 0; d /= 2) {
-            if (d < size) {
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const int i = base + 32 * e;
-                    c[e] = keep(c[e], __shfl_xor_sync(~0u, c[e], d), ((i & size) == 0) == ((lane & d) == 0));
-                }
-            }
-        }
+    for (int o = 1; o < 32; o <<= 1) {
+        const int below = __shfl_up_sync(~0u, to, o);
+        if ((threadIdx.x & 31) >= o) to += below;
     }
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        if (base + 32 * e < n) settle(c[e], base + 32 * e);
+    all = __shfl_sync(~0u, to, 31);
+    return to - n;
 }
-// CAP: the list's length, at most 16 per thread.  Short lists are one warp's work: no barrier.
-template <int SB, int CAP, typename F>
-__device__ __forceinline__ void place_candidates(unsigned long long* found, int n, int tid, int bar, F settle) {
-    if (n <= 128) {
-        if (tid >= 32) return;
-        if (n <= 32) return sort_by<32, 1>(found, n, tid, bar, settle);
-        if (n <= 64) return sort_by<32, 2>(found, n, tid, bar, settle);
-        return sort_by<32, 4>(found, n, tid, bar, settle);
+
+// The n candidates in order, from the largest: settle(candidate, place) by one thread each.  They are
+// dealt into 256 bins by rank, from M's down to lo's, the bins' starts are sums of counts, and within a bin
+// (equal logits, or fp32 ones close by) a candidate's place is the number of larger ones.  `order` holds n
+// numbers, `bins` 256.  (A bitonic network over 85 candidates took a warp 5,000 to 9,000 cycles beside
+// busy ones, every pair counted as much.)
+constexpr int kBins = 256;
+template <typename T, int SB, typename F>
+__device__ __forceinline__ void place_candidates(const unsigned long long* found, int n, uint32_t lo, float M, int k, int* bins,
+                                                 uint16_t* order, int tid, int bar, F settle) {
+    const uint32_t top = rank_of<T>(M), range = top - lo;
+    const int shift = range < kBins ? 0 : 32 - 8 - __clz(range);
+    auto bin_of = [&](unsigned long long c) { return (top - (uint32_t(c >> 32) >> Order<T>::kShift)) >> shift; };
+    for (int i = tid; i < kBins; i += SB) bins[i] = 0;
+    sync<SB>(bar);
+    for (int i = tid; i < n; i += SB) atomicAdd(&bins[bin_of(found[i])], 1);
+    sync<SB>(bar);
+    if (tid < 32) {
+        int4* const mine = reinterpret_cast<int4*>(bins) + 2 * tid;
+        int4 p = mine[0], q = mine[1];
+        int all;
+        int at = warp_before(p.x + p.y + p.z + p.w + q.x + q.y + q.z + q.w, all);
+        int next;
+        next = at + p.x; p.x = at; at = next;
+        next = at + p.y; p.y = at; at = next;
+        next = at + p.z; p.z = at; at = next;
+        next = at + p.w; p.w = at; at = next;
+        next = at + q.x; q.x = at; at = next;
+        next = at + q.y; q.y = at; at = next;
+        next = at + q.z; q.z = at; at = next;
+        q.w = at;
+        mine[0] = p;
+        mine[1] = q;
     }
-    if (n <= 4 * SB || CAP <= 4 * SB) return sort_by<SB, 4>(found, n, tid, bar, settle);
-    if constexpr (CAP > 4 * SB)
-        if (n <= 8 * SB || CAP <= 8 * SB) return sort_by<SB, 8>(found, n, tid, bar, settle);
-    if constexpr (CAP > 8 * SB) sort_by<SB, 16>(found, n, tid, bar, settle);
+    sync<SB>(bar);
+    for (int i = tid; i < n; i += SB) order[atomicAdd(&bins[bin_of(found[i])], 1)] = uint16_t(i);
+    sync<SB>(bar);   // now a bin's number is its end
+    for (int i = tid; i < n; i += SB) {
+        const unsigned long long c = found[i];
+        const uint32_t bin = bin_of(c);
+        int place = bin == 0 ? 0 : bins[bin - 1];
+        if (place >= k) continue;
+        const int end = bins[bin];
+        for (int j = place; j < end; ++j) place += found[order[j]] > c;
+        if (place < k) settle(c, place);
+    }
 }
 
 // Other CTAs' shared memory.
@@ -540,12 +528,12 @@ __device__ __forceinline__ int group_shift(int most, int groups) {
     return gs;
 }
 // The maxima of a thread's groups, from four vectors at a time: those from vector `at` on.
-template <typename T, int B>
-__device__ __forceinline__ float keep_maxima(float (*gm)[B], int gs, int at, const uint4 (&raw)[4], float& run, int tid) {
+template <typename T, int B, typename GT>
+__device__ __forceinline__ float keep_maxima(GT (*gm)[B], int gs, int at, const uint4 (&raw)[4], float& run, int tid) {
     if (gs >= 2) {
         const float t = top_of<T>(raw);
         run = (at & ((1 << gs) - 1)) == 0 ? t : fmaxf(run, t);
-        gm[at >> gs][tid] = run;
+        gm[at >> gs][tid] = from_f<GT>(run);
         return t;
     }
     float tops[4];
@@ -554,10 +542,10 @@ __device__ __forceinline__ float keep_maxima(float (*gm)[B], int gs, int at, con
     const float t01 = fmaxf(tops[0], tops[1]), t23 = fmaxf(tops[2], tops[3]);
     if (gs == 0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) gm[at + i][tid] = tops[i];
+        for (int i = 0; i < 4; ++i) gm[at + i][tid] = from_f<GT>(tops[i]);
     } else {
-        gm[at >> 1][tid] = t01;
-        gm[(at >> 1) + 1][tid] = t23;
+        gm[at >> 1][tid] = from_f<GT>(t01);
+        gm[(at >> 1) + 1][tid] = from_f<GT>(t23);
     }
     return fmaxf(t01, t23);
 }
@@ -572,8 +560,8 @@ __device__ __forceinline__ float lg2(float v) {
 template <typename T, typename F>
 __device__ __forceinline__ uint32_t search_rank(uint32_t lo, int sets, float M, int k, F count) {
     constexpr int SH = Order<T>::kShift;
-    const int enough = k + k / 8 + 4;
-    const float aim = lg2(float(k) + 0.06f * float(k) + 1.0f);
+    const int enough = k + k / 4 + 4;
+    const float aim = lg2(1.1f * float(k) + 1.0f);
     uint32_t hi = rank_of<T>(M) + 1;
     float from = logit_of(lo << SH), to = M, lfrom = lg2(float(sets)), lto = 0.0f;   // the ends, and log2 of their counts
     for (int step = 0; hi - lo > 1; step = step == 2 ? 0 : step + 1) {
@@ -630,16 +618,6 @@ struct Stage {
     uint4* raw;
     int *id, *count;   // of a vector's first element
 };
-__device__ __forceinline__ int warp_before(int n, int& all) {   // the sum over the lanes below, and over all
-    int to = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int below = __shfl_up_sync(~0u, to, o);
-        if ((threadIdx.x & 31) >= o) to += below;
-    }
-    all = __shfl_sync(~0u, to, 31);
-    return to - n;
-}
 // Places for the n of each lane of a warp, behind those that *count has already.
 __device__ __forceinline__ int warp_places(int n, int* count) {
     int all;
@@ -687,13 +665,16 @@ __device__ __forceinline__ void offer_staged(const Stage& st, int m, float least
 // A CTA per row: warps that read rows, and warps that choose entries
 // ---------------------------------------------------------------------------
 
-constexpr int kSlots = 8;     // groups of vectors per thread
 constexpr int kList = 1024;   // groups that are read again; more: the exact search
 
-template <int B, int NT, int TV, int ST> struct TopShared {   // dynamic shared memory of a CTA
+// Dynamic shared memory of a CTA.  The maxima of groups are kept in the logits' own type: 16 groups of a
+// thread's vectors, or 8 of fp32 ones, and the largest of all.
+template <typename T, int B, int NT, int TV, int ST> struct TopShared {
+    static constexpr int G = sizeof(T) == 2 ? 16 : 8;
     uint4 ring[ST][TV * B];
     unsigned long long found[NT][kCandidates];
-    float gmax[NT + 1][kSlots + 1][B];   // per row: of a thread's groups, of all its vectors
+    T gmax[NT + 1][G + 1][B];   // per row
+    int bins[NT][kBins];
     uint16_t list[NT][kList];
 };
 
@@ -703,12 +684,13 @@ template <int B, int NT, int TV, int ST> struct TopShared {   // dynamic shared 
 // then one per team.
 template <typename T, int B, int SB, int NT, int TV, int ST, int PER_SM>
 __global__ void __launch_bounds__(B + NT * SB, PER_SM) k_top(const StatsArgs a) {
-    constexpr int N = Vec<T>::N, nw = B / 32, G = kSlots, NB = NT + 1, HELD = B / SB, KEYS = HELD * 4;
+    using Shared = TopShared<T, B, NT, TV, ST>;
+    constexpr int N = Vec<T>::N, nw = B / 32, G = Shared::G, NB = NT + 1, HELD = B / SB, KEYS = HELD * 4, LOADS = 8;
     static_assert(nw <= 16 && 2 * NB + NT < 16, "parts of a row for half a warp, 16 named barriers");
     __shared__ float4 wparts[NB][nw];
     __shared__ int counts[NT][2][8], nfound[NT], nlist[NT], nstage[NT];
     extern __shared__ __align__(128) uint4 ring[];
-    TopShared<B, NT, TV, ST>& sh = *reinterpret_cast<TopShared<B, NT, TV, ST>*>(ring);
+    Shared& sh = *reinterpret_cast<Shared*>(ring);
     const int lane = threadIdx.x & 31;
     const float c2 = a.c2;
     const int group = blockIdx.x, ngroups = gridDim.x;
@@ -735,9 +717,9 @@ __global__ void __launch_bounds__(B + NT * SB, PER_SM) k_top(const StatsArgs a) 
             const int places = pl.hi > pl.lo ? pl.hi - pl.lo + pl.off : 0;
             const int gs = group_shift((places + TV * B - 1) / (TV * B) * TV, G);
             if (done == NB) bar_sync(1 + NB + buffer, B + SB); else ++done;
-            float(*const gm)[B] = sh.gmax[buffer];
+            T(*const gm)[B] = sh.gmax[buffer];
 #pragma unroll
-            for (int g = 0; g < G; ++g) gm[g][tid] = kNegInf;
+            for (int g = 0; g < G; ++g) gm[g][tid] = from_f<T>(kNegInf);
             Running<T> sum;
             float top = kNegInf, run = kNegInf;
             for (int base = 0; base * B < places; base += TV) {
@@ -748,13 +730,13 @@ __global__ void __launch_bounds__(B + NT * SB, PER_SM) k_top(const StatsArgs a) 
                     if (B * g >= mine) break;
                     uint4 raw[4];
                     load_four<T, B>(buf, g, mine, raw);
-                    const float t = keep_maxima<T, B>(gm, gs, base + g, raw, run, tid);
+                    const float t = keep_maxima<T, B, T>(gm, gs, base + g, raw, run, tid);
                     top = fmaxf(top, t);
                     sum.raise(t, c2);
                     sum.add(raw, B * (g + 3) < mine, c2c2, c2);
                 }
             }
-            gm[G][tid] = top;
+            gm[G][tid] = from_f<T>(top);
             const float4 part = warp_part(sum, top, xe, edge, c2);
             if (lane == 0) wparts[buffer][warp] = part;
             bar_arrive(1 + buffer, B + SB);
@@ -789,7 +771,7 @@ __global__ void __launch_bounds__(B + NT * SB, PER_SM) k_top(const StatsArgs a) 
         const float xy = warp == 0 && a.logp && y < a.vocab ? to_f(x[y]) : 0.0f;
         const int places = pl.hi > pl.lo ? pl.hi - pl.lo + pl.off : 0;
         const int gs = group_shift((places + TV * B - 1) / (TV * B) * TV, G);
-        const float(*const gm)[B] = sh.gmax[buffer];
+        const T(*const gm)[B] = sh.gmax[buffer];
         if (tid == 0) nfound[team] = nlist[team] = 0;
         bar_sync(1 + buffer, B + SB);
         const RowSums sums = join_parts<nw>(lane < nw ? wparts[buffer][lane] : make_float4(kNegInf, 0.0f, 0.0f, INFINITY), c2);
@@ -808,15 +790,15 @@ __global__ void __launch_bounds__(B + NT * SB, PER_SM) k_top(const StatsArgs a) 
         for (int i = 0; i < KEYS; ++i) key[i] = kNegInf;
         if (ss == 0) {
 #pragma unroll
-            for (int i = 0; i < HELD; ++i) key[i] = gm[G][tid + i * SB];
+            for (int i = 0; i < HELD; ++i) key[i] = to_f(gm[G][tid + i * SB]);
         } else {
 #pragma unroll
             for (int i = 0; i < HELD; ++i)
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
-                    const float v = gm[g][tid + i * SB];
-                    if (ss == 1) key[4 * i + g / 4] = fmaxf(key[4 * i + g / 4], v);
-                    else key[4 * i + g / 2] = fmaxf(key[4 * i + g / 2], v);
+                    const float v = to_f(gm[g][tid + i * SB]);
+                    const int half = 4 * i + g / (G / 2), quarter = 4 * i + g / (G / 4);
+                    if (ss == 1) key[half] = fmaxf(key[half], v); else key[quarter] = fmaxf(key[quarter], v);
                 }
         }
         auto count = [&](float v) {
@@ -840,10 +822,10 @@ __global__ void __launch_bounds__(B + NT * SB, PER_SM) k_top(const StatsArgs a) 
 #pragma unroll
         for (int h = 0; h < HELD; ++h) {
             const int t = tid + h * SB;
-            if (!(gm[G][t] >= least)) continue;
+            if (!(to_f(gm[G][t]) >= least)) continue;
             unsigned some = 0;
 #pragma unroll
-            for (int g = 0; g < G; ++g) some |= gm[g][t] >= least ? 1u << g : 0u;
+            for (int g = 0; g < G; ++g) some |= to_f(gm[g][t]) >= least ? 1u << g : 0u;
             int i = atomicAdd(&nlist[team], __popc(some));
             for (; some != 0 && i < kList; some &= some - 1) list[i++] = uint16_t((__ffs(some) - 1) * B + t);
         }
@@ -854,36 +836,43 @@ __global__ void __launch_bounds__(B + NT * SB, PER_SM) k_top(const StatsArgs a) 
         static_assert(80 * SB <= int(sizeof(sh.gmax[0])), "a round's vectors take the place of a row's maxima");
         uint4* const staged = reinterpret_cast<uint4*>(sh.gmax[buffer]);
         const Stage stage{staged, reinterpret_cast<int*>(staged + 4 * SB), &nstage[team]};
-        for (int base = 0; base < items; base += 4 * SB) {
-            if (tid == 0) nstage[team] = 0;
-            uint4 raw[4];
-            int at[4];
-            unsigned pass = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
+        for (int base = 0; base < items; base += LOADS * SB) {
+            uint4 raw[LOADS];
+            auto place_at = [&](int i) {   // the id of a vector's first element, below 0 for none
                 const int item = base + tid + SB * i;
-                at[i] = -1;
-                if (item < items) {
-                    const int e = list[item >> gs], t = e & (B - 1);
-                    const int place = t + B * (((e / B) << gs) + (item & ((1 << gs) - 1)));
-                    if (place >= pl.off && place < places) at[i] = pl.head + (pl.lo + place - pl.off) * N;
-                }
-                if (at[i] >= 0) raw[i] = ld16(x + at[i]);
+                if (item >= items) return -1;
+                const int e = list[item >> gs], t = e & (B - 1);
+                const int place = t + B * (((e / B) << gs) + (item & ((1 << gs) - 1)));
+                return place >= pl.off && place < places ? pl.head + (pl.lo + place - pl.off) * N : -1;
+            };
+            unsigned there = 0;
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) {
+                const int at = place_at(i);
+                there |= at >= 0 ? 1u << i : 0u;
+                if (at >= 0) raw[i] = ld16(x + at);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) pass |= at[i] >= 0 && Vec<T>::top(raw[i]) >= least ? 1u << i : 0u;
-            sync<SB>(bar);
-            stage_vectors<4>(raw, pass, [&](int i) { return at[i]; }, stage);
-            sync<SB>(bar);
-            offer_staged<T, SB, kCandidates>(stage, nstage[team], least, found, &nfound[team], tid);
-            sync<SB>(bar);
+            for (int h = 0; h < LOADS; h += 4) {
+                if (base + SB * h >= items) break;
+                if (tid == 0) nstage[team] = 0;
+                const uint4 four[4] = {raw[h], raw[h + 1], raw[h + 2], raw[h + 3]};
+                unsigned pass = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) pass |= (there >> (h + i) & 1) && Vec<T>::top(four[i]) >= least ? 1u << i : 0u;
+                sync<SB>(bar);
+                stage_vectors<4>(four, pass, [&](int i) { return place_at(h + i); }, stage);
+                sync<SB>(bar);
+                offer_staged<T, SB, kCandidates>(stage, nstage[team], least, found, &nfound[team], tid);
+                sync<SB>(bar);
+            }
         }
         bar_arrive(1 + NB + buffer, B + SB);   // the maxima have been used
         int n = nfound[team];
         if (n > kCandidates || groups > kList)
             n = exact_candidates<T, SB>(x, a.vocab, a.k, lo, row.M, found, &nfound[team], counts[team], turn, tid, bar);
-        place_candidates<SB, kCandidates>(found, n, tid, bar, [&](unsigned long long c, int place) {
-            if (place < a.k) put_entry(a, r, place, int(~uint32_t(c)), row.share(logit_of(uint32_t(c >> 32))));
+        place_candidates<T, SB>(found, n, lo, row.M, a.k, sh.bins[team], list, tid, bar, [&](unsigned long long c, int place) {
+            put_entry(a, r, place, int(~uint32_t(c)), row.share(logit_of(uint32_t(c >> 32))));
         });
         for (int i = n + tid; i < a.k; i += SB) put_entry(a, r, i, -1, kNegInf);
         sync<SB>(bar);   // before the next row's candidates
@@ -896,7 +885,7 @@ cudaError_t top_launch(const StatsArgs& a, int sms, GroupCache& cache, cudaStrea
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(1);
     cfg.blockDim = dim3(B + NT * SB);
-    cfg.dynamicSmemBytes = sizeof(TopShared<B, NT, TV, ST>);
+    cfg.dynamicSmemBytes = sizeof(TopShared<T, B, NT, TV, ST>);
     cfg.stream = s;
     int groups = 0;
     cudaError_t e = resident_groups(reinterpret_cast<const void*>(kernel), cfg, RowShape{B + NT * SB, 0}, sms, cache, groups);
@@ -917,6 +906,7 @@ __global__ void __launch_bounds__(128, NV > 8 ? 3 : NV > 4 ? 4 : 6) k_held(const
     __shared__ float4 wparts[W == 1 ? 1 : 2][4];
     __shared__ float2 wtops[W == 1 ? 1 : 2][4];
     __shared__ int counts[2][8], nfound[TEAMS], nstage[TEAMS];
+    __shared__ __align__(16) int bins[TOP ? TEAMS : 1][kBins];
     extern __shared__ __align__(128) uint4 ring[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, team = warp / W, tid = threadIdx.x % SB;
     // per team: the staged vectors and their ids, and the candidates
@@ -971,7 +961,7 @@ __global__ void __launch_bounds__(128, NV > 8 ? 3 : NV > 4 ? 4 : 6) k_held(const
 #pragma unroll
         for (int i = 0; i < NV; i += 4) {
             const uint4 four[4] = {raw[i], raw[i + 1], raw[i + 2], raw[i + 3]};
-            sum.add(four, (i + 3) * SB + tid - pl.off < pl.body && (i > 0 || tid >= pl.off), c2c2, c2);
+            sum.add(four, false, c2c2, c2);
         }
         if (edge) sum.add_one(xe, c2);
         RowSums sums{M, warp_sum(sum.s), warp_sum(sum.w), kNegInf};
@@ -1028,8 +1018,8 @@ __global__ void __launch_bounds__(128, NV > 8 ? 3 : NV > 4 ? 4 : 6) k_held(const
         sync<SB>(1);
         int n = nfound[team];
         if (n > CAP) n = exact_candidates<T, SB>(x, a.vocab, a.k, lo, M, found, &nfound[team], counts, turn, tid, 1);
-        place_candidates<SB, CAP>(found, n, tid, 1, [&](unsigned long long c, int place) {
-            if (place < a.k) put_entry(a, r, place, int(~uint32_t(c)), row.share(logit_of(uint32_t(c >> 32))));
+        place_candidates<T, SB>(found, n, lo, M, a.k, bins[team], reinterpret_cast<uint16_t*>(stage.raw), tid, 1, [&](unsigned long long c, int place) {
+            put_entry(a, r, place, int(~uint32_t(c)), row.share(logit_of(uint32_t(c >> 32))));
         });
         for (int i = n + tid; i < a.k; i += SB) put_entry(a, r, i, -1, kNegInf);
         sync<SB>(1);   // before the next row's candidates
@@ -1073,6 +1063,7 @@ __global__ void __launch_bounds__(B, (TOP ? 256 : 512) / B) k_stats(const StatsA
     constexpr int TV = 8, ST = 3, nw = B / 32, G = kGroups;
     __shared__ float4 wparts[2][8], cparts[2][kMaxCluster];   // by row parity: of the warps, of the CTAs
     __shared__ int counts[2][8], nfound[2], nlist[2];
+    __shared__ __align__(16) int bins[TOP ? kBins : 4];
     extern __shared__ __align__(128) uint4 ring[];   // [ST][TV * B]
     unsigned long long* const found = reinterpret_cast<unsigned long long*>(ring + ST * TV * B);   // [kCandidates]
     float(*const gmax)[B] = reinterpret_cast<float(*)[B]>(found + kCandidates);                     // [G][B]
@@ -1120,7 +1111,7 @@ __global__ void __launch_bounds__(B, (TOP ? 256 : 512) / B) k_stats(const StatsA
                 if (B * g >= mine) break;
                 uint4 raw[4];
                 load_four<T, B>(buf, g, mine, raw);
-                const float t = TOP ? keep_maxima<T, B>(gmax + rank * own, gs, base + g, raw, run, tid) : top_of<T>(raw);
+                const float t = TOP ? keep_maxima<T, B, float>(gmax + rank * own, gs, base + g, raw, run, tid) : top_of<T>(raw);
                 top = fmaxf(top, t);
                 sum.raise(t, c2);
                 sum.add(raw, B * (g + 3) < mine, c2c2, c2);
@@ -1207,8 +1198,8 @@ __global__ void __launch_bounds__(B, (TOP ? 256 : 512) / B) k_stats(const StatsA
         if (rank != 0) continue;
         int n = nfound[was];
         if (n > kCandidates) n = exact_candidates<T, B>(x, a.vocab, a.k, lo, row.M, found, &nfound[was], counts, turn, tid, 0);
-        place_candidates<B, kCandidates>(found, n, tid, 0, [&](unsigned long long c, int place) {
-            if (place < a.k) put_entry(a, r, place, int(~uint32_t(c)), row.share(logit_of(uint32_t(c >> 32))));
+        place_candidates<T, B>(found, n, lo, row.M, a.k, bins, list, tid, 0, [&](unsigned long long c, int place) {
+            put_entry(a, r, place, int(~uint32_t(c)), row.share(logit_of(uint32_t(c >> 32))));
         });
         for (int i = n + tid; i < a.k; i += B) put_entry(a, r, i, -1, kNegInf);
     }
@@ -1253,7 +1244,7 @@ cudaError_t stats(const StatsArgs& a, int sms, GroupCache& cache, cudaStream_t s
         if (threads == 128) return stats_launch<T, 128, true>(a, clog, sms, cache, s);
         return stats_launch<T, 256, true>(a, clog, sms, cache, s);
     }
-    return top_launch<T, 256, 64, 2, 4, 4, 2>(a, sms, cache, s);
+    return top_launch<T, 256, 64, 2, 4, 3, 2>(a, sms, cache, s);
 }
 
 // ---------------------------------------------------------------------------
