@@ -24,9 +24,9 @@
  *
  * Memory.  The caller owns every tensor.  Rows are contiguous, row t starting at
  * element t * ld; any ld >= cols and any element-aligned address is accepted.
- * Where rows begin on 16-byte boundaries and hold whole blocks of 8 elements, or
- * follow one another without gaps from such a boundary on, accesses are vectors;
- * others are by elements.  y may be x's or the residual's own memory (same address
+ * Where rows begin on 16-byte boundaries (fp32: 32-byte ones) and hold whole blocks
+ * of 8 elements, or follow one another without gaps from such a boundary on,
+ * accesses are vectors; others are by elements.  y may be x's or the residual's own memory (same address
  * and ld).  Any other overlap of y with an argument is an error.
  *
  * The call is asynchronous on the given stream, keeps no state and no scratch, and

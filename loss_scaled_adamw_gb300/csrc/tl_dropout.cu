@@ -64,49 +64,72 @@ __device__ __forceinline__ float dropped(float x, bool keep, float scale, float 
     return keep ? __fmaf_rn(x, scale, residual) : residual;
 }
 
-// Whole blocks of eight elements in 16-byte vectors.  `chunks` blocks to a row; rows without gaps are
-// one row.
-template <typename T, bool RES, int NB, int TB>
+// Threads per CTA, and blocks of eight elements under way per thread.  us for 268M bf16 elements without a
+// residual with 1 / 2 / 4 / 8 blocks and 256 threads: 203 / 181 / 173 / 169, with 4 and 128 threads 170; with a
+// residual 225 for all of 1 to 4; 8.4M elements with a residual 7.9 / 7.4 / 7.7 with 1 / 2 / 4, 7.3 with 2 and
+// 128 threads, without one 7.3 / 7.2 / 8.0 with 2 / 4 / 8, 7.1 with 4 and 128.
+constexpr int kDropThreads = 128;
+template <bool RES> constexpr int kBlocks = RES ? 2 : 4;
+
+// Eight consecutive elements: one access of 16 bytes, or of 32 (fp32).
+template <typename T> struct Eight {
+    uint4 v;
+    __device__ __forceinline__ void load(const T* p) { v = ld16(p); }
+    __device__ __forceinline__ void wide(float (&f)[8]) const { Vec<T>::wide(v, f); }
+    static __device__ __forceinline__ void store(T* p, const float (&f)[8]) { st16(p, Vec<T>::narrow(f)); }
+};
+template <> struct Eight<float> {
+    float f[8];
+    __device__ __forceinline__ void load(const float* p) {
+        asm volatile("ld.global.L1::no_allocate.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7]) : "l"(p) : "memory");
+    }
+    __device__ __forceinline__ void wide(float (&g)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] = f[i];
+    }
+    static __device__ __forceinline__ void store(float* p, const float (&f)[8]) {
+        asm volatile("st.global.L1::no_allocate.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                     ::"l"(p), "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]) : "memory");
+    }
+};
+
+// Whole blocks, one to a thread and access, NB of them under way per thread.  FLAT: rows without gaps are
+// one row; else a row has `chunks` blocks.
+template <typename T, bool RES, bool FLAT, int NB, int TB>
 __global__ void __launch_bounds__(TB) k_dropout(const DropoutArgs a, const int64_t blocks, const int64_t chunks) {
-    constexpr int N = Vec<T>::N, VB = 8 / N;   // vectors to a block
-    const Philox draw(a);
-    uint4 x[NB][VB], res[RES ? NB : 1][VB];
-    int64_t row[NB], col[NB];
+    Eight<T> x[NB], res[RES ? NB : 1];
+    int64_t at[NB] = {};   // the row
     const int64_t first = int64_t(blockIdx.x) * (NB * TB) + threadIdx.x;
+    const Philox draw(a);
+    auto element = [&](int i, int64_t ld) {
+        const int64_t b = first + i * TB;
+        return FLAT ? b * 8 : at[i] * ld + (b - at[i] * chunks) * 8;
+    };
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
         const int64_t b = first + i * TB;
-        row[i] = a.rows == 1 ? 0 : b / chunks;
-        col[i] = (b - row[i] * chunks) * 8;
+        if (!FLAT) at[i] = (b >> 32) == 0 && (chunks >> 32) == 0 ? int64_t(uint32_t(b) / uint32_t(chunks)) : b / chunks;
         if (b < blocks) {
-#pragma unroll
-            for (int v = 0; v < VB; ++v) {
-                x[i][v] = ld16(static_cast<const T*>(a.x) + row[i] * a.ldx + col[i] + v * N);
-                if (RES) res[i][v] = ld16(static_cast<const T*>(a.residual) + row[i] * a.ldr + col[i] + v * N);
-            }
+            x[i].load(static_cast<const T*>(a.x) + element(i, a.ldx));
+            if (RES) res[i].load(static_cast<const T*>(a.residual) + element(i, a.ldr));
         }
     }
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
         const int64_t b = first + i * TB;
-        if (b >= blocks) continue;
+        if (b >= blocks) break;
         const uint4 bits = a.random ? draw(uint64_t(b)) : make_uint4(0, 0, 0, 0);
+        float f[8], g[8];
+        x[i].wide(f);
+        if (RES) res[i].wide(g);
 #pragma unroll
-        for (int v = 0; v < VB; ++v) {
-            float f[N], g[N];
-            Vec<T>::wide(x[i][v], f);
-            if (RES) Vec<T>::wide(res[i][v], g);
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const int e = v * N + j;
-                f[j] = dropped(f[j], kept(word_of(bits, e >> 1), e, a.limit), a.scale, RES ? g[j] : 0.0f);
-            }
-            st16(static_cast<T*>(a.y) + row[i] * a.ldy + col[i] + v * N, Vec<T>::narrow(f));
-        }
+        for (int j = 0; j < 8; ++j) f[j] = dropped(f[j], kept(word_of(bits, j >> 1), j, a.limit), a.scale, RES ? g[j] : 0.0f);
+        Eight<T>::store(static_cast<T*>(a.y) + element(i, a.ldy), f);
     }
     // the elements behind the last whole block (of the one row)
     const int64_t n = blocks * 8 + threadIdx.x;
-    if (blockIdx.x == 0 && a.rows == 1 && n < a.cols) {
+    if (FLAT && blockIdx.x == 0 && n < a.cols) {
         const uint4 bits = a.random ? draw(uint64_t(blocks)) : make_uint4(0, 0, 0, 0);
         const float r = RES ? to_f(static_cast<const T*>(a.residual)[n]) : 0.0f;
         const bool keep = kept(word_of(bits, int(threadIdx.x) >> 1), int(threadIdx.x), a.limit);
@@ -123,35 +146,56 @@ __global__ void __launch_bounds__(TB) k_dropout_any(const DropoutArgs a, const i
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t first = (int64_t(blockIdx.x) * (TB / 32) + warp) * 256;
     if (first >= numel) return;
+    T x[8], res[RES ? 8 : 1];
+    int64_t to[8];   // the element's place in y
+    int64_t row = a.rows == 1 ? 0 : (first + lane) / a.cols, col = first + lane - row * a.cols;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (first + 32 * i + lane < numel) {
+            x[i] = static_cast<const T*>(a.x)[row * a.ldx + col];
+            if (RES) res[i] = static_cast<const T*>(a.residual)[row * a.ldr + col];
+        }
+        to[i] = row * a.ldy + col;
+        col += 32;
+        if (a.cols >= 32) {
+            if (col >= a.cols) {
+                col -= a.cols;
+                ++row;
+            }
+        } else {
+            const int steps = int(col) / int(a.cols);
+            row += steps;
+            col -= steps * a.cols;
+        }
+    }
     bits[threadIdx.x] = a.random ? draw(uint64_t(first >> 3) + lane) : make_uint4(0, 0, 0, 0);
     __syncwarp();
     const uint32_t* const words = reinterpret_cast<const uint32_t*>(bits + warp * 32);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const int64_t e = first + 32 * i + lane;
-        if (e >= numel) break;
-        const int64_t row = a.rows == 1 ? 0 : e / a.cols, col = e - row * a.cols;
-        const float x = to_f(static_cast<const T*>(a.x)[row * a.ldx + col]);
-        const float r = RES ? to_f(static_cast<const T*>(a.residual)[row * a.ldr + col]) : 0.0f;
+        if (first + 32 * i + lane >= numel) break;
         const bool keep = kept(words[(32 * i + lane) >> 1], lane, a.limit);
-        static_cast<T*>(a.y)[row * a.ldy + col] = from_f<T>(dropped(x, keep, a.scale, r));
+        static_cast<T*>(a.y)[to[i]] = from_f<T>(dropped(to_f(x[i]), keep, a.scale, RES ? to_f(res[i]) : 0.0f));
     }
 }
 
 template <typename T, bool RES>
 cudaError_t launch(DropoutArgs a, cudaStream_t s) {
-    constexpr int NB = Vec<T>::N / (RES ? 2 : 1), TB = 256;
+    constexpr int NB = kBlocks<RES>, TB = kDropThreads;
     const int64_t numel = a.rows * a.cols;
     if (a.rows > 1 && a.ldx == a.cols && a.ldy == a.cols && (!RES || a.ldr == a.cols)) {   // no gaps
         a.rows = 1;
         a.cols = a.ldx = a.ldr = a.ldy = numel;
     }
-    bool whole = aligned(a.x, 16) && aligned(a.y, 16) && (!RES || aligned(a.residual, 16));
+    constexpr uintptr_t unit = 8 * sizeof(T);
+    bool whole = aligned(a.x, unit) && aligned(a.y, unit) && (!RES || aligned(a.residual, unit));
     if (a.rows > 1) whole = whole && a.cols % 8 == 0 && a.ldx % 8 == 0 && a.ldy % 8 == 0 && (!RES || a.ldr % 8 == 0);
     const int64_t per = whole ? int64_t(NB) * TB * 8 : int64_t(TB) * 8, ctas = (numel + per - 1) / per;
     if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
-    if (whole)
-        k_dropout<T, RES, NB, TB><<<unsigned(ctas), TB, 0, s>>>(a, numel / 8, a.cols / 8);
+    if (whole && a.rows == 1)
+        k_dropout<T, RES, true, NB, TB><<<unsigned(ctas), TB, 0, s>>>(a, numel / 8, 0);
+    else if (whole)
+        k_dropout<T, RES, false, NB, TB><<<unsigned(ctas), TB, 0, s>>>(a, numel / 8, a.cols / 8);
     else
         k_dropout_any<T, RES, TB><<<unsigned(ctas), TB, 0, s>>>(a, numel);
     return cudaGetLastError();

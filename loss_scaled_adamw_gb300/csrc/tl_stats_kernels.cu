@@ -667,10 +667,10 @@ __device__ __forceinline__ void offer_staged(const Stage& st, int m, float least
 
 constexpr int kList = 1024;   // groups that are read again; more: the exact search
 
-// Dynamic shared memory of a CTA.  The maxima of groups are kept in the logits' own type: 16 groups of a
-// thread's vectors, or 8 of fp32 ones, and the largest of all.
+// Dynamic shared memory of a CTA.  The maxima of a thread's 16 groups of vectors, and the largest of all,
+// are kept in the logits' own type.
 template <typename T, int B, int NT, int TV, int ST> struct TopShared {
-    static constexpr int G = sizeof(T) == 2 ? 16 : 8;
+    static constexpr int G = 16;
     uint4 ring[ST][TV * B];
     unsigned long long found[NT][kCandidates];
     T gmax[NT + 1][G + 1][B];   // per row
@@ -1244,7 +1244,8 @@ cudaError_t stats(const StatsArgs& a, int sms, GroupCache& cache, cudaStream_t s
         if (threads == 128) return stats_launch<T, 128, true>(a, clog, sms, cache, s);
         return stats_launch<T, 256, true>(a, clog, sms, cache, s);
     }
-    return top_launch<T, 256, 64, 2, 4, 3, 2>(a, sms, cache, s);
+    if constexpr (sizeof(T) == 4) return top_launch<T, 256, 64, 1, 4, 4, 2>(a, sms, cache, s);
+    else return top_launch<T, 256, 64, 2, 4, 3, 2>(a, sms, cache, s);
 }
 
 // ---------------------------------------------------------------------------

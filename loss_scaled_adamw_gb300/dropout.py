@@ -16,6 +16,8 @@ from __future__ import annotations
 
 import ctypes
 
+import torch
+
 from . import TL_OK, TLError, losses
 
 DROPOUT_EXPORTED = ("tl_dropout",)
@@ -35,11 +37,14 @@ def tl_dropout(x, y, p: float, key, site: int = 0, residual=None, stream=None) -
     x, y and residual: float32, bfloat16 or float16 CUDA tensors of one shape and dtype,
     contiguous, or 2-D with contiguous rows.  y may be x or the residual itself.  The
     gradient of x is the same call on the gradient of y, without a residual."""
-    lib = losses._load()
-    if not getattr(x, "is_cuda", False):
+    bind = losses._bind
+    if bind is None:
+        losses._load()
+        bind = losses._bind
+    device = x.get_device() if isinstance(x, torch.Tensor) else -1
+    if device < 0:
         raise ValueError("x must be a CUDA tensor")
-    device = x.device.index
     handle = losses._raw_stream(device) if stream is None else losses._any_stream(stream).value
-    rc = losses._bind.dropout(x, y, residual, key, site, p, handle, device)
+    rc = bind.dropout(x, y, residual, key, site, p, handle, device)
     if rc != TL_OK:
-        raise TLError("tl_dropout", rc, lib.tl_status_string(rc).decode())
+        raise TLError("tl_dropout", rc, losses._load().tl_status_string(rc).decode())
