@@ -67,8 +67,12 @@ int check_logits(tl_loss_ctx* ctx, const tl_logits* x) {
     return TL_OK;
 }
 
-// log2(e) / temperature: a rounding of it is common to a row's exponents, and shows in its entropy.
+// log2(e) / temperature, and what its rounding to fp32 leaves out: a rounding that is common to a row's
+// exponents shows in its entropy.
 float exponent_scale(float temperature) { return float(1.4426950408889634 / double(temperature)); }
+float exponent_rest(float temperature) {
+    return float(1.4426950408889634 / double(temperature) - double(exponent_scale(temperature)));
+}
 
 // Fills the parts of the launch arguments that every call shares.
 void base_args(tl_loss_ctx* ctx, const tl_logits* x, const int64_t* target, LossArgs& a, Spans& sp) {
@@ -360,6 +364,7 @@ int tl_token_stats(tl_loss_ctx* ctx, const tl_logits* logits, const tl_token_sta
     a.vocab = int32_t(logits->vocab);
     a.it = 1.0f / logits->temperature;
     a.c2 = exponent_scale(logits->temperature);
+    a.c2_low = exponent_rest(logits->temperature);
     a.target = args->target;
     a.logp = args->logp;
     a.entropy = args->entropy;

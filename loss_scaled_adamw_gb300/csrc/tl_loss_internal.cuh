@@ -77,7 +77,8 @@ struct StatsArgs {
     int64_t ld;
     int64_t rows;
     int32_t vocab;
-    float it, c2;          // 1 / temperature, and times log2 e (rounded once)
+    float it;              // 1 / temperature
+    float c2, c2_low;      // log2 e / temperature, and what its rounding left out
     const int64_t* target; // null: every row is valid, no logp
     float* logp;
     float* entropy;
@@ -95,7 +96,7 @@ struct TokenGradArgs {
     int64_t ld;
     int64_t rows;
     int32_t vocab;
-    float it, c2;
+    float it, c2;          // as above
     const int64_t* target;
     const float* saved;
     const float* grad_logp;

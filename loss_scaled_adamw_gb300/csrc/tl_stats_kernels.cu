@@ -62,10 +62,31 @@ __device__ __forceinline__ float max_nan(float v, float least) {
     return r;
 }
 
+// log2(e) / temperature, and what its rounding left out: with fp32 logits it is counted too, where an entropy
+// shows it (temperature 0.7: off by 1.7e-7 of itself without, 6e-8 with it); 16-bit ones have no time for it.
+struct Scale {
+    float c2, low;
+    __device__ __forceinline__ Scale(const StatsArgs& a) : c2(a.c2), low(a.c2_low) {}
+};
+
+// 2^z for |z| <= 1/2 or a little above: the series of e^(z ln 2), whose ninth term is below 2^-27.
+__device__ __forceinline__ float power_near_1(float z) {
+    const float t = z * kLn2;
+    float p = 1.0f / 5040.0f;
+    p = __fmaf_rn(p, t, 1.0f / 720.0f);
+    p = __fmaf_rn(p, t, 1.0f / 120.0f);
+    p = __fmaf_rn(p, t, 1.0f / 24.0f);
+    p = __fmaf_rn(p, t, 1.0f / 6.0f);
+    p = __fmaf_rn(p, t, 0.5f);
+    p = __fmaf_rn(p, t, 1.0f);
+    return __fmaf_rn(p, t, 1.0f);
+}
+
 // A thread's sums over the elements that it has seen, against a reference near its largest one.
 template <typename T> struct Running {
     static constexpr int N = Vec<T>::N, U = 4;
     float m = kNegInf, limit = kNegInf, s = 0.0f, w = 0.0f;
+    float s_left = 0.0f, w_left = 0.0f;   // fp32 logits: what the sums' additions left out; 16-bit ones have no time for it
     float u = 0.0f;      // the reference's whole number
     bool slow = false;   // element by element, see below
 
@@ -77,29 +98,39 @@ template <typename T> struct Running {
     // To a much larger element.  Smaller steps are left: exponentials up to 2^32 of the reference do no harm.
     __device__ __forceinline__ void raise(float top, float c2) {
         if (!(top > limit)) return;
+        fold();
         move_sums(m, top, c2, s, w);
         m = top;
         limit = m + 32.0f / c2;
         slow = big(m, c2) || (sizeof(T) == 2 && !((m - kFloor) * c2 > 150.0f));
         u = slow ? 0.0f : anchor(m, c2);
     }
-    __device__ __forceinline__ void add_one(float v, float c2) {
+    __device__ __forceinline__ void add_one(float v, const Scale& c) {
         const float ref = part_ref(m);
-        const float z = max_nan(big(ref, c2) ? (v - ref) * c2 : __fmaf_rn(v, c2, -anchor(ref, c2)), kLowest), e = ex2(z);
+        const bool far = big(ref, c.c2);
+        float z = far ? (v - ref) * c.c2 : __fmaf_rn(v, c.c2, -anchor(ref, c.c2));
+        if (sizeof(T) == 4 && v > kNegInf) z = __fmaf_rn(far ? v - ref : v, c.low, z);
+        z = max_nan(z, kLowest);
+        const float e = ex2(z);
         s += e;
         w = __fmaf_rn(e, z, w);
     }
     // The sums of U vectors; HOLD: with elements held above kFloor.
-    template <bool HOLD> __device__ __forceinline__ void sums_of(const uint4 (&raw)[U], pair_t c2c2, float& s_, float& w_) const {
-        const pair_t uu = pair_of(-u, -u);
+    template <bool HOLD> __device__ __forceinline__ void sums_of(const uint4 (&raw)[U], const Scale& c, float& s_, float& w_) const {
+        const pair_t uu = pair_of(-u, -u), c2c2 = pair_of(c.c2, c.c2), lolo = pair_of(c.low, c.low);
         pair_t s2 = 0, w2 = 0;   // of these vectors first: see tree_sum
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             float f[N];
             Vec<T>::wide(HOLD ? held(raw[i]) : raw[i], f);
+            if (HOLD && sizeof(T) == 4) {   // -inf times a negative low part
+#pragma unroll
+                for (int j = 0; j < N; ++j) f[j] = max_nan(f[j], -3.4e38f);
+            }
 #pragma unroll
             for (int j = 0; j < N; j += 2) {
                 pair_t z = fma_pair(pair_of(f[j], f[j + 1]), c2c2, uu);
+                if (sizeof(T) == 4) z = fma_pair(pair_of(f[j], f[j + 1]), lolo, z);
                 float z0, z1;
                 apart(z, z0, z1);
                 if (HOLD && sizeof(T) == 4) {
@@ -119,7 +150,7 @@ template <typename T> struct Running {
         w_ = p0 + p1;
     }
     // U vectors, of which the largest element has been through raise(); whole: none of them is empty.
-    __device__ __forceinline__ void add(const uint4 (&raw)[U], bool whole, pair_t c2c2, float c2) {
+    __device__ __forceinline__ void add(const uint4 (&raw)[U], bool whole, const Scale& c) {
         if (slow || m == kNegInf) {
 #pragma unroll 1
             for (int i = 0; i < U; ++i) {
@@ -127,15 +158,46 @@ template <typename T> struct Running {
                 float f[N];
                 Vec<T>::wide(v, f);
 #pragma unroll
-                for (int j = 0; j < N; ++j) add_one(f[j], c2);
+                for (int j = 0; j < N; ++j) add_one(f[j], c);
             }
             return;
         }
-        float ds = 0.0f, dw = __int_as_float(0x7fffffff);
-        if (whole) sums_of<false>(raw, c2c2, ds, dw);
-        if (dw != dw) sums_of<true>(raw, c2c2, ds, dw);   // 0 times an excluded entry's exponent, or a NaN entry
-        s += ds;
-        w += dw;
+        float ds = 0.0f, dw = __int_as_float(0x7fffffff), left;
+        if (whole) sums_of<false>(raw, c, ds, dw);
+        if (dw != dw) sums_of<true>(raw, c, ds, dw);   // 0 times an excluded entry's exponent, or a NaN entry
+        if (sizeof(T) == 4) {
+            s = sum_parts(s, ds, left);
+            s_left += left;
+            w = sum_parts(w, dw, left);
+            w_left += left;
+        } else {
+            s += ds;
+            w += dw;
+        }
+    }
+    __device__ __forceinline__ void fold() {
+        if (sizeof(T) != 4) return;
+        s += s_left;
+        w += w_left;
+        s_left = w_left = 0.0f;
+    }
+    // The exponential of the thread's largest element again, from its exponent in full and without the
+    // hardware unit's error: the reference may be 32 bits below it, where the exponent rounds to 2^-20, and a row
+    // that it dominates has nothing to average either error with (entropies off by 1.6e-7 of themselves where
+    // labels have most of the probability, 5e-8 so).
+    __device__ __forceinline__ void retake(float top, const Scale& c) {
+        fold();
+        if (slow || !(m > kNegInf) || !(__fmaf_rn(top, c.c2, -u) > -64.0f)) return;   // nothing, or too little to count
+        const float low = sizeof(T) == 4 ? c.low : 0.0f;
+        const float p = __fmul_rn(top, c.c2), pe = __fmaf_rn(top, low, __fmaf_rn(top, c.c2, -p));
+        float left;
+        const float at = sum_parts(p, -u, left), n = rintf(at), rest = left + pe;
+        const float e = power_near_1((at - n) + rest) * __int_as_float((int(n) + 127) << 23);
+        float z = __fmaf_rn(top, c.c2, -u);
+        if (sizeof(T) == 4) z = __fmaf_rn(top, low, z);
+        const float d = e - ex2(z);
+        s += d;
+        w += __fmaf_rn(e, (at - z) + rest, d * z);
     }
     static __device__ __forceinline__ uint4 held(uint4 v) {
         if constexpr (sizeof(T) == 2) {
@@ -340,9 +402,6 @@ __device__ __forceinline__ uint32_t remote_address(const void* smem, uint32_t ra
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(at), "r"(rank));
     return to;
 }
-__device__ __forceinline__ void store_remote(uint32_t to, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(v) : "memory");
-}
 __device__ __forceinline__ void store_remote(uint32_t to, unsigned long long v) {
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to), "l"(v) : "memory");
 }
@@ -372,20 +431,22 @@ template <int PARTS> __device__ __forceinline__ RowSums join_parts(float4 p, flo
     return r;
 }
 // The warp's part of them, its edge elements (-inf: none) included.
-template <typename T> __device__ __forceinline__ float4 warp_part(Running<T>& t, float top, float xe, bool edge, float c2) {
+template <typename T> __device__ __forceinline__ float4 warp_part(Running<T>& t, float top, float xe, bool edge, const Scale& c) {
+    t.retake(top, c);
     const float wt = warp_max(fmaxf(top, xe)), ref = part_ref(wt), least = -warp_max(-top);
-    move_sums(t.m, ref, c2, t.s, t.w);
+    move_sums(t.m, ref, c.c2, t.s, t.w);
     t.m = ref;
-    if (edge) t.add_one(xe, c2);
+    if (edge) t.add_one(xe, c);
     return make_float4(wt, warp_sum(t.s), warp_sum(t.w), least);
 }
 
 // A row's softmax, and its outputs.
 struct RowSoftmax {
-    float M, S, W, u, c2, it, n, rest;
+    float M, S, W, u, c2, low, it, n, rest;
     bool none, far;   // none: no softmax
-    __device__ __forceinline__ RowSoftmax(const RowSums& r, const StatsArgs& a)
-        : M(r.M), S(r.S), W(r.W), u(anchor(r.M, a.c2)), c2(a.c2), it(a.it), none(!(fabsf(r.M) < INFINITY) || r.S != r.S),
+    // fp32: whether the scale's low part counts (Scale)
+    __device__ __forceinline__ RowSoftmax(const RowSums& r, const StatsArgs& a, bool fp32)
+        : M(r.M), S(r.S), W(r.W), u(anchor(r.M, a.c2)), c2(a.c2), low(fp32 ? a.c2_low : 0.0f), it(a.it), none(!(fabsf(r.M) < INFINITY) || r.S != r.S),
           far(big(r.M, a.c2)) {
         log2_parts(S, n, rest);
     }
@@ -393,13 +454,14 @@ struct RowSoftmax {
     // whose exponent overflows, has its distance.
     __device__ __forceinline__ float share(float x) const {
         if (none) return __int_as_float(0x7fffffff);
-        const float r = log_share(x, M, u, c2, far, n, rest);
+        if (x == kNegInf) return kNegInf;
+        const float r = log_share(x, M, u, c2, far, n, __fmaf_rn(far ? M - x : -x, low, rest));
         return fminf(r == kNegInf ? (x - M) * it : r, 0.0f);
     }
     // By a warp; xy: the label's logit.
     __device__ __forceinline__ void finish(const StatsArgs& a, int64_t r, int64_t y, float xy) const {
         const float kNaN = __int_as_float(0x7fffffff), log_sum = -share(M), lp = share(xy);
-        const float H = fmaxf(log_sum + ((far ? 0.0f : __fmaf_rn(M, c2, -u)) - W / S) * kLn2, 0.0f);
+        const float H = fmaxf(log_sum + ((far ? 0.0f : __fmaf_rn(M, low, __fmaf_rn(M, c2, -u))) - W / S) * kLn2, 0.0f);
         if ((threadIdx.x & 31) != 0) return;
         if (a.logp) a.logp[r] = y < a.vocab ? lp : kNaN;
         if (a.entropy) a.entropy[r] = none ? kNaN : H;
@@ -706,7 +768,7 @@ __global__ void __launch_bounds__(B + NT * SB, PER_SM) k_top(const StatsArgs a) 
         // ------------------------------------------------------------ the rows
         const int tid = threadIdx.x, warp = tid >> 5;
         Feed<T, B, TV, ST> feed(a, ring, group, ngroups, 0, 0, tid);
-        const pair_t c2c2 = pair_of(c2, c2);
+        const Scale scale(a);
         int done = 0;   // rows so far, up to NB
         for (int64_t r = group; r < a.rows; r += ngroups) {
             if (label(r) < 0) continue;
@@ -733,11 +795,11 @@ __global__ void __launch_bounds__(B + NT * SB, PER_SM) k_top(const StatsArgs a) 
                     const float t = keep_maxima<T, B, T>(gm, gs, base + g, raw, run, tid);
                     top = fmaxf(top, t);
                     sum.raise(t, c2);
-                    sum.add(raw, B * (g + 3) < mine, c2c2, c2);
+                    sum.add(raw, B * (g + 3) < mine, scale);
                 }
             }
             gm[G][tid] = from_f<T>(top);
-            const float4 part = warp_part(sum, top, xe, edge, c2);
+            const float4 part = warp_part(sum, top, xe, edge, scale);
             if (lane == 0) wparts[buffer][warp] = part;
             bar_arrive(1 + buffer, B + SB);
             next();
@@ -775,7 +837,7 @@ __global__ void __launch_bounds__(B + NT * SB, PER_SM) k_top(const StatsArgs a) 
         if (tid == 0) nfound[team] = nlist[team] = 0;
         bar_sync(1 + buffer, B + SB);
         const RowSums sums = join_parts<nw>(lane < nw ? wparts[buffer][lane] : make_float4(kNegInf, 0.0f, 0.0f, INFINITY), c2);
-        const RowSoftmax row(sums, a);
+        const RowSoftmax row(sums, a, sizeof(T) == 4);
         if (warp == 0) row.finish(a, r, y, xy);
         if (row.none) {
             for (int i = tid; i < a.k; i += SB) put_entry(a, r, i, -1, row.share(0.0f));
@@ -901,7 +963,7 @@ cudaError_t top_launch(const StatsArgs& a, int sms, GroupCache& cache, cudaStrea
 // A warp per row (W = 1, four rows to a CTA) or a CTA of W warps, NV vectors per thread.  The row is
 // read once; the entries are chosen where it is.
 template <typename T, int W, int NV, bool TOP>
-__global__ void __launch_bounds__(128, NV > 8 ? 3 : NV > 4 ? 4 : 6) k_held(const StatsArgs a) {
+__global__ void __launch_bounds__(128, NV > 8 ? (TOP ? 3 : 4) : NV > 4 ? (TOP ? 5 : 6) : TOP ? 7 : 8) k_held(const StatsArgs a) {
     constexpr int N = Vec<T>::N, SB = 32 * W, TEAMS = 4 / W, CAP = W == 1 ? 512 : kCandidates;
     __shared__ float4 wparts[W == 1 ? 1 : 2][4];
     __shared__ float2 wtops[W == 1 ? 1 : 2][4];
@@ -913,7 +975,7 @@ __global__ void __launch_bounds__(128, NV > 8 ? 3 : NV > 4 ? 4 : 6) k_held(const
     const Stage stage{ring + team * (SB * NV), reinterpret_cast<int*>(ring + TEAMS * SB * NV) + team * (SB * NV), &nstage[team]};
     unsigned long long* const found = reinterpret_cast<unsigned long long*>(reinterpret_cast<int*>(ring + TEAMS * SB * NV) + TEAMS * SB * NV) + team * CAP;
     const float c2 = a.c2;
-    const pair_t c2c2 = pair_of(c2, c2);
+    const Scale scale(a);
     const int64_t step = int64_t(gridDim.x) * TEAMS, start = int64_t(blockIdx.x) * TEAMS + team;
     int64_t ynext = a.target && start < a.rows ? a.target[start] : 0;
     int turn = 0, par = 0;
@@ -937,14 +999,14 @@ __global__ void __launch_bounds__(128, NV > 8 ? 3 : NV > 4 ? 4 : 6) k_held(const
         }
         const float xe = edge ? to_f(x[pl.edge_at(tid)]) : kNegInf;
         const float xy = a.logp && y < a.vocab ? to_f(x[y]) : 0.0f;
-        float tops[NV], top = xe, low = INFINITY;   // low: the least of the vectors' largest entries
+        float tops[NV], top = kNegInf, low = INFINITY;   // low: the least of the vectors' largest entries
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             top = fmaxf(top, tops[i] = Vec<T>::top(raw[i]));
             const int v = i * SB + tid - pl.off;
             if (TOP && v >= 0 && v < pl.body) low = fminf(low, tops[i]);
         }
-        float M = warp_max(top);
+        float M = warp_max(fmaxf(top, xe));
         if (TOP) low = -warp_max(-low);
         if (W > 1) {
             if (lane == 0) wtops[par][warp] = make_float2(M, low);
@@ -961,9 +1023,10 @@ __global__ void __launch_bounds__(128, NV > 8 ? 3 : NV > 4 ? 4 : 6) k_held(const
 #pragma unroll
         for (int i = 0; i < NV; i += 4) {
             const uint4 four[4] = {raw[i], raw[i + 1], raw[i + 2], raw[i + 3]};
-            sum.add(four, false, c2c2, c2);
+            sum.add(four, false, scale);
         }
-        if (edge) sum.add_one(xe, c2);
+        sum.retake(top, scale);
+        if (edge) sum.add_one(xe, scale);
         RowSums sums{M, warp_sum(sum.s), warp_sum(sum.w), kNegInf};
         if (W > 1) {
             if (lane == 0) wparts[par][warp] = make_float4(0.0f, sums.S, sums.W, 0.0f);
@@ -972,11 +1035,12 @@ __global__ void __launch_bounds__(128, NV > 8 ? 3 : NV > 4 ? 4 : 6) k_held(const
             sums.W = (wparts[par][0].z + wparts[par][1].z) + (wparts[par][2].z + wparts[par][3].z);
             par ^= 1;
         }
-        const RowSoftmax row(sums, a);
-        if (W == 1 || warp == 0) row.finish(a, r, y, xy);
-        if (!TOP) continue;
-        if (row.none) {
-            for (int i = tid; i < a.k; i += SB) put_entry(a, r, i, -1, row.share(0.0f));
+        const RowSoftmax row(sums, a, sizeof(T) == 4);
+        const bool finishes = W == 1 || warp == 0;
+        if (!TOP || row.none) {
+            if (finishes) row.finish(a, r, y, xy);
+            if (TOP)
+                for (int i = tid; i < a.k; i += SB) put_entry(a, r, i, -1, row.share(0.0f));
             continue;
         }
         // t among the vectors' maxima while there are twice as many as k, else among the entries themselves
@@ -1022,7 +1086,8 @@ __global__ void __launch_bounds__(128, NV > 8 ? 3 : NV > 4 ? 4 : 6) k_held(const
             put_entry(a, r, place, int(~uint32_t(c)), row.share(logit_of(uint32_t(c >> 32))));
         });
         for (int i = n + tid; i < a.k; i += SB) put_entry(a, r, i, -1, kNegInf);
-        sync<SB>(1);   // before the next row's candidates
+        if (finishes) row.finish(a, r, y, xy);
+        if (W == 1) __syncwarp();   // before the next row's candidates; with more warps its barriers come first
     }
 }
 
@@ -1053,33 +1118,25 @@ template <typename T, bool TOP> cudaError_t held(const StatsArgs& a, int places,
 // A group of CTAs per row
 // ---------------------------------------------------------------------------
 
-constexpr int kGroups = 8;   // groups of vectors to the threads of one place in the row's CTAs
-
-// A group of 2^clog CTAs takes one row at a time, each CTA a contiguous share of the row's vectors.  With
-// alternatives (TOP) for few rows alone, where a row is spread over CTAs: each CTA hands its groups'
-// maxima to all others, all of them search for t alike, and the first one collects the candidates.
-template <typename T, int B, bool TOP>
-__global__ void __launch_bounds__(B, (TOP ? 256 : 512) / B) k_stats(const StatsArgs a, const int clog) {
-    constexpr int TV = 8, ST = 3, nw = B / 32, G = kGroups;
+// Without alternatives: a group of 2^clog CTAs takes one row at a time, each CTA a contiguous share of the
+// row's vectors.  What bounds it: memory (4,096 x 128,256 bf16: 148 us, 7.1 TB/s of reads; one row 4.7 us).
+template <typename T, int B>
+__global__ void __launch_bounds__(B, 512 / B) k_stats(const StatsArgs a, const int clog) {
+    constexpr int TV = 8, ST = 3, nw = B / 32;
     __shared__ float4 wparts[2][8], cparts[2][kMaxCluster];   // by row parity: of the warps, of the CTAs
-    __shared__ int counts[2][8], nfound[2], nlist[2];
-    __shared__ __align__(16) int bins[TOP ? kBins : 4];
     extern __shared__ __align__(128) uint4 ring[];   // [ST][TV * B]
-    unsigned long long* const found = reinterpret_cast<unsigned long long*>(ring + ST * TV * B);   // [kCandidates]
-    float(*const gmax)[B] = reinterpret_cast<float(*)[B]>(found + kCandidates);                     // [G][B]
-    uint16_t* const list = reinterpret_cast<uint16_t*>(gmax + G);                                   // [G * B]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cluster = 1 << clog, rank = cluster > 1 ? int(cluster_rank()) : 0;
     const int group = int(blockIdx.x) >> clog, ngroups = int(gridDim.x) >> clog;
-    const int own = G >> clog;   // groups of this CTA's threads
     const float c2 = a.c2;
-    const pair_t c2c2 = pair_of(c2, c2);
+    const Scale scale(a);
+    const float4 none_part = make_float4(kNegInf, 0.0f, 0.0f, INFINITY);
     Feed<T, B, TV, ST> feed(a, ring, group, ngroups, rank, clog, tid);
     if (cluster > 1) {   // every CTA of the group runs before any writes into another
         cluster_arrive();
         cluster_wait();
     }
-    int par = 0, turn = 0, finisher = 0;
+    int par = 0, finisher = 0;
     int64_t ynext = a.target && group < a.rows ? a.target[group] : 0;
     for (int64_t r = group; r < a.rows; r += ngroups) {
         const int64_t y = ynext;
@@ -1096,13 +1153,8 @@ __global__ void __launch_bounds__(B, (TOP ? 256 : 512) / B) k_stats(const StatsA
         const bool finishes = rank == 0 && warp == finisher;
         const float xy = finishes && a.logp && y < a.vocab ? to_f(x[y]) : 0.0f;
         const int places = pl.hi > pl.lo ? pl.hi - pl.lo + pl.off : 0;
-        int gs = 0;
-        if (TOP) {
-            gs = group_shift((places + TV * B - 1) / (TV * B) * TV, own);
-            for (int g = 0; g < own; ++g) gmax[rank * own + g][tid] = kNegInf;
-        }
         Running<T> sum;
-        float top = kNegInf, run = kNegInf;
+        float top = kNegInf;
         for (int base = 0; base * B < places; base += TV) {
             const uint4* const buf = feed.take();
             const int mine = places - base * B - tid;
@@ -1111,50 +1163,109 @@ __global__ void __launch_bounds__(B, (TOP ? 256 : 512) / B) k_stats(const StatsA
                 if (B * g >= mine) break;
                 uint4 raw[4];
                 load_four<T, B>(buf, g, mine, raw);
-                const float t = TOP ? keep_maxima<T, B, float>(gmax + rank * own, gs, base + g, raw, run, tid) : top_of<T>(raw);
+                const float t = top_of<T>(raw);
                 top = fmaxf(top, t);
                 sum.raise(t, c2);
-                sum.add(raw, B * (g + 3) < mine, c2c2, c2);
+                sum.add(raw, B * (g + 3) < mine, scale);
             }
         }
-        {
-            const float4 part = warp_part(sum, top, xe, edge, c2);
-            if (lane == 0) wparts[par][warp] = part;
-            if (tid == 0) nfound[par] = nlist[par] = 0;
-        }
-        const float4 none_part = make_float4(kNegInf, 0.0f, 0.0f, INFINITY);
+        const float4 part = warp_part(sum, top, xe, edge, scale);
+        if (lane == 0) wparts[par][warp] = part;
         __syncthreads();
         if (cluster > 1) {
             if (warp == 0) {
                 const RowSums p = join_parts<8>(lane < nw ? wparts[par][lane] : none_part, c2);
                 if (lane < cluster) store_remote(&cparts[par][rank], uint32_t(lane), make_float4(p.M, p.S, p.W, p.least));
             }
-            if (TOP)
-                for (int c = 0; c < cluster; ++c) {
-                    if (c == rank) continue;
-                    for (int g = rank * own; g < (rank + 1) * own; ++g)
-                        store_remote(remote_address(&gmax[g][tid], uint32_t(c)), gmax[g][tid]);
-                }
             cluster_arrive();
             cluster_wait();
         }
-        const int was = par;
+        if (finishes) {
+            const RowSums sums = cluster > 1 ? join_parts<8>(lane < cluster ? cparts[par][lane] : none_part, c2)
+                                             : join_parts<8>(lane < nw ? wparts[par][lane] : none_part, c2);
+            RowSoftmax(sums, a, sizeof(T) == 4).finish(a, r, y, xy);
+        }
         par ^= 1;
         finisher = finisher + 1 == nw ? 0 : finisher + 1;
-        if (!TOP && !finishes) continue;
-        const RowSums sums = cluster > 1 ? join_parts<8>(lane < cluster ? cparts[was][lane] : none_part, c2)
-                                         : join_parts<8>(lane < nw ? wparts[was][lane] : none_part, c2);
-        const RowSoftmax row(sums, a);
-        if (finishes) row.finish(a, r, y, xy);
-        if (!TOP) continue;
-        if (row.none) {
-            if (rank == 0)
-                for (int i = tid; i < a.k; i += B) put_entry(a, r, i, -1, row.share(0.0f));
+    }
+    copy_wait<0>();
+}
+
+// With alternatives, for few rows: each CTA of the group chooses the k largest entries of its share and hands
+// them, with its sums, to the first one, which puts all of them in order.  What bounds it: latency.
+constexpr int kJoined = 4096;   // candidates of all CTAs
+template <int B> struct SpreadShared {
+    static constexpr int G = 8;      // groups of vectors per thread
+    uint4 ring[3][8 * B];
+    unsigned long long found[kJoined];
+    union {                          // the groups' maxima; then the share's candidates
+        float gmax[G][B];
+        unsigned long long home[G * B / 2];
+    };
+    uint16_t list[kJoined];          // groups to look at again; then the order of the candidates
+};
+template <typename T, int B>
+__global__ void __launch_bounds__(B, 1) k_spread(const StatsArgs a, const int clog) {
+    constexpr int TV = 8, ST = 3, nw = B / 32, G = SpreadShared<B>::G, kHome = G * B / 2, kPlaces = B * TV;
+    static_assert(G * B <= kJoined, "every group has a place in the list");
+    __shared__ float4 wparts[8], cparts[kMaxCluster];   // of the warps, of the CTAs
+    __shared__ int counts[2][8], nfound, nlist, nhome, first_place;
+    __shared__ __align__(16) int bins[kBins];
+    extern __shared__ __align__(128) uint4 ring[];
+    SpreadShared<B>& sh = *reinterpret_cast<SpreadShared<B>*>(ring);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int cluster = 1 << clog, rank = int(cluster_rank());
+    const int group = int(blockIdx.x) >> clog, ngroups = int(gridDim.x) >> clog;
+    const float c2 = a.c2;
+    const Scale scale(a);
+    const float4 none_part = make_float4(kNegInf, 0.0f, 0.0f, INFINITY);
+    Feed<T, B, TV, ST> feed(a, ring, group, ngroups, rank, clog, tid);
+    if (tid == 0) nfound = 0;
+    cluster_arrive();   // every CTA of the group runs before any writes into another
+    cluster_wait();
+    int turn = 0;
+    int64_t ynext = a.target && group < a.rows ? a.target[group] : 0;
+    for (int64_t r = group; r < a.rows; r += ngroups) {
+        const int64_t y = ynext;
+        if (a.target && r + ngroups < a.rows) ynext = a.target[r + ngroups];
+        if (y < 0) {
+            if (rank == 0) ignored_row(a, r, tid, B);
             continue;
         }
+        const T* const x = feed.row_at(r);
+        const Place<T> pl = feed.place_of(x);
+        const bool edge = rank == 0 && tid < pl.edges;
+        const float xe = edge ? to_f(x[pl.edge_at(tid)]) : kNegInf;
+        const float xy = rank == 0 && warp == 0 && a.logp && y < a.vocab ? to_f(x[y]) : 0.0f;
+        const int places = pl.hi > pl.lo ? pl.hi - pl.lo + pl.off : 0;
+        const int gs = group_shift((places + kPlaces - 1) / kPlaces * TV, G);
+#pragma unroll
+        for (int g = 0; g < G; ++g) sh.gmax[g][tid] = kNegInf;
+        Running<T> sum;
+        float top = kNegInf, run = kNegInf;
+        const uint4* buf = nullptr;
+        for (int base = 0; base * B < places; base += TV) {
+            buf = feed.take();
+            const int mine = places - base * B - tid;
+#pragma unroll 1
+            for (int g = 0; g < TV; g += 4) {
+                if (B * g >= mine) break;
+                uint4 raw[4];
+                load_four<T, B>(buf, g, mine, raw);
+                const float t = keep_maxima<T, B, float>(sh.gmax, gs, base + g, raw, run, tid);
+                top = fmaxf(top, t);
+                sum.raise(t, c2);
+                sum.add(raw, B * (g + 3) < mine, scale);
+            }
+        }
+        const float4 part = warp_part(sum, top, xe, edge, scale);
+        if (lane == 0) wparts[warp] = part;
+        if (tid == 0) nlist = nhome = 0;
+        __syncthreads();
+        const RowSums share = join_parts<8>(lane < nw ? wparts[lane] : none_part, c2);
         float key[G];
 #pragma unroll
-        for (int g = 0; g < G; ++g) key[g] = gmax[g][tid];
+        for (int g = 0; g < G; ++g) key[g] = sh.gmax[g][tid];
         auto count = [&](float v) {
             int c = 0;
 #pragma unroll
@@ -1162,21 +1273,24 @@ __global__ void __launch_bounds__(B, (TOP ? 256 : 512) / B) k_stats(const StatsA
             return sum_over<B>(c, counts, turn, tid, 0);
         };
         uint32_t lo = kLeast<T>;
-        const bool full = a.k <= B && sums.least > kNegInf;   // each thread has a group from the least of their tops on
-        if (full) lo = rank_of<T>(sums.least);
-        const int from = full ? B * G : count(logit_of(lo << Order<T>::kShift));
-        if (from > a.k) lo = search_rank<T>(lo, from, row.M, a.k, count);
+        if (share.M > kNegInf && share.M < INFINITY) {
+            const bool full = a.k <= B && share.least > kNegInf;   // each thread has a group from the least of their tops on
+            if (full) lo = rank_of<T>(share.least);
+            const int from = full ? B * G : count(logit_of(lo << Order<T>::kShift));
+            if (from > a.k) lo = search_rank<T>(lo, from, share.M, a.k, count);
+        }
         const float least = logit_of(lo << Order<T>::kShift);
-        // the groups from there on, each CTA its own, and their entries, to the first CTA
-        if (top >= least)
-            for (int g = 0; g < own; ++g)
-                if (gmax[rank * own + g][tid] >= least) list[atomicAdd(&nlist[was], 1)] = uint16_t(g * B + tid);
+        if (top >= least) {
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+                if (key[g] >= least) sh.list[atomicAdd(&nlist, 1)] = uint16_t(g * B + tid);
+        }
         __syncthreads();
-        const uint32_t far_found = remote_address(found, 0), far_count = remote_address(&nfound[was], 0);
-        auto add = [&](int n) { return add_remote(far_count, n); };
-        auto store = [&](int i, unsigned long long c) { if (i < kCandidates) store_remote(far_found + 8u * uint32_t(i), c); };
+        auto add = [&](int n) { return atomicAdd(&nhome, n); };
+        auto store = [&](int i, unsigned long long c) { if (i < kHome) sh.home[i] = c; };
         if (edge && xe >= least) store(add(1), candidate(order_of(xe), pl.edge_at(tid)));
-        const int items = nlist[was] << gs;
+        const int items = nlist << gs;
+        const uint4* const tile = places <= kPlaces ? buf - tid : nullptr;   // a share of one tile is still there
         for (int first = tid; first < items; first += 4 * B) {
             uint4 raw[4];
             int at[4];
@@ -1185,34 +1299,61 @@ __global__ void __launch_bounds__(B, (TOP ? 256 : 512) / B) k_stats(const StatsA
                 const int item = first + B * i;
                 at[i] = -1;
                 if (item < items) {
-                    const int e = list[item >> gs], t = e & (B - 1);
+                    const int e = sh.list[item >> gs], t = e & (B - 1);
                     const int place = t + B * (((e / B) << gs) + (item & ((1 << gs) - 1)));
-                    if (place >= pl.off && place < places) at[i] = pl.head + (pl.lo + place - pl.off) * Vec<T>::N;
+                    if (place >= pl.off && place < places) {
+                        at[i] = pl.head + (pl.lo + place - pl.off) * Vec<T>::N;
+                        raw[i] = tile ? tile[place] : ld16(x + at[i]);
+                    }
                 }
-                if (at[i] >= 0) raw[i] = ld16(x + at[i]);
             }
             offer_vectors<T, 4>(raw, least, [&](int i) { return at[i]; }, add, store);
         }
+        __syncthreads();
+        const int here = nhome;
+        if (tid == 0 && here > 0) first_place = add_remote(remote_address(&nfound, 0), here <= kHome ? here : kJoined + 1);
+        if (warp == 1 && lane == 0)
+            store_remote(&cparts[rank], 0u, make_float4(share.M, share.S, share.W, __uint_as_float(lo)));
+        __syncthreads();
+        const uint32_t to = remote_address(sh.found, 0) + 8u * uint32_t(first_place);
+        if (here > 0 && here <= kHome)
+            for (int i = tid; i < here && first_place + i < kJoined; i += B) store_remote(to + 8u * uint32_t(i), sh.home[i]);
         cluster_arrive();
         cluster_wait();
-        if (rank != 0) continue;
-        int n = nfound[was];
-        if (n > kCandidates) n = exact_candidates<T, B>(x, a.vocab, a.k, lo, row.M, found, &nfound[was], counts, turn, tid, 0);
-        place_candidates<T, B>(found, n, lo, row.M, a.k, bins, list, tid, 0, [&](unsigned long long c, int place) {
-            put_entry(a, r, place, int(~uint32_t(c)), row.share(logit_of(uint32_t(c >> 32))));
-        });
-        for (int i = n + tid; i < a.k; i += B) put_entry(a, r, i, -1, kNegInf);
+        if (rank == 0) {
+            const float4 p = lane < cluster ? cparts[lane] : make_float4(kNegInf, 0.0f, 0.0f, __uint_as_float(~0u));
+            lo = __reduce_min_sync(~0u, p.x > kNegInf ? __float_as_uint(p.w) : ~0u);
+            const RowSoftmax row(join_parts<8>(make_float4(p.x, p.y, p.z, 0.0f), c2), a, sizeof(T) == 4);
+            if (row.none) {
+                for (int i = tid; i < a.k; i += B) put_entry(a, r, i, -1, row.share(0.0f));
+                __syncthreads();
+            } else {
+                int n = nfound;
+                __syncthreads();
+                if (n > kJoined) n = exact_candidates<T, B>(x, a.vocab, a.k, lo, row.M, sh.found, &nfound, counts, turn, tid, 0);
+                place_candidates<T, B>(sh.found, n, lo, row.M, a.k, bins, sh.list, tid, 0, [&](unsigned long long c, int place) {
+                    put_entry(a, r, place, int(~uint32_t(c)), row.share(logit_of(uint32_t(c >> 32))));
+                });
+                for (int i = n + tid; i < a.k; i += B) put_entry(a, r, i, -1, kNegInf);
+            }
+            if (warp == 0) row.finish(a, r, y, xy);
+            if (tid == 0) nfound = 0;
+        }
+        if (r + ngroups < a.rows) {   // the first CTA has done with the row
+            cluster_arrive();
+            cluster_wait();
+        }
     }
     copy_wait<0>();
 }
 
 template <typename T, int B, bool TOP>
 cudaError_t stats_launch(const StatsArgs& a, int clog, int sms, GroupCache& cache, cudaStream_t s) {
-    auto* kernel = k_stats<T, B, TOP>;
+    auto* kernel = TOP ? k_spread<T, B> : k_stats<T, B>;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(1u << clog);
     cfg.blockDim = dim3(B);
-    cfg.dynamicSmemBytes = size_t(16) * 3 * 8 * B + (TOP ? size_t(8) * kCandidates + size_t(6) * kGroups * B : 0);
+    cfg.dynamicSmemBytes = TOP ? sizeof(SpreadShared<B>) : size_t(16) * 3 * 8 * B;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1232,7 +1373,10 @@ cudaError_t stats_launch(const StatsArgs& a, int clog, int sms, GroupCache& cach
 template <typename T>
 cudaError_t stats(const StatsArgs& a, int sms, GroupCache& cache, cudaStream_t s) {
     const int vecs = (a.vocab + Vec<T>::N - 1) / Vec<T>::N, threads = vecs <= 8192 ? 128 : 256;
-    if (vecs + 7 <= 2048) return a.k > 0 ? held<T, true>(a, vecs + 7, sms, cache, s) : held<T, false>(a, vecs + 7, sms, cache, s);
+    // places of a row: its vectors, and the empty places before them (where all rows lie alike, theirs)
+    const uintptr_t body = (reinterpret_cast<uintptr_t>(a.x) + 15) / 16;
+    const int places = vecs + ((a.ld * int64_t(sizeof(T))) % 128 == 0 ? int(body & 7) : 7);
+    if (places <= 2048) return a.k > 0 ? held<T, true>(a, places, sms, cache, s) : held<T, false>(a, places, sms, cache, s);
     // few rows: spread each over more CTAs while the GPU has idle SMs and the share is over a tile
     int clog = 0;
     while (clog < kMaxClusterLog && a.rows << (clog + 1) <= sms && (threads * 8) << clog < vecs) clog += 1;
