@@ -731,23 +731,25 @@ constexpr int kList = 1024;   // groups that are read again; more: the exact sea
 
 // Dynamic shared memory of a CTA.  The maxima of a thread's 16 groups of vectors, and the largest of all,
 // are kept in the logits' own type.
+// A buffer belongs to one team (their number is a multiple of the teams'): a team that runs ahead of another
+// would else take the other's rows for its own.
 template <typename T, int B, int NT, int TV, int ST> struct TopShared {
-    static constexpr int G = 16;
+    static constexpr int G = 16, NB = 2 * NT;
     uint4 ring[ST][TV * B];
     unsigned long long found[NT][kCandidates];
-    T gmax[NT + 1][G + 1][B];   // per row
+    T gmax[NB][G + 1][B];   // per buffer
     int bins[NT][kBins];
     uint16_t list[NT][kList];
 };
 
 // B threads read rows and leave the maxima of groups; NT teams of SB threads take rows in turns and
-// choose their entries while the former are in the next rows.  NT + 1 rows' maxima are kept (`buffer`).
-// Named barriers 1 + buffer: a row's maxima and sums are there; 1 + NT + 1 + buffer: they have been used;
+// choose their entries while the former are in the next rows.  NB rows' maxima are kept (`buffer`).
+// Named barriers 1 + buffer: a row's maxima and sums are there; 1 + NB + buffer: they have been used;
 // then one per team.
 template <typename T, int B, int SB, int NT, int TV, int ST, int PER_SM>
 __global__ void __launch_bounds__(B + NT * SB, PER_SM) k_top(const StatsArgs a) {
     using Shared = TopShared<T, B, NT, TV, ST>;
-    constexpr int N = Vec<T>::N, nw = B / 32, G = Shared::G, NB = NT + 1, HELD = B / SB, KEYS = HELD * 4, LOADS = 8;
+    constexpr int N = Vec<T>::N, nw = B / 32, G = Shared::G, NB = Shared::NB, HELD = B / SB, KEYS = HELD * 4, LOADS = 8;
     static_assert(nw <= 16 && 2 * NB + NT < 16, "parts of a row for half a warp, 16 named barriers");
     __shared__ float4 wparts[NB][nw];
     __shared__ int counts[NT][2][8], nfound[NT], nlist[NT], nstage[NT];
@@ -859,7 +861,7 @@ __global__ void __launch_bounds__(B + NT * SB, PER_SM) k_top(const StatsArgs a) 
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
                     const float v = to_f(gm[g][tid + i * SB]);
-                    const int half = 4 * i + g / (G / 2), quarter = 4 * i + g / (G / 4);
+                    const int half = 4 * i + (g & 1), quarter = 4 * i + (g & 3);   // also where few groups are used
                     if (ss == 1) key[half] = fmaxf(key[half], v); else key[quarter] = fmaxf(key[quarter], v);
                 }
         }
@@ -963,10 +965,10 @@ cudaError_t top_launch(const StatsArgs& a, int sms, GroupCache& cache, cudaStrea
 // A warp per row (W = 1, four rows to a CTA) or a CTA of W warps, NV vectors per thread.  The row is
 // read once; the entries are chosen where it is.
 template <typename T, int W, int NV, bool TOP>
-__global__ void __launch_bounds__(128, NV > 8 ? (TOP ? 3 : 4) : NV > 4 ? (TOP ? 5 : 6) : TOP ? 7 : 8) k_held(const StatsArgs a) {
-    constexpr int N = Vec<T>::N, SB = 32 * W, TEAMS = 4 / W, CAP = W == 1 ? 512 : kCandidates;
-    __shared__ float4 wparts[W == 1 ? 1 : 2][4];
-    __shared__ float2 wtops[W == 1 ? 1 : 2][4];
+__global__ void __launch_bounds__(W > 4 ? 32 * W : 128, W > 4 ? 2 : NV > 8 ? (TOP ? 3 : 4) : NV > 4 ? (TOP ? 5 : 6) : TOP ? 7 : 8) k_held(const StatsArgs a) {
+    constexpr int N = Vec<T>::N, SB = 32 * W, TEAMS = W == 1 ? 4 : 1, CAP = W == 1 ? 512 : kCandidates;
+    __shared__ float4 wparts[W == 1 ? 1 : 2][W];
+    __shared__ float2 wtops[W == 1 ? 1 : 2][W];
     __shared__ int counts[2][8], nfound[TEAMS], nstage[TEAMS];
     __shared__ __align__(16) int bins[TOP ? TEAMS : 1][kBins];
     extern __shared__ __align__(128) uint4 ring[];
@@ -1012,8 +1014,11 @@ __global__ void __launch_bounds__(128, NV > 8 ? (TOP ? 3 : 4) : NV > 4 ? (TOP ? 
             if (lane == 0) wtops[par][warp] = make_float2(M, low);
             if (TOP && tid == 0) nfound[0] = nstage[0] = 0;
             __syncthreads();
-            M = fmaxf(fmaxf(wtops[par][0].x, wtops[par][1].x), fmaxf(wtops[par][2].x, wtops[par][3].x));
-            low = fminf(fminf(wtops[par][0].y, wtops[par][1].y), fminf(wtops[par][2].y, wtops[par][3].y));
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                M = fmaxf(M, wtops[par][i].x);
+                low = fminf(low, wtops[par][i].y);
+            }
         } else if (TOP) {
             if (lane == 0) nfound[team] = nstage[team] = 0;
             __syncwarp();
@@ -1031,8 +1036,12 @@ __global__ void __launch_bounds__(128, NV > 8 ? (TOP ? 3 : 4) : NV > 4 ? (TOP ? 
         if (W > 1) {
             if (lane == 0) wparts[par][warp] = make_float4(0.0f, sums.S, sums.W, 0.0f);
             __syncthreads();
-            sums.S = (wparts[par][0].y + wparts[par][1].y) + (wparts[par][2].y + wparts[par][3].y);
-            sums.W = (wparts[par][0].z + wparts[par][1].z) + (wparts[par][2].z + wparts[par][3].z);
+            sums.S = sums.W = 0.0f;
+#pragma unroll
+            for (int i = 0; i < W; i += 4) {
+                sums.S += (wparts[par][i].y + wparts[par][i + 1].y) + (wparts[par][i + 2].y + wparts[par][i + 3].y);
+                sums.W += (wparts[par][i].z + wparts[par][i + 1].z) + (wparts[par][i + 2].z + wparts[par][i + 3].z);
+            }
             par ^= 1;
         }
         const RowSoftmax row(sums, a, sizeof(T) == 4);
@@ -1096,22 +1105,25 @@ cudaError_t held_launch(const StatsArgs& a, int sms, GroupCache& cache, cudaStre
     auto* kernel = k_held<T, W, NV, TOP>;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(1);
-    cfg.blockDim = dim3(128);
-    cfg.dynamicSmemBytes = TOP ? size_t(8) * (W == 1 ? 4 * 512 : kCandidates) + size_t(20) * NV * 128 : 0;
+    constexpr int threads = W > 4 ? 32 * W : 128, rows = W == 1 ? 4 : 1;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = TOP ? size_t(8) * (W == 1 ? 4 * 512 : kCandidates) + size_t(20) * NV * threads : 0;
     cfg.stream = s;
     int groups = 0;
-    cudaError_t e = resident_groups(reinterpret_cast<const void*>(kernel), cfg, RowShape{128, 0}, sms, cache, groups);
+    cudaError_t e = resident_groups(reinterpret_cast<const void*>(kernel), cfg, RowShape{threads, 0}, sms, cache, groups);
     if (e != cudaSuccess) return e;
-    const int64_t want = (a.rows + 4 / W - 1) / (4 / W);
+    const int64_t want = (a.rows + rows - 1) / rows;
     cfg.gridDim.x = unsigned(groups < want ? groups : want);
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
+constexpr int kHeldPlaces = 4096, kHeldRows = 304;
 template <typename T, bool TOP> cudaError_t held(const StatsArgs& a, int places, int sms, GroupCache& cache, cudaStream_t s) {
     if (places <= 128) return held_launch<T, 1, 4, TOP>(a, sms, cache, s);
     if (places <= 256) return held_launch<T, 1, 8, TOP>(a, sms, cache, s);
     if (places <= 512) return held_launch<T, 4, 4, TOP>(a, sms, cache, s);
     if (places <= 1024) return held_launch<T, 4, 8, TOP>(a, sms, cache, s);
-    return held_launch<T, 4, 16, TOP>(a, sms, cache, s);
+    if (places <= 2048) return held_launch<T, 4, 16, TOP>(a, sms, cache, s);
+    return held_launch<T, 8, 16, TOP>(a, sms, cache, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -1376,7 +1388,7 @@ cudaError_t stats(const StatsArgs& a, int sms, GroupCache& cache, cudaStream_t s
     // places of a row: its vectors, and the empty places before them (where all rows lie alike, theirs)
     const uintptr_t body = (reinterpret_cast<uintptr_t>(a.x) + 15) / 16;
     const int places = vecs + ((a.ld * int64_t(sizeof(T))) % 128 == 0 ? int(body & 7) : 7);
-    if (places <= 2048) return a.k > 0 ? held<T, true>(a, places, sms, cache, s) : held<T, false>(a, places, sms, cache, s);
+    if (places <= (a.rows <= kHeldRows ? kHeldPlaces : 2048)) return a.k > 0 ? held<T, true>(a, places, sms, cache, s) : held<T, false>(a, places, sms, cache, s);
     // few rows: spread each over more CTAs while the GPU has idle SMs and the share is over a tile
     int clog = 0;
     while (clog < kMaxClusterLog && a.rows << (clog + 1) <= sms && (threads * 8) << clog < vecs) clog += 1;
