@@ -1,4 +1,6 @@
-"""Three post-training objectives on one small model, each trained with the optimizer step.
+"""Three post-training objectives on one small model, each trained with the optimizer step, and one of the
+caller's own: a policy gradient with an entropy bonus, made of per-token log-probabilities and entropies,
+with dropout on the hidden states.
 
 The model is an embedding followed by a linear head over the vocabulary, in fp16 with
 dynamic loss scaling; PyTorch does its two matrix products.  Everything from the logits on
@@ -18,6 +20,7 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import loss_scaled_adamw_gb300 as tl  # noqa: E402
 
 VOCAB, WIDTH, ROWS, TOP = 8192, 128, 256, 16
+DROP, BONUS = 0.1, 0.01
 
 
 class Model:
@@ -34,15 +37,25 @@ class Model:
         self.ctx = tl.tl_create([w.numel() for w in self.masters], self.params, self.masters, *state, cfg)
         self.hp = tl.tl_adamw_hp(lr=5e-3, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.0)
 
-    def logits(self, tokens):
-        self.hidden = self.embedding[tokens]
+    def logits(self, tokens, key=None):
+        """With a key: dropout on the hidden states, whose mask the backward pass draws again."""
+        self.hidden, self.key = self.embedding[tokens], key
+        if key is not None:
+            tl.tl_dropout(self.hidden, self.hidden, DROP, key)
         return self.hidden @ self.head.t()
 
-    def update(self, tokens, dlogits, n: int):
-        """Backward through the two products, then one logical update of one micro-batch."""
+    def gradients(self, tokens, dlogits):
+        """Backward through the two products."""
+        g_hidden = dlogits @ self.head
+        if self.key is not None:
+            tl.tl_dropout(g_hidden, g_hidden, DROP, self.key)
         g_embedding = torch.zeros_like(self.embedding)
-        g_embedding.index_add_(0, tokens, dlogits @ self.head)
-        tl.logical_update(self.ctx, [[g_embedding, dlogits.t() @ self.hidden]], [n], max_norm=1.0, hp=self.hp)
+        g_embedding.index_add_(0, tokens, g_hidden)
+        return [g_embedding, dlogits.t() @ self.hidden]
+
+    def update(self, tokens, dlogits, n: int):
+        """Then one logical update of one micro-batch."""
+        tl.logical_update(self.ctx, [self.gradients(tokens, dlogits)], [n], max_norm=1.0, hp=self.hp)
 
 
 def train(name: str, steps: int, lctx):
@@ -81,6 +94,46 @@ def train(name: str, steps: int, lctx):
     return result[:, 0].tolist(), tl.tl_read_status(model.ctx)
 
 
+class Bonus:
+    """The mean over n tokens of -advantage * log-probability - BONUS * entropy: forward by tl_token_stats,
+    gradient of the logits by tl_token_grad from the derivatives for each token."""
+
+    def __init__(self, lctx, targets, advantage, n: int, seed):
+        self.lctx, self.targets, self.seed = lctx, targets, seed
+        self.valid = (targets >= 0).float()
+        self.g_logp, self.g_entropy = -advantage * self.valid / n, -BONUS * self.valid / n
+        rows = targets.shape[0]
+        self.logp, self.entropy = torch.zeros(rows, device="cuda"), torch.zeros(rows, device="cuda")
+        self.saved = torch.zeros(rows, 3, device="cuda")
+
+    def loss(self, logits):
+        tl.tl_token_stats(self.lctx, logits, self.targets, logp=self.logp, entropy=self.entropy, saved=self.saved)
+        return (self.g_logp * self.logp + self.g_entropy * self.entropy).sum()
+
+    def gradient(self, logits):
+        """In the place of the logits."""
+        tl.tl_token_grad(self.lctx, logits, self.saved, logits, self.targets, self.g_logp, self.g_entropy, seed=self.seed)
+
+
+def train_bonus(steps: int, lctx):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(7)
+    model, losses = Model(1), torch.zeros(steps, device="cuda")
+    tokens = torch.randint(0, VOCAB, (ROWS,), generator=g, device="cuda")
+    targets = torch.randint(0, VOCAB, (ROWS,), generator=g, device="cuda")
+    targets[::8] = -100
+    n = ROWS - ROWS // 8
+    bonus = Bonus(lctx, targets, torch.ones(ROWS, device="cuda"), n, tl.tl_scale_ptr(model.ctx))
+    key = torch.tensor([7, 0], dtype=torch.int64, device="cuda")      # seed, ticket
+    for step in range(steps):
+        logits = model.logits(tokens, key)
+        losses[step] = bonus.loss(logits)
+        bonus.gradient(logits)
+        model.update(tokens, logits, n)
+        key[1:].add_(1)                                  # another mask for the next micro-batch
+    return losses.tolist(), tl.tl_read_status(model.ctx)
+
+
 def main():
     parser = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     parser.add_argument("--steps", type=int, default=60)
@@ -88,7 +141,12 @@ def main():
     lctx = tl.tl_loss_create(max_rows=ROWS, max_pairs=ROWS // 32)
     for name in ("distill", "preference", "policy"):
         losses, status = train(name, steps, lctx)
-        print(f"{name:10s} loss {losses[0]:.4f} -> {losses[-1]:.4f}   steps committed {status.t}, S = {status.S:g}")
+        report(name, losses, status)
+    report("bonus", *train_bonus(steps, lctx))
+
+
+def report(name, losses, status):
+    print(f"{name:10s} loss {losses[0]:.4f} -> {losses[-1]:.4f}   steps committed {status.t}, S = {status.S:g}")
 
 
 if __name__ == "__main__":

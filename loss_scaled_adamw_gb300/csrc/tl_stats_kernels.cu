@@ -1116,7 +1116,6 @@ cudaError_t held_launch(const StatsArgs& a, int sms, GroupCache& cache, cudaStre
     cfg.gridDim.x = unsigned(groups < want ? groups : want);
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
-constexpr int kHeldPlaces = 4096, kHeldRows = 304;
 template <typename T, bool TOP> cudaError_t held(const StatsArgs& a, int places, int sms, GroupCache& cache, cudaStream_t s) {
     if (places <= 128) return held_launch<T, 1, 4, TOP>(a, sms, cache, s);
     if (places <= 256) return held_launch<T, 1, 8, TOP>(a, sms, cache, s);
@@ -1388,7 +1387,11 @@ cudaError_t stats(const StatsArgs& a, int sms, GroupCache& cache, cudaStream_t s
     // places of a row: its vectors, and the empty places before them (where all rows lie alike, theirs)
     const uintptr_t body = (reinterpret_cast<uintptr_t>(a.x) + 15) / 16;
     const int places = vecs + ((a.ld * int64_t(sizeof(T))) % 128 == 0 ? int(body & 7) : 7);
-    if (places <= (a.rows <= kHeldRows ? kHeldPlaces : 2048)) return a.k > 0 ? held<T, true>(a, places, sms, cache, s) : held<T, false>(a, places, sms, cache, s);
+    // In registers up to 2,048 vectors, and up to 4,096 for rows that get a CTA each at once: us in registers / as below,
+    // bf16: 16,384 x 8,192 with 64 alternatives 152 / 283, 4,096 x 12,000 with 8 62 / 75, without 26 / 27, 4,096 x 17,000 with
+    // 8 104 / 84, without 49 / 34; 304 x 24,000 with 20 9.7 / 11.1, 600 x 24,000 with 20 18.2 / 15.0, 1 x 30,000 with 20
+    // 7.1 / 9.0.
+    if (places <= (a.rows <= 2 * sms ? 4096 : 2048)) return a.k > 0 ? held<T, true>(a, places, sms, cache, s) : held<T, false>(a, places, sms, cache, s);
     // few rows: spread each over more CTAs while the GPU has idle SMs and the share is over a tile
     int clog = 0;
     while (clog < kMaxClusterLog && a.rows << (clog + 1) <= sms && (threads * 8) << clog < vecs) clog += 1;
