@@ -9,6 +9,7 @@
 #include "tl_spans.h"
 
 #include <cmath>
+#include <type_traits>
 
 #include "../../include/tl_dropout.h"
 
@@ -95,42 +96,45 @@ template <> struct Eight<float> {
 };
 
 // Whole blocks, one to a thread and access, NB of them under way per thread.  FLAT: rows without gaps are
-// one row; else a row has `chunks` blocks.
-template <typename T, bool RES, bool FLAT, int NB, int TB>
+// one row; else a row has `chunks` blocks.  DRAW: numbers are drawn, else all of them are 0.
+template <typename T, bool RES, bool FLAT, bool DRAW, int NB, int TB>
 __global__ void __launch_bounds__(TB) k_dropout(const DropoutArgs a, const int64_t blocks, const int64_t chunks) {
-    Eight<T> x[NB], res[RES ? NB : 1];
-    int64_t at[NB] = {};   // the row
     const int64_t first = int64_t(blockIdx.x) * (NB * TB) + threadIdx.x;
     const Philox draw(a);
-    auto element = [&](int i, int64_t ld) {
-        const int64_t b = first + i * TB;
-        return FLAT ? b * 8 : at[i] * ld + (b - at[i] * chunks) * 8;
-    };
+    auto some = [&](auto whole) {   // whole: every thread has NB blocks
+        Eight<T> x[NB], res[RES ? NB : 1];
+        int64_t at[NB] = {};   // the row
+        auto element = [&](int i, int64_t ld) {
+            const int64_t b = first + i * TB;
+            return FLAT ? first * 8 + i * TB * 8 : at[i] * ld + (b - at[i] * chunks) * 8;
+        };
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-        const int64_t b = first + i * TB;
-        if (!FLAT) at[i] = (b >> 32) == 0 && (chunks >> 32) == 0 ? int64_t(uint32_t(b) / uint32_t(chunks)) : b / chunks;
-        if (b < blocks) {
-            x[i].load(static_cast<const T*>(a.x) + element(i, a.ldx));
-            if (RES) res[i].load(static_cast<const T*>(a.residual) + element(i, a.ldr));
+        for (int i = 0; i < NB; ++i) {
+            const int64_t b = first + i * TB;
+            if (!FLAT) at[i] = (b >> 32) == 0 && (chunks >> 32) == 0 ? int64_t(uint32_t(b) / uint32_t(chunks)) : b / chunks;
+            if (decltype(whole)::value || b < blocks) {
+                x[i].load(static_cast<const T*>(a.x) + element(i, a.ldx));
+                if (RES) res[i].load(static_cast<const T*>(a.residual) + element(i, a.ldr));
+            }
         }
-    }
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-        const int64_t b = first + i * TB;
-        if (b >= blocks) break;
-        const uint4 bits = a.random ? draw(uint64_t(b)) : make_uint4(0, 0, 0, 0);
-        float f[8], g[8];
-        x[i].wide(f);
-        if (RES) res[i].wide(g);
+        for (int i = 0; i < NB; ++i) {
+            const int64_t b = first + i * TB;
+            if (!decltype(whole)::value && b >= blocks) break;
+            const uint4 bits = DRAW ? draw(uint64_t(b)) : make_uint4(0, 0, 0, 0);
+            float f[8], g[8];
+            x[i].wide(f);
+            if (RES) res[i].wide(g);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = dropped(f[j], kept(word_of(bits, j >> 1), j, a.limit), a.scale, RES ? g[j] : 0.0f);
-        Eight<T>::store(static_cast<T*>(a.y) + element(i, a.ldy), f);
-    }
+            for (int j = 0; j < 8; ++j) f[j] = dropped(f[j], kept(word_of(bits, j >> 1), j, a.limit), a.scale, RES ? g[j] : 0.0f);
+            Eight<T>::store(static_cast<T*>(a.y) + element(i, a.ldy), f);
+        }
+    };
+    if ((int64_t(blockIdx.x) + 1) * (NB * TB) <= blocks) some(std::true_type{}); else some(std::false_type{});
     // the elements behind the last whole block (of the one row)
     const int64_t n = blocks * 8 + threadIdx.x;
     if (FLAT && blockIdx.x == 0 && n < a.cols) {
-        const uint4 bits = a.random ? draw(uint64_t(blocks)) : make_uint4(0, 0, 0, 0);
+        const uint4 bits = DRAW ? draw(uint64_t(blocks)) : make_uint4(0, 0, 0, 0);
         const float r = RES ? to_f(static_cast<const T*>(a.residual)[n]) : 0.0f;
         const bool keep = kept(word_of(bits, int(threadIdx.x) >> 1), int(threadIdx.x), a.limit);
         static_cast<T*>(a.y)[n] = from_f<T>(dropped(to_f(static_cast<const T*>(a.x)[n]), keep, a.scale, r));
@@ -192,11 +196,13 @@ cudaError_t launch(DropoutArgs a, cudaStream_t s) {
     if (a.rows > 1) whole = whole && a.cols % 8 == 0 && a.ldx % 8 == 0 && a.ldy % 8 == 0 && (!RES || a.ldr % 8 == 0);
     const int64_t per = whole ? int64_t(NB) * TB * 8 : int64_t(TB) * 8, ctas = (numel + per - 1) / per;
     if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
-    if (whole && a.rows == 1)
-        k_dropout<T, RES, true, NB, TB><<<unsigned(ctas), TB, 0, s>>>(a, numel / 8, 0);
-    else if (whole)
-        k_dropout<T, RES, false, NB, TB><<<unsigned(ctas), TB, 0, s>>>(a, numel / 8, a.cols / 8);
-    else
+    if (whole && a.rows == 1) {
+        auto* kernel = a.random ? k_dropout<T, RES, true, true, NB, TB> : k_dropout<T, RES, true, false, NB, TB>;
+        kernel<<<unsigned(ctas), TB, 0, s>>>(a, numel / 8, 0);
+    } else if (whole) {
+        auto* kernel = a.random ? k_dropout<T, RES, false, true, NB, TB> : k_dropout<T, RES, false, false, NB, TB>;
+        kernel<<<unsigned(ctas), TB, 0, s>>>(a, numel / 8, a.cols / 8);
+    } else
         k_dropout_any<T, RES, TB><<<unsigned(ctas), TB, 0, s>>>(a, numel);
     return cudaGetLastError();
 }
