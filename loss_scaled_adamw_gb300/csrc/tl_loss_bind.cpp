@@ -199,13 +199,13 @@ int token_stats(PyObject* const* a) {
     p.saved = saved_of(a[7], x.rows, device);
     if (a[8] != Py_None || a[9] != Py_None) {   // one without the other is refused
         const Matrix ids = matrix(a[8], device, "top_ids"), t = matrix(a[9], device, "top_logp");
-        if (t.rows != x.rows || ids.rows != x.rows || ids.cols != t.cols || ids.ld != t.ld)
+        if (t.rows != x.rows || ids.rows != x.rows || ids.cols != t.cols || (t.rows > 1 && ids.ld != t.ld))
             refuse("top_ids and top_logp", "[rows, k] with one row stride");
         if (t.type != at::kFloat) refuse("top_logp", "float32");
         if (t.cols > INT32_MAX) refuse("k", "below 2^31");
         p.top_id = ids.data;
         p.top_logp = static_cast<float*>(t.data);
-        p.ld_top = t.ld;
+        p.ld_top = t.rows > 1 ? t.ld : t.cols;
         p.k = static_cast<int32_t>(t.cols);
         p.id_bytes = ids.type == at::kInt ? 4 : ids.type == at::kLong ? 8 : -1;
     }

@@ -110,7 +110,7 @@ struct TokenGradArgs {
 // (asking the runtime for it costs more than a small launch).  A group waits for
 // nothing outside itself, so this sizes the grid and no more.
 struct GroupCache {
-    static constexpr int kEntries = 64;
+    static constexpr int kEntries = 128;
     struct Entry {
         const void* kernel;
         int threads, cluster, smem, groups;

@@ -355,8 +355,9 @@ def test_gradient_against_differences(lctx):
 
 # ------------------------------------------------------------------ streams, graphs, repetition
 
-def test_repeats_bit_for_bit_on_other_streams(lctx):
-    x, y = make(700, 5003, "bf16", 8)
+@pytest.mark.parametrize("T,V", [(700, 5003), (900, 1000), (400, 33001), (3, 60000)])
+def test_repeats_bit_for_bit_on_other_streams(lctx, T, V):
+    x, y = make(T, V, "bf16", 8)
     _, first = run(lctx, x, y, 33)
     side = torch.cuda.Stream()
     for stream in (side, torch.cuda.current_stream(), side):
@@ -406,3 +407,68 @@ def test_captured_pass_with_new_inputs(lctx):
         for a, b in zip(replayed, (d, dd, result)):
             assert torch.equal(a, b)
         assert float(result[1]) >= 0 and float(result[3]) == n
+
+
+def test_two_streams_at_once(lctx):
+    """Calls that overlap share nothing: two streams, one context each, eight calls in turns."""
+    other = tl.tl_loss_create(20000)
+    cases = [(make(500, 20001, "bf16", i), ctx, torch.cuda.Stream()) for i, ctx in enumerate((lctx, other))]
+    want, outs = [R.stats(x[:6], y[:6], 30) for (x, y), _, _ in cases], []
+    held = [(x.cuda(), y.cuda()) for (x, y), _, _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for (xd, yd), (_, ctx, stream) in zip(held, cases):
+            with torch.cuda.stream(stream):
+                ids, top = torch.empty(500, 30, dtype=torch.int32, device="cuda"), torch.empty(500, 30, device="cuda")
+                e, saved, lp = torch.empty(500, device="cuda"), torch.empty(500, 3, device="cuda"), torch.empty(500, device="cuda")
+                tl.tl_token_stats(ctx, xd, yd, logp=lp, entropy=e, saved=saved, top_ids=ids, top_logp=top)
+                outs.append((lp, e, saved, ids, top))
+    torch.cuda.synchronize()
+    for i, (lp, e, saved, ids, top) in enumerate(outs):
+        compare({"logp": lp[:6].cpu(), "entropy": e[:6].cpu(), "saved": saved[:6].cpu(), "ids": ids[:6].cpu().long(),
+                 "top": top[:6].cpu()}, want[i % 2])
+        for a, b in zip(outs[i], outs[i % 2]):
+            assert torch.equal(torch.nan_to_num(a), torch.nan_to_num(b))
+
+
+def test_offsets_beyond_32_bits(lctx):
+    """Rows 2^29 elements apart: the last starts at element 2^32."""
+    T, V, ld = 9, 20000, 1 << 29
+    free, _ = torch.cuda.mem_get_info()
+    if free < 2 * (T * ld) + (1 << 30):
+        pytest.skip("not enough memory")
+    buf = torch.empty((T - 1) * ld + V, dtype=torch.bfloat16, device="cuda")
+    X = torch.as_strided(buf, (T, V), (ld, 1))
+    x, y = make(T, V, "bf16", 19, masked=0.0)
+    X.copy_(x)
+    ids, top = torch.zeros(T, 9, dtype=torch.int64, device="cuda"), torch.zeros(T, 9, device="cuda")
+    e, saved = torch.zeros(T, device="cuda"), torch.zeros(T, 3, device="cuda")
+    tl.tl_token_stats(lctx, X, entropy=e, saved=saved, top_ids=ids, top_logp=top)
+    want = R.stats(x, None, 9)
+    compare({"entropy": e.cpu(), "saved": saved.cpu(), "ids": ids.cpu(), "top": top.cpu()}, want)
+    ga = torch.ones(T, device="cuda")
+    tl.tl_token_grad(lctx, X, saved, X, targets=y.cuda(), grad_logp=ga)
+    d = R.grad(x, y, torch.ones(T))
+    assert ((X.cpu().double() - d).abs() <= d.abs() * 2.0 ** -8 * 1.01 + 1e-4).all()
+
+
+@pytest.mark.parametrize("rows", [1, 200])
+@pytest.mark.parametrize("V", [900, 20000, 40000])
+def test_nearly_constant_fp32_rows(lctx, rows, V):
+    """Thousands of entries within a few last places of each other: their order is still exact."""
+    g = torch.Generator().manual_seed(V)
+    base = (torch.full((3, V), 1000.0).view(torch.int32) + torch.randint(0, 40, (3, V), generator=g).int()).view(torch.float32)
+    base[1] = -base[1]
+    x = base[torch.arange(rows) % 3]
+    _, got = run(lctx, x, None, 50)
+    compare(got, {n: v[torch.arange(rows) % 3] for n, v in R.stats(base, None, 50).items()})
+
+
+def test_one_row_into_wider_buffers(lctx):
+    x, y = make(1, 3000, "bf16", 3)
+    ids, top = torch.full((4, 20), 7, dtype=torch.int32, device="cuda"), torch.full((4, 9), 7.0, device="cuda")
+    tl.tl_token_stats(lctx, x.cuda(), top_ids=ids[1:2, :5], top_logp=top[2:3, :5])
+    want = R.stats(x, None, 5)
+    assert torch.equal(ids[1, :5].cpu().long(), want["ids"][0]) and (ids[1, 5:] == 7).all() and (ids[[0, 2, 3]] == 7).all()
+    close(top[2:3, :5].cpu(), want["top"], REL + 4 * EPS * want["top"].abs(), "top")
+    assert (top[2, 5:] == 7).all() and (top[[0, 1, 3]] == 7).all()
