@@ -378,9 +378,22 @@ __device__ __forceinline__ int warp_before(int n, int& all) {   // the sum over 
 // numbers, `bins` 256.  (A bitonic network over 85 candidates took a warp 5,000 to 9,000 cycles beside
 // busy ones, every pair counted as much.)
 constexpr int kBins = 256;
+// Up to so many are counted pair by pair: 16,384 x 1,000 bf16 with 8 alternatives (11 candidates) 29.8 us counted, 31.9 in bins,
+// with 32 (40) 43.1 / 40.0; 4,096 x 8,192 with 8 31.4 / 34.8.
+constexpr int kCounted = 24;
 template <typename T, int SB, typename F>
 __device__ __forceinline__ void place_candidates(const unsigned long long* found, int n, uint32_t lo, float M, int k, int* bins,
                                                  uint16_t* order, int tid, int bar, F settle) {
+    if (n <= kCounted) {   // few: counted, without a barrier
+        for (int i = tid; i < n; i += SB) {
+            const unsigned long long c = found[i];
+            int place = 0;
+#pragma unroll 4
+            for (int j = 0; j < n; ++j) place += found[j] > c;
+            if (place < k) settle(c, place);
+        }
+        return;
+    }
     const uint32_t top = rank_of<T>(M), range = top - lo;
     const int shift = range < kBins ? 0 : 32 - 8 - __clz(range);
     auto bin_of = [&](unsigned long long c) { return (top - (uint32_t(c >> 32) >> Order<T>::kShift)) >> shift; };
@@ -703,18 +716,12 @@ struct Stage {
     uint4* raw;
     int *id, *count;   // of a vector's first element
 };
-// Places for the n of each lane of a warp, behind those that *count has already.
-__device__ __forceinline__ int warp_places(int n, int* count) {
-    int all;
-    const int before = warp_before(n, all);
-    int first = 0;
-    if ((threadIdx.x & 31) == 0 && all > 0) first = atomicAdd(count, all);
-    return __shfl_sync(~0u, first, 0) + before;
-}
+// Places for a thread's n, behind those that *count has already.
+__device__ __forceinline__ int places_for(int n, int* count) { return n > 0 ? atomicAdd(count, n) : 0; }
 // A thread's vectors `pass` (a bit each), of the first element's id id(i).
 template <int NV, typename Id>
 __device__ __forceinline__ void stage_vectors(const uint4 (&raw)[NV], unsigned pass, Id id, const Stage& st) {
-    int to = warp_places(__popc(pass), st.count);
+    int to = places_for(__popc(pass), st.count);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
         if (pass >> i & 1) {
@@ -738,7 +745,7 @@ __device__ __forceinline__ void offer_staged(const Stage& st, int m, float least
 #pragma unroll
             for (int j = 0; j < N; ++j) some |= f[j] >= least ? 1u << j : 0u;
         }
-        int to = warp_places(__popc(some), nfound);
+        int to = places_for(__popc(some), nfound);
         for (; some != 0 && to < CAP; some &= some - 1) {
             const int j = __ffs(some) - 1;
             found[to++] = candidate(order_of(to_f(reinterpret_cast<const T*>(st.raw + i)[j])), id + j);
@@ -985,17 +992,20 @@ cudaError_t top_launch(const StatsArgs& a, int sms, GroupCache& cache, cudaStrea
 // Short rows, held in registers
 // ---------------------------------------------------------------------------
 
-// A warp per row (W = 1, four rows to a CTA) or a CTA of W warps, NV vectors per thread.  The row is
-// read once; the entries are chosen where it is.
+// A team of W warps per row, four warps to a CTA or (W = 8) eight, NV vectors per thread.  The row is read
+// once; the entries are chosen where it is.
 template <typename T, int W, int NV, bool TOP>
 __global__ void __launch_bounds__(W > 4 ? 32 * W : 128, W > 4 ? 2 : NV > 8 ? (TOP ? 3 : 4) : NV > 4 ? (TOP ? 5 : 6) : TOP ? 7 : 8) k_held(const StatsArgs a) {
-    constexpr int N = Vec<T>::N, SB = 32 * W, TEAMS = W == 1 ? 4 : 1, CAP = W == 1 ? 512 : kCandidates;
-    __shared__ float4 wparts[W == 1 ? 1 : 2][W];
-    __shared__ float2 wtops[W == 1 ? 1 : 2][W];
-    __shared__ int counts[2][8], nfound[TEAMS], nstage[TEAMS];
+    constexpr int N = Vec<T>::N, SB = 32 * W, TEAMS = W < 4 ? 4 / W : 1, CAP = W == 1 ? 512 : kCandidates;
+    __shared__ float4 wparts_of[TEAMS][2][W];   // by row parity
+    __shared__ float2 wtops_of[TEAMS][2][W];
+    __shared__ int counts_of[TEAMS][2][8], nfound[TEAMS], nstage[TEAMS];
     __shared__ __align__(16) int bins[TOP ? TEAMS : 1][kBins];
     extern __shared__ __align__(128) uint4 ring[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, team = warp / W, tid = threadIdx.x % SB;
+    const int lane = threadIdx.x & 31, team = threadIdx.x / SB, tid = threadIdx.x % SB, warp = tid >> 5, bar = 1 + team;
+    float4(*const wparts)[W] = wparts_of[team];
+    float2(*const wtops)[W] = wtops_of[team];
+    int(*const counts)[8] = counts_of[team];
     // per team: the staged vectors and their ids, and the candidates
     const Stage stage{ring + team * (SB * NV), reinterpret_cast<int*>(ring + TEAMS * SB * NV) + team * (SB * NV), &nstage[team]};
     unsigned long long* const found = reinterpret_cast<unsigned long long*>(reinterpret_cast<int*>(ring + TEAMS * SB * NV) + TEAMS * SB * NV) + team * CAP;
@@ -1035,8 +1045,8 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128, W > 4 ? 2 : NV > 8 ? (TO
         if (TOP) low = -warp_max(-low);
         if (W > 1) {
             if (lane == 0) wtops[par][warp] = make_float2(M, low);
-            if (TOP && tid == 0) nfound[0] = nstage[0] = 0;
-            __syncthreads();
+            if (TOP && tid == 0) nfound[team] = nstage[team] = 0;
+            sync<SB>(bar);
 #pragma unroll
             for (int i = 0; i < W; ++i) {
                 M = fmaxf(M, wtops[par][i].x);
@@ -1058,17 +1068,17 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128, W > 4 ? 2 : NV > 8 ? (TO
         RowSums sums{M, warp_sum(sum.s), warp_sum(sum.w), kNegInf};
         if (W > 1) {
             if (lane == 0) wparts[par][warp] = make_float4(0.0f, sums.S, sums.W, 0.0f);
-            __syncthreads();
+            sync<SB>(bar);
             sums.S = sums.W = 0.0f;
 #pragma unroll
-            for (int i = 0; i < W; i += 4) {
-                sums.S += (wparts[par][i].y + wparts[par][i + 1].y) + (wparts[par][i + 2].y + wparts[par][i + 3].y);
-                sums.W += (wparts[par][i].z + wparts[par][i + 1].z) + (wparts[par][i + 2].z + wparts[par][i + 3].z);
+            for (int i = 0; i < W; i += 2) {
+                sums.S += wparts[par][i].y + wparts[par][i + 1].y;
+                sums.W += wparts[par][i].z + wparts[par][i + 1].z;
             }
             par ^= 1;
         }
         const RowSoftmax row(sums, a, sizeof(T) == 4);
-        const bool finishes = W == 1 || warp == 0;
+        const bool finishes = warp == 0;
         if (!TOP || row.none) {
             if (finishes) row.finish(a, r, y, xy);
             if (TOP)
@@ -1082,7 +1092,7 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128, W > 4 ? 2 : NV > 8 ? (TO
                 int c = 0;
 #pragma unroll
                 for (int i = 0; i < NV; ++i) c += tops[i] >= v;
-                return sum_over<SB>(c, counts, turn, tid, 1);
+                return sum_over<SB>(c, counts, turn, tid, bar);
             };
             const bool full = low > kNegInf;
             if (full) lo = rank_of<T>(low);
@@ -1098,7 +1108,7 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128, W > 4 ? 2 : NV > 8 ? (TO
 #pragma unroll
                     for (int j = 0; j < N; ++j) c += f[j] >= v;
                 }
-                return sum_over<SB>(c, counts, turn, tid, 1);
+                return sum_over<SB>(c, counts, turn, tid, bar);
             };
             const int from = count(logit_of(lo << Order<T>::kShift));
             if (from > a.k) lo = search_rank<T>(lo, from, M, a.k, count);
@@ -1109,12 +1119,12 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128, W > 4 ? 2 : NV > 8 ? (TO
 #pragma unroll
         for (int i = 0; i < NV; ++i) pass |= tops[i] >= least ? 1u << i : 0u;
         stage_vectors<NV>(raw, pass, [&](int i) { return pl.head + (i * SB + tid - pl.off) * N; }, stage);
-        sync<SB>(1);
+        sync<SB>(bar);
         offer_staged<T, SB, CAP>(stage, nstage[team], least, found, &nfound[team], tid);
-        sync<SB>(1);
+        sync<SB>(bar);
         int n = nfound[team];
-        if (n > CAP) n = exact_candidates<T, SB>(x, a.vocab, a.k, lo, M, found, &nfound[team], counts, turn, tid, 1);
-        place_candidates<T, SB>(found, n, lo, M, a.k, bins[team], reinterpret_cast<uint16_t*>(stage.raw), tid, 1, [&](unsigned long long c, int place) {
+        if (n > CAP) n = exact_candidates<T, SB>(x, a.vocab, a.k, lo, M, found, &nfound[team], counts, turn, tid, bar);
+        place_candidates<T, SB>(found, n, lo, M, a.k, bins[team], reinterpret_cast<uint16_t*>(stage.raw), tid, bar, [&](unsigned long long c, int place) {
             put_entry(a, r, place, int(~uint32_t(c)), row.share(logit_of(uint32_t(c >> 32))));
         });
         for (int i = n + tid; i < a.k; i += SB) put_entry(a, r, i, -1, kNegInf);
@@ -1128,9 +1138,9 @@ cudaError_t held_launch(const StatsArgs& a, int sms, GroupCache& cache, cudaStre
     auto* kernel = k_held<T, W, NV, TOP>;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(1);
-    constexpr int threads = W > 4 ? 32 * W : 128, rows = W == 1 ? 4 : 1;
+    constexpr int threads = W > 4 ? 32 * W : 128, rows = W < 4 ? 4 / W : 1;
     cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = TOP ? size_t(8) * (W == 1 ? 4 * 512 : kCandidates) + size_t(20) * NV * threads : 0;
+    cfg.dynamicSmemBytes = TOP ? size_t(8) * rows * (W == 1 ? 512 : kCandidates) + size_t(20) * NV * threads : 0;
     cfg.stream = s;
     int groups = 0;
     cudaError_t e = resident_groups(reinterpret_cast<const void*>(kernel), cfg, RowShape{threads, 0}, sms, cache, groups);
@@ -1139,11 +1149,15 @@ cudaError_t held_launch(const StatsArgs& a, int sms, GroupCache& cache, cudaStre
     cfg.gridDim.x = unsigned(groups < want ? groups : want);
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
+// As few warps to a row as hold it with 16 vectors per thread where there are rows for all of them, else more with
+// fewer vectors.  us, bf16, one warp with 16 vectors / four with 4: 16,384 x 2,001 with 8 alternatives 54 / 82, without 26 / 38,
+// 1,000 x 3,001 with 8 6.4 / 7.4, 300 x 3,001 5.8 / 5.1 (two warps with 8: 70, 33 and 6.8 of the first three); two warps with 16 /
+// four with 8: 16,384 x 8,192 with 8 109 / 118, with 64 143 / 151, 1,000 x 8,192 with 8 11.0 / 10.7.
 template <typename T, bool TOP> cudaError_t held(const StatsArgs& a, int places, int sms, GroupCache& cache, cudaStream_t s) {
     if (places <= 128) return held_launch<T, 1, 4, TOP>(a, sms, cache, s);
     if (places <= 256) return held_launch<T, 1, 8, TOP>(a, sms, cache, s);
-    if (places <= 512) return held_launch<T, 4, 4, TOP>(a, sms, cache, s);
-    if (places <= 1024) return held_launch<T, 4, 8, TOP>(a, sms, cache, s);
+    if (places <= 512) return a.rows > 4 * sms ? held_launch<T, 1, 16, TOP>(a, sms, cache, s) : held_launch<T, 4, 4, TOP>(a, sms, cache, s);
+    if (places <= 1024) return a.rows > 8 * sms ? held_launch<T, 2, 16, TOP>(a, sms, cache, s) : held_launch<T, 4, 8, TOP>(a, sms, cache, s);
     if (places <= 2048) return held_launch<T, 4, 16, TOP>(a, sms, cache, s);
     return held_launch<T, 8, 16, TOP>(a, sms, cache, s);
 }
@@ -1411,7 +1425,7 @@ cudaError_t stats(const StatsArgs& a, int sms, GroupCache& cache, cudaStream_t s
     const uintptr_t body = (reinterpret_cast<uintptr_t>(a.x) + 15) / 16;
     const int places = vecs + ((a.ld * int64_t(sizeof(T))) % 128 == 0 ? int(body & 7) : 7);
     // In registers up to 2,048 vectors, and up to 4,096 for rows that get a CTA each at once: us in registers / as below,
-    // bf16: 16,384 x 8,192 with 64 alternatives 152 / 283, 4,096 x 12,000 with 8 62 / 75, without 26 / 27, 4,096 x 17,000 with
+    // bf16: 16,384 x 8,192 with 64 alternatives 143 / 283, 4,096 x 12,000 with 8 62 / 75, without 26 / 27, 4,096 x 17,000 with
     // 8 104 / 84, without 49 / 34; 304 x 24,000 with 20 9.7 / 11.1, 600 x 24,000 with 20 18.2 / 15.0, 1 x 30,000 with 20
     // 7.1 / 9.0.
     if (places <= (a.rows <= 2 * sms ? 4096 : 2048)) return a.k > 0 ? held<T, true>(a, places, sms, cache, s) : held<T, false>(a, places, sms, cache, s);
