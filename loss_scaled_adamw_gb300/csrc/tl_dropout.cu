@@ -65,10 +65,10 @@ __device__ __forceinline__ float dropped(float x, bool keep, float scale, float 
     return keep ? __fmaf_rn(x, scale, residual) : residual;
 }
 
-// Threads per CTA, and blocks of eight elements under way per thread.  us for 268M bf16 elements without a
-// residual with 1 / 2 / 4 / 8 blocks and 256 threads: 203 / 181 / 173 / 169, with 4 and 128 threads 170; with a
-// residual 225 for all of 1 to 4; 8.4M elements with a residual 7.9 / 7.4 / 7.7 with 1 / 2 / 4, 7.3 with 2 and
-// 128 threads, without one 7.3 / 7.2 / 8.0 with 2 / 4 / 8, 7.1 with 4 and 128.
+// Threads per CTA, and blocks of eight elements under way per thread.  us for 268M bf16 elements without a residual
+// with 2 / 4 / 8 blocks and 128 threads: 160 / 152 / 186, with 4 and 256 threads 153; with a residual 224 with 1, 2 or 4;
+// 8.4M elements with a residual 7.6 / 6.5 / 6.4 with 1 / 2 / 4, without one 6.4 / 6.1 / 7.1 with 2 / 4 / 8.  What bounds it: memory
+// (152 us are 104 % of the copy rate, and 119 instructions for a thread's eight elements fill 70 % of the issue slots).
 constexpr int kDropThreads = 128;
 template <bool RES> constexpr int kBlocks = RES ? 2 : 4;
 
