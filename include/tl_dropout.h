@@ -26,7 +26,8 @@
  * element t * ld; any ld >= cols and any element-aligned address is accepted.
  * Where rows begin on 16-byte boundaries (fp32: 32-byte ones) and hold whole blocks
  * of 8 elements, or follow one another without gaps from such a boundary on,
- * accesses are vectors; others are by elements.  y may be x's or the residual's own memory (same address
+ * accesses are vectors, and so they are for long 16-bit rows at one phase (address
+ * modulo 16) in all operands; others are by elements.  y may be x's or the residual's own memory (same address
  * and ld).  Any other overlap of y with an argument is an error.
  *
  * The call is asynchronous on the given stream, keeps no state and no scratch, and

@@ -45,9 +45,9 @@ def check(got, x, p, seed, ticket, site, res=None):
         assert torch.equal((got != 0) & (x != 0), keep & (x != 0))
 
 
-CASES = [(1, 1, 0, 0), (1, 7, 0, 0), (1, 8, 0, 0), (1, 2048, 0, 0), (1, 4099, 0, 0), (1, 4099, 0, 3), (3, 5, 0, 0), (3, 5, 2, 1),
+CASES = [(1, 1, 0, 0), (1, 7, 0, 0), (1, 8, 0, 0), (1, 2048, 0, 0), (1, 4099, 0, 0), (1, 4099, 0, 3), (1, 20001, 0, 5), (3, 5, 0, 0), (3, 5, 2, 1),
          (17, 64, 0, 0), (17, 64, 8, 0), (17, 64, 8, 1), (17, 64, 3, 0), (33, 1153, 6, 3), (9, 8192, 64, 8), (40, 288, 0, 0),
-         (1000, 129, 0, 0), (300, 2048, 0, 0), (70, 16392, 16, 0), (500, 3, 1, 0), (257, 1, 1, 0), (5, 2051, 5, 4)]
+         (1000, 129, 0, 0), (300, 2048, 0, 0), (70, 16392, 16, 0), (23, 8192, 7, 3), (11, 4097, 6, 5), (40, 700, 3, 0), (9, 1031, 2, 7), (13, 513, 0, 0), (6, 2049, 1, 6), (500, 3, 1, 0), (257, 1, 1, 0), (5, 2051, 5, 4)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
