@@ -166,7 +166,8 @@ int tl_create(tl_ctx** out, int64_t ntensors, const int64_t* numel, void* const*
               float* const* master, float* const* m, float* const* v, float* const* acc,
               const tl_config* cfg, tl_stream stream);
 
-/* Release the context (waits for the device first).  NULL is accepted. */
+/* Release the context (waits for the device first, so not while a stream of it is
+ * being captured: CUDA ends the capture then).  NULL is accepted. */
 int tl_destroy(tl_ctx* ctx);
 
 /* Accumulate micro-batch i into the fp32 buffer (step a2).

@@ -105,7 +105,8 @@ typedef struct {
  * 0 <= max_pairs <= 2^28), TL_ENOMEM, TL_ECUDA. */
 int tl_loss_create(tl_loss_ctx** out, int64_t max_rows, int64_t max_pairs, tl_stream stream);
 
-/* Release it (waits for the device first).  NULL is accepted. */
+/* Release it (waits for the device first, so not while a stream of it is being
+ * captured).  NULL is accepted. */
 int tl_loss_destroy(tl_loss_ctx* ctx);
 
 /* logp[t] = z_t[target[t]] - log sum_j exp(z_t[j]); 0 for ignored rows.

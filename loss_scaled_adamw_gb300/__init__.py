@@ -21,6 +21,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 from typing import Sequence
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -184,8 +185,28 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+# Contexts that were dropped and not destroyed: (destroy function, handle).  A finaliser runs whenever the
+# garbage collector does, in any thread, so also while a stream is being captured, where waiting for the device or
+# freeing its memory would end the capture.  It leaves the handle here; the calls that allocate and wait for
+# the device themselves (create, destroy) release what has gathered.
+_dropped = []
+
+
+def _release_dropped():
+    while True:
+        try:
+            destroy, handle = _dropped.pop()
+        except IndexError:
+            return
+        destroy(handle)
+
+
 class Context:
-    """Owns one tl_ctx and the tensor lists it was created over."""
+    """Owns one tl_ctx and the tensor lists it was created over.
+
+    tl_destroy waits for the device and releases the scratch.  Of a context that is dropped without it the scratch is
+    released by the next create or destroy of a context, and the tensors at once, by torch's rules: where the last
+    calls ran on another stream than the tensors', destroy the context first."""
 
     def __init__(self, handle: ctypes.c_void_p, keep):
         self.handle = handle
@@ -193,8 +214,8 @@ class Context:
         self.lr_table = None  # the learning-rate schedule tensor while one is set
 
     def __del__(self):
-        if getattr(self, "handle", None) and _lib is not None:
-            _lib.tl_destroy(self.handle)
+        if getattr(self, "handle", None) and _lib is not None and not sys.is_finalizing():
+            _dropped.append((_lib.tl_destroy, self.handle))
             self.handle = None
 
 
@@ -209,6 +230,7 @@ def _check(ctx, fn: str, rc: int):
 
 def tl_create(numel: Sequence[int], params, masters, ms, vs, accs, cfg: tl_config, stream=None) -> Context:
     lib = load_library()
+    _release_dropped()
     n = len(numel)
     lists = [p if isinstance(p, PtrList) else PtrList(p) for p in (params, masters, ms, vs, accs)]
     for lst in lists:
@@ -227,6 +249,7 @@ def tl_destroy(ctx: Context) -> None:
     if ctx.handle:
         rc = load_library().tl_destroy(ctx.handle)
         ctx.handle = None
+        _release_dropped()
         if rc != TL_OK:
             raise TLError("tl_destroy", rc)
 

@@ -18,10 +18,11 @@ until it has run.
 from __future__ import annotations
 
 import ctypes
+import sys
 
 import torch
 
-from . import TL_OK, TLError, load_library
+from . import TL_OK, TLError, _dropped, _release_dropped, load_library
 from . import _stream as _any_stream
 
 LOSS_EXPORTED = ("tl_loss_create", "tl_loss_destroy", "tl_token_logprob", "tl_policy_loss", "tl_preference_loss",
@@ -110,7 +111,8 @@ def _load():
 
 
 class LossContext:
-    """Owns one tl_loss_ctx (its scratch lives on the device that was current at creation)."""
+    """Owns one tl_loss_ctx (its scratch lives on the device that was current at creation).  Dropped without
+    tl_loss_destroy, its scratch is released by the next create or destroy of a context."""
 
     def __init__(self, handle, device: int):
         self.handle = handle
@@ -121,8 +123,8 @@ class LossContext:
         return self.handle.value if self.handle else None
 
     def __del__(self):
-        if getattr(self, "handle", None) and _lib is not None:
-            _lib.tl_loss_destroy(self.handle)
+        if getattr(self, "handle", None) and _lib is not None and not sys.is_finalizing():
+            _dropped.append((_lib.tl_loss_destroy, self.handle))
             self.handle = None
 
 
@@ -135,6 +137,7 @@ def _check(lctx, fn: str, rc: int):
 def tl_loss_create(max_rows: int, max_pairs: int = 0, stream=None) -> LossContext:
     """A context for calls of at most max_rows rows and max_pairs preference pairs."""
     lib = _load()
+    _release_dropped()
     h = _vp()
     rc = lib.tl_loss_create(ctypes.byref(h), int(max_rows), int(max_pairs), _any_stream(stream))
     if rc != TL_OK:
@@ -146,6 +149,7 @@ def tl_loss_destroy(lctx: LossContext) -> None:
     if lctx.handle:
         rc = _load().tl_loss_destroy(lctx.handle)
         lctx.handle = None
+        _release_dropped()
         if rc != TL_OK:
             raise TLError("tl_loss_destroy", rc)
 
