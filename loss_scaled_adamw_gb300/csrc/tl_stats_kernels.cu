@@ -1053,8 +1053,9 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128, W > 4 ? 2 : NV > 8 ? (TO
         if (TOP) low = -warp_max(-low);
         if (W > 1) {
             if (lane == 0) wtops[par][warp] = make_float2(M, low);
-            if (TOP && tid == 0) nfound[team] = nstage[team] = 0;
             sync<SB>(bar);
+            // behind this barrier every warp has read the last row's count; the one of wparts comes before its use
+            if (TOP && tid == 0) nfound[team] = nstage[team] = 0;
 #pragma unroll
             for (int i = 0; i < W; ++i) {
                 M = fmaxf(M, wtops[par][i].x);
@@ -1137,7 +1138,7 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128, W > 4 ? 2 : NV > 8 ? (TO
         });
         for (int i = n + tid; i < a.k; i += SB) put_entry(a, r, i, -1, kNegInf);
         if (finishes) row.finish(a, r, y, xy);
-        if (W == 1) __syncwarp();   // before the next row's candidates; with more warps its barriers come first
+        if (W == 1) __syncwarp();   // before the next row's counts; with more warps its first barrier comes before them
     }
 }
 
