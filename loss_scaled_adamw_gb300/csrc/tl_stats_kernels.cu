@@ -90,10 +90,10 @@ template <typename T> struct Running {
     float u = 0.0f;      // the reference's whole number
     bool slow = false;   // element by element, see below
 
-    // Vectors with an excluded entry (-inf) are summed again, their 16-bit logits held above this one before
-    // they are widened (32-bit ones: their exponents).  That needs the lowest to be far below the
-    // reference, 2^-150 of it.
-    static constexpr float kFloor = sizeof(T) == 4 ? kNegInf : Vec<T>::kEmpty == 0xfc00fc00u ? -65504.0f : -9.9e29f;
+    // Vectors with an excluded entry (-inf) are summed again, their logits held above this one (16-bit ones before
+    // they are widened; 32-bit ones' exponents are held as well).  That needs it to be far below the reference, 2^-150
+    // of it, which very large temperatures do not leave, and its exponent to be in fp32, which very small ones do not.
+    static constexpr float kFloor = sizeof(T) == 4 ? -3.4e38f : Vec<T>::kEmpty == 0xfc00fc00u ? -65504.0f : -9.9e29f;
 
     // To a much larger element.  Smaller steps are left: exponentials up to 2^32 of the reference do no harm.
     __device__ __forceinline__ void raise(float top, float c2) {
@@ -102,7 +102,7 @@ template <typename T> struct Running {
         move_sums(m, top, c2, s, w);
         m = top;
         limit = m + 32.0f / c2;
-        slow = big(m, c2) || (sizeof(T) == 2 && !((m - kFloor) * c2 > 150.0f));
+        slow = big(m, c2) || !((m - kFloor) * c2 > 150.0f) || (sizeof(T) == 2 && !(kFloor * c2 > -3.4e38f));
         u = slow ? 0.0f : anchor(m, c2);
     }
     __device__ __forceinline__ void add_one(float v, const Scale& c) {
@@ -125,7 +125,7 @@ template <typename T> struct Running {
             Vec<T>::wide(HOLD ? held(raw[i]) : raw[i], f);
             if (HOLD && sizeof(T) == 4) {   // -inf times a negative low part
 #pragma unroll
-                for (int j = 0; j < N; ++j) f[j] = max_nan(f[j], -3.4e38f);
+                for (int j = 0; j < N; ++j) f[j] = max_nan(f[j], kFloor);
             }
 #pragma unroll
             for (int j = 0; j < N; j += 2) {
