@@ -16,10 +16,16 @@ namespace {
 // Sums of a part of a row
 // ---------------------------------------------------------------------------
 
+// (x - m) / 2: it is in fp32 where x - m is not (a type's largest and lowest value in one row), and halving
+// rounds nothing above 2^-126.  Doubled scales are in fp32 too (temperatures are normal numbers).
+__device__ __forceinline__ float half_apart(float x, float m) { return __fmaf_rn(0.5f, x, -0.5f * m); }
+// (x - m) c.
+__device__ __forceinline__ float distance(float x, float m, float c) { return half_apart(x, m) * (2.0f * c); }
+
 // From exponents against a part's reference m to those against `to`: what is added.
 __device__ __forceinline__ float exponent_step(float m, float to, float c2) {
     if (!big(to, c2)) return big(m, c2) ? __fmaf_rn(m, c2, -anchor(to, c2)) : anchor(m, c2) - anchor(to, c2);
-    return (m - to) * c2 - (big(m, c2) ? 0.0f : __fmaf_rn(m, c2, -anchor(m, c2)));
+    return distance(m, to, c2) - (big(m, c2) ? 0.0f : __fmaf_rn(m, c2, -anchor(m, c2)));
 }
 // S and W of a part with reference m, against `to`.  An empty part's 0 (or NaN) stays.
 __device__ __forceinline__ void move_sums(float m, float to, float c2, float& s, float& w) {
@@ -55,10 +61,15 @@ __device__ __forceinline__ pair_t add_pair(pair_t a, pair_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-// The larger of both, NaN if v is.
+// The larger, the smaller of both, NaN if v is.
 __device__ __forceinline__ float max_nan(float v, float least) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "f"(least));
+    return r;
+}
+__device__ __forceinline__ float min_nan(float v, float most) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "f"(most));
     return r;
 }
 
@@ -108,8 +119,8 @@ template <typename T> struct Running {
     __device__ __forceinline__ void add_one(float v, const Scale& c) {
         const float ref = part_ref(m);
         const bool far = big(ref, c.c2);
-        float z = far ? (v - ref) * c.c2 : __fmaf_rn(v, c.c2, -anchor(ref, c.c2));
-        if (sizeof(T) == 4 && v > kNegInf) z = __fmaf_rn(far ? v - ref : v, c.low, z);
+        float z = far ? distance(v, ref, c.c2) : __fmaf_rn(v, c.c2, -anchor(ref, c.c2));
+        if (sizeof(T) == 4 && v > kNegInf) z = far ? __fmaf_rn(half_apart(v, ref), 2.0f * c.low, z) : __fmaf_rn(v, c.low, z);
         z = max_nan(z, kLowest);
         const float e = ex2(z);
         s += e;
@@ -487,17 +498,18 @@ struct RowSoftmax {
         log2_parts(S, n, rest);
     }
     // log q of an entry x.  Roundings of the sum are not let above 0, and an entry at a type's lowest value,
-    // whose exponent overflows, has its distance.
+    // whose exponent overflows, has its distance (-inf where that is beyond fp32 as well).
     __device__ __forceinline__ float share(float x) const {
         if (none) return __int_as_float(0x7fffffff);
         if (x == kNegInf) return kNegInf;
-        const float r = log_share(x, M, u, c2, far, n, __fmaf_rn(far ? M - x : -x, low, rest));
-        return fminf(r == kNegInf ? (x - M) * it : r, 0.0f);
+        const float below = far ? __fmaf_rn(half_apart(M, x), 2.0f * low, rest) : __fmaf_rn(-x, low, rest);
+        const float r = log_share(x, M, u, c2, far, n, fabsf(below) < INFINITY ? below : rest);
+        return min_nan(r == kNegInf ? __fmaf_rn(-(n + rest), kLn2, distance(x, M, it)) : r, 0.0f);
     }
     // By a warp; xy: the label's logit.
     __device__ __forceinline__ void finish(const StatsArgs& a, int64_t r, int64_t y, float xy) const {
         const float kNaN = __int_as_float(0x7fffffff), log_sum = -share(M), lp = share(xy);
-        const float H = fmaxf(log_sum + ((far ? 0.0f : __fmaf_rn(M, low, __fmaf_rn(M, c2, -u))) - W / S) * kLn2, 0.0f);
+        const float H = max_nan(log_sum + ((far ? 0.0f : __fmaf_rn(M, low, __fmaf_rn(M, c2, -u))) - W / S) * kLn2, 0.0f);
         if ((threadIdx.x & 31) != 0) return;
         if (a.logp) a.logp[r] = y < a.vocab ? lp : kNaN;
         if (a.entropy) a.entropy[r] = none ? kNaN : H;
@@ -1494,7 +1506,7 @@ __global__ void __launch_bounds__(TB) k_token_grad(const TokenGradArgs a, const 
     const float c2 = a.c2, kNaN = __int_as_float(0x7fffffff);
     const float M = a.saved[3 * r], H = a.saved[3 * r + 2];
     const bool far = big(M, c2);
-    const float u = far ? 0.0f : anchor(M, c2), base = far ? M : 0.0f;
+    const float u = far ? 0.0f : anchor(M, c2), base = far ? M : 0.0f;   // exponents are (v - base) c2 - u
     // log2 q_j = w_j - rest
     const float rest = __fmaf_rn(a.saved[3 * r + 1], kLog2e, far ? 0.0f : __fmaf_rn(M, c2, -u));
     const float step = (a.seed ? *a.seed : 1.0f) * a.it;
@@ -1502,7 +1514,7 @@ __global__ void __launch_bounds__(TB) k_token_grad(const TokenGradArgs a, const 
     const float scale = -step * ex2(-rest) + (y >= a.vocab ? kNaN : 0.0f);
     const float A = scale * __fmaf_rn(gb, __fmaf_rn(-rest, kLn2, H), ga), B = scale * gb * kLn2, at_label = step * ga;
     auto value = [&](float v) {
-        const float w = fmaxf(__fmaf_rn(v - base, c2, -u), kLowest);
+        const float w = fmaxf(__fmaf_rn(half_apart(v, base), 2.0f * c2, -u), kLowest);
         return ex2(w) * __fmaf_rn(w, B, A);
     };
     // the label's element: in vector yv, or at an edge
