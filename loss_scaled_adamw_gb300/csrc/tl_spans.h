@@ -41,13 +41,15 @@ inline int64_t span_bytes(int64_t rows, int64_t cols, int64_t ld, int64_t size) 
     return rows < 1 || cols < 1 ? 0 : ((rows - 1) * ld + cols) * size;
 }
 
-// Whether two row-strided matrices of one shape share an element: equal strides
-// interleave when their columns stay apart, others are held to disjoint spans.
+// Whether two row-strided matrices of one shape share an element without being the same one: equal strides
+// interleave when their columns stay apart, others are held to disjoint spans.  The stride of a single row is
+// not used (and may be anything).
 inline bool rows_clash(const void* x, int64_t ldx, const void* d, int64_t ldd, int64_t rows, int64_t cols, int64_t size) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(d);
     const uintptr_t ahi = a + uintptr_t(span_bytes(rows, cols, ldx, size));
     const uintptr_t bhi = b + uintptr_t(span_bytes(rows, cols, ldd, size));
     if (a >= bhi || b >= ahi) return false;
+    if (rows == 1) return a != b;
     if (ldx != ldd) return true;
     if (a == b) return false;   // in place
     const uintptr_t stride = uintptr_t(ldx * size), width = uintptr_t(cols * size);

@@ -1,0 +1,35 @@
+"""Arguments of dropout on the CPU, where the checks that every call makes end before the device is asked."""
+import os
+import subprocess
+import sys
+
+import pytest
+
+pytest.importorskip("torch")
+
+from loss_scaled_adamw_gb300 import _build
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def test_one_row_has_no_stride():
+    """In a child process: a stride times the element size that wraps to 0 has been divided by."""
+    _build.build()
+    code = """
+import sys; sys.path[:0] = [%r, %r]
+import ctypes, test_token_host as H, loss_scaled_adamw_gb300 as tl
+from loss_scaled_adamw_gb300 import losses
+lib = losses._load()
+lib.tl_dropout.restype, lib.tl_dropout.argtypes = ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]
+call = lambda **kw: lib.tl_dropout(ctypes.byref(H._dropout_args(rows=1, dtype=tl.TL_F32, **kw)), None)
+ok, far = (tl.TL_ECUDA, tl.TL_ESTATE), 1 << 62
+assert call(y=H.BASE + 8, ldx=far, ldy=far) == tl.TL_EINVAL           # overlaps x, 8 bytes on
+assert call(y=H.BASE + 396, ldx=far, ldy=far) == tl.TL_EINVAL
+assert call(y=H.BASE + 400, ldx=far, ldy=far) in ok                   # behind x
+assert call(y=H.BASE, ldx=far, ldy=far) in ok                         # in place
+assert call(y=H.BASE, ldx=120, ldy=100) in ok                         # in place, whatever the strides
+assert call(x=H.BASE + 4096, y=H.BASE, residual=H.BASE, ldr=1000, ldy=100) in ok
+assert call(x=H.BASE + 4096, y=H.BASE, residual=H.BASE + 4, ldr=100, ldy=100) == tl.TL_EINVAL
+assert call(y=H.BASE, ldx=99, ldy=100) == tl.TL_EINVAL
+""" % (ROOT, os.path.join(ROOT, "tests"))
+    subprocess.run([sys.executable, "-c", code], check=True, timeout=300)
