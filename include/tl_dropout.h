@@ -50,7 +50,7 @@ typedef struct {
     const void* x;
     const void* residual;   /* NULL: none */
     void* y;
-    int64_t rows, cols;     /* >= 0; rows * cols at most 2^43 */
+    int64_t rows, cols;     /* >= 0; rows * cols at most 2^40 */
     int64_t ldx, ldr, ldy;  /* elements, >= cols, < 2^40 where there are several rows (of one row not used) */
     const int64_t* key;     /* device: seed, ticket (0 .. 2^56 - 1) */
     uint32_t site;          /* which dropout of the model */

@@ -75,7 +75,7 @@ typedef struct tl_loss_ctx tl_loss_ctx;
 typedef struct {
     const void* data;
     int64_t rows;       /* >= 0 */
-    int64_t vocab;      /* 1 .. 2^30 */
+    int64_t vocab;      /* 1 .. 2^30; rows * vocab at most 2^40 */
     int64_t ld;         /* >= vocab, < 2^40 */
     int32_t dtype;
     float temperature;  /* > 0, normal; 1 for plain logits */

@@ -313,7 +313,7 @@ extern "C" int tl_dropout(const tl_dropout_args* args, tl_stream stream) {
     if (args == nullptr) return TL_EINVAL;
     const tl_dropout_args& g = *args;
     if (!float_type(g.dtype) || !(g.p >= 0.0f && g.p <= 1.0f)) return TL_EINVAL;
-    if (g.rows < 0 || g.cols < 0 || (g.rows > 0 && g.cols > (int64_t(1) << 43) / g.rows)) return TL_EINVAL;
+    if (g.rows < 0 || g.cols < 0 || too_many(g.rows, g.cols)) return TL_EINVAL;
     if (g.key == nullptr || !aligned(g.key, 8)) return TL_EINVAL;
     const int64_t size = type_bytes(g.dtype);
     if (g.rows > 0 && g.cols > 0) {

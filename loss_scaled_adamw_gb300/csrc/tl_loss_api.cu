@@ -60,6 +60,7 @@ int check_logits(tl_loss_ctx* ctx, const tl_logits* x) {
     if (x->vocab < 1 || x->vocab > (int64_t(1) << 30)) return fail(ctx, TL_EINVAL, "vocab must be in [1, 2^30]");
     if (x->ld < x->vocab || x->ld >= kMaxLd) return fail(ctx, TL_EINVAL, "ld must be in [vocab, 2^40)");
     if (x->rows > 0 && x->ld > kMaxSpan / x->rows) return fail(ctx, TL_EINVAL, "rows * ld must be at most 2^56");
+    if (too_many(x->rows, x->vocab)) return fail(ctx, TL_EINVAL, "rows * vocab must be at most 2^40");
     if (!(x->temperature >= FLT_MIN) || !std::isfinite(x->temperature) || !std::isnormal(1.0f / x->temperature))
         return fail(ctx, TL_EINVAL, "temperature must be positive, normal and have a normal reciprocal");
     if (x->rows > 0 && (x->data == nullptr || !aligned(x->data, uintptr_t(type_bytes(x->dtype)))))

@@ -16,6 +16,10 @@ inline int64_t type_bytes(int dt) { return dt == TL_F32 ? 4 : 2; }
 // the product is bounded too.
 constexpr int64_t kMaxLd = int64_t(1) << 40;
 constexpr int64_t kMaxSpan = int64_t(1) << 56;
+// Elements of a matrix: more than any device holds, and every kernel's grid is below 2^31 CTAs up to there (of at
+// least 1,024 elements each, or of whole rows).
+constexpr int64_t kMaxElements = int64_t(1) << 40;
+inline bool too_many(int64_t rows, int64_t cols) { return rows > 0 && cols > kMaxElements / rows; }
 
 // The memory a call touches: no output may share bytes with anything else.
 struct Spans {

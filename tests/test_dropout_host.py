@@ -1,4 +1,5 @@
 """Arguments of dropout on the CPU, where the checks that every call makes end before the device is asked."""
+import ctypes
 import os
 import subprocess
 import sys
@@ -7,6 +8,8 @@ import pytest
 
 pytest.importorskip("torch")
 
+import loss_scaled_adamw_gb300 as tl
+import test_token_host as H
 from loss_scaled_adamw_gb300 import _build
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -33,3 +36,15 @@ assert call(x=H.BASE + 4096, y=H.BASE, residual=H.BASE + 4, ldr=100, ldy=100) ==
 assert call(y=H.BASE, ldx=99, ldy=100) == tl.TL_EINVAL
 """ % (ROOT, os.path.join(ROOT, "tests"))
     subprocess.run([sys.executable, "-c", code], check=True, timeout=300)
+
+
+lib = H.lib
+
+
+def test_more_elements_than_a_grid_takes_are_refused(lib):
+    """As an argument, not as a failed launch."""
+    lib.tl_dropout.restype, lib.tl_dropout.argtypes = ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]
+    for cols, ok in ((1 << 20, True), ((1 << 20) + 1, False), (1 << 21, False), (1 << 23, False)):
+        args = H._dropout_args(rows=1 << 20, cols=cols, ldx=cols + 1, ldy=cols + 1, y=H.BASE + (1 << 46))
+        rc = lib.tl_dropout(ctypes.byref(args), None)
+        assert rc in (tl.TL_ECUDA, tl.TL_ESTATE) if ok else rc == tl.TL_EINVAL, cols
