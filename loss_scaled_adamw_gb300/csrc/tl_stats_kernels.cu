@@ -797,8 +797,9 @@ template <typename T, int B, int NT, int TV, int ST> struct TopShared {
 template <typename T, int B, int SB, int NT, int TV, int ST, int PER_SM>
 __global__ void __launch_bounds__(B + NT * SB, PER_SM) k_top(const StatsArgs a) {
     using Shared = TopShared<T, B, NT, TV, ST>;
-    constexpr int N = Vec<T>::N, nw = B / 32, G = Shared::G, NB = Shared::NB, HELD = B / SB, KEYS = HELD * 4, LOADS = 8;
+    constexpr int N = Vec<T>::N, nw = B / 32, G = Shared::G, NB = Shared::NB, HELD = B / SB, KEYS = HELD * 2, LOADS = 8;
     static_assert(nw <= 16 && 2 * NB + NT < 16, "parts of a row for half a warp, 16 named barriers");
+    static_assert(kMaxAlternatives <= B, "every thread's half of a row is a set of its own");
     __shared__ float4 wparts[NB][nw];
     __shared__ int counts[NT][2][8], nfound[NT], nlist[NT], nstage[NT];
     extern __shared__ __align__(128) uint4 ring[];
@@ -895,12 +896,12 @@ __global__ void __launch_bounds__(B + NT * SB, PER_SM) k_top(const StatsArgs a) 
             continue;
         }
         // The sets among which t is searched: the threads' vectors as wholes while there are twice as many
-        // as k (the k largest of 4 k sets have 1.15 k entries >= t, of 2 k 1.39 k), else 2 or 4 to a thread.
-        const int ss = 2 * a.k <= B ? 0 : a.k <= B ? 1 : 2;   // log2 of that
+        // as k (the k largest of 4 k sets have 1.15 k entries >= t, of 2 k 1.39 k), else halves of them.
+        const bool halves = 2 * a.k > B;
         float key[KEYS];   // of HELD threads
 #pragma unroll
         for (int i = 0; i < KEYS; ++i) key[i] = kNegInf;
-        if (ss == 0) {
+        if (!halves) {
 #pragma unroll
             for (int i = 0; i < HELD; ++i) key[i] = to_f(gm[G][tid + i * SB]);
         } else {
@@ -908,14 +909,13 @@ __global__ void __launch_bounds__(B + NT * SB, PER_SM) k_top(const StatsArgs a) 
             for (int i = 0; i < HELD; ++i)
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
-                    const float v = to_f(gm[g][tid + i * SB]);
-                    const int half = 4 * i + (g & 1), quarter = 4 * i + (g & 3);   // also where few groups are used
-                    if (ss == 1) key[half] = fmaxf(key[half], v); else key[quarter] = fmaxf(key[quarter], v);
+                    const int half = 2 * i + (g & 1);   // also where few groups are used
+                    key[half] = fmaxf(key[half], to_f(gm[g][tid + i * SB]));
                 }
         }
         auto count = [&](float v) {
             int c = 0;
-            if (ss == 0) {
+            if (!halves) {
 #pragma unroll
                 for (int i = 0; i < HELD; ++i) c += key[i] >= v;
             } else {
@@ -925,9 +925,9 @@ __global__ void __launch_bounds__(B + NT * SB, PER_SM) k_top(const StatsArgs a) 
             return sum_over<SB>(c, counts[team], turn, tid, bar);
         };
         uint32_t lo = kLeast<T>;
-        const bool full = a.k <= B && sums.least > kNegInf;   // each thread has a set from the least of their tops on
+        const bool full = sums.least > kNegInf;   // each thread has a set from the least of their tops on
         if (full) lo = rank_of<T>(sums.least);
-        const int from = full ? B << ss : count(logit_of(lo << Order<T>::kShift));
+        const int from = full ? (halves ? 2 * B : B) : count(logit_of(lo << Order<T>::kShift));
         if (from > a.k) lo = search_rank<T>(lo, from, row.M, a.k, count);
         const float least = logit_of(lo << Order<T>::kShift);
         // the groups from there on
