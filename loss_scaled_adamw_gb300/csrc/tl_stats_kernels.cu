@@ -74,7 +74,8 @@ __device__ __forceinline__ float min_nan(float v, float most) {
 }
 
 // log2(e) / temperature, and what its rounding left out: with fp32 logits it is counted too, where an entropy
-// shows it (temperature 0.7: off by 1.7e-7 of itself without, 6e-8 with it); 16-bit ones have no time for it.
+// shows it (temperature 0.72, whose scale rounds by 5e-8: off by 1.2e-7 of itself without, 7e-8 with it); 16-bit ones
+// have no time for it.
 struct Scale {
     float c2, low;
     __device__ __forceinline__ Scale(const StatsArgs& a) : c2(a.c2), low(a.c2_low) {}
