@@ -61,6 +61,9 @@ typedef struct {
 
 int tl_dropout(const tl_dropout_args* args, tl_stream stream);
 
+/* The text of the calling thread's last call of tl_dropout that returned an error ("" before the first). */
+const char* tl_dropout_last_error(void);
+
 #ifdef __cplusplus
 }
 #endif

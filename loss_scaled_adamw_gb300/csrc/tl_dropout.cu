@@ -299,6 +299,13 @@ template <typename T> cudaError_t launch_by(const DropoutArgs& a, cudaStream_t s
     return a.residual ? launch<T, true>(a, s) : launch<T, false>(a, s);
 }
 
+// The last error of the calling thread: a call has no context that would hold it.
+thread_local const char* last_error = "";
+int fail(int code, const char* text) {
+    last_error = text;
+    return code;
+}
+
 // One matrix operand: its address and stride.
 bool operand(const void* p, int64_t ld, int64_t rows, int64_t cols, int64_t size) {
     return p != nullptr && aligned(p, uintptr_t(size)) && ld >= cols && (rows == 1 || (ld < kMaxLd && ld <= kMaxSpan / rows));
@@ -309,26 +316,35 @@ bool operand(const void* p, int64_t ld, int64_t rows, int64_t cols, int64_t size
 
 using namespace tl;
 
+extern "C" const char* tl_dropout_last_error(void) { return last_error; }
+
 extern "C" int tl_dropout(const tl_dropout_args* args, tl_stream stream) {
-    if (args == nullptr) return TL_EINVAL;
+    if (args == nullptr) return fail(TL_EINVAL, "args must not be NULL");
     const tl_dropout_args& g = *args;
-    if (!float_type(g.dtype) || !(g.p >= 0.0f && g.p <= 1.0f)) return TL_EINVAL;
-    if (g.rows < 0 || g.cols < 0 || too_many(g.rows, g.cols)) return TL_EINVAL;
-    if (g.key == nullptr || !aligned(g.key, 8)) return TL_EINVAL;
+    if (!float_type(g.dtype)) return fail(TL_EINVAL, "dtype must be TL_F32, TL_BF16 or TL_F16");
+    if (!(g.p >= 0.0f && g.p <= 1.0f)) return fail(TL_EINVAL, "p must be in [0, 1]");
+    if (g.rows < 0 || g.cols < 0 || too_many(g.rows, g.cols))
+        return fail(TL_EINVAL, "rows and cols must be at least 0, rows * cols at most 2^40");
+    if (g.key == nullptr || !aligned(g.key, 8)) return fail(TL_EINVAL, "key must be an address aligned to 8 bytes");
     const int64_t size = type_bytes(g.dtype);
     if (g.rows > 0 && g.cols > 0) {
-        if (!operand(g.x, g.ldx, g.rows, g.cols, size) || !operand(g.y, g.ldy, g.rows, g.cols, size)) return TL_EINVAL;
-        if (g.residual != nullptr && !operand(g.residual, g.ldr, g.rows, g.cols, size)) return TL_EINVAL;
-        if (rows_clash(g.x, g.ldx, g.y, g.ldy, g.rows, g.cols, size)) return TL_EINVAL;
-        if (g.residual != nullptr && rows_clash(g.residual, g.ldr, g.y, g.ldy, g.rows, g.cols, size)) return TL_EINVAL;
+        if (!operand(g.x, g.ldx, g.rows, g.cols, size)) return fail(TL_EINVAL, "x must be an aligned address, ldx in [cols, 2^40)");
+        if (!operand(g.y, g.ldy, g.rows, g.cols, size)) return fail(TL_EINVAL, "y must be an aligned address, ldy in [cols, 2^40)");
+        if (g.residual != nullptr && !operand(g.residual, g.ldr, g.rows, g.cols, size))
+            return fail(TL_EINVAL, "residual must be an aligned address, ldr in [cols, 2^40)");
+        if (rows_clash(g.x, g.ldx, g.y, g.ldy, g.rows, g.cols, size))
+            return fail(TL_EINVAL, "y overlaps x without being the same tensor");
+        if (g.residual != nullptr && rows_clash(g.residual, g.ldr, g.y, g.ldy, g.rows, g.cols, size))
+            return fail(TL_EINVAL, "y overlaps residual without being the same tensor");
         Spans sp;
         sp.add(g.key, 16, false);
         sp.add(g.y, span_bytes(g.rows, g.cols, g.ldy, size), true);
-        if (sp.clash()) return TL_EINVAL;
+        if (sp.clash()) return fail(TL_EINVAL, "y overlaps key");
     }
     int dev = -1;
-    if (cudaGetDevice(&dev) != cudaSuccess) return TL_ECUDA;
-    if (dev != g.device) return TL_ESTATE;
+    const cudaError_t asked = cudaGetDevice(&dev);
+    if (asked != cudaSuccess) return fail(TL_ECUDA, cudaGetErrorString(asked));
+    if (dev != g.device) return fail(TL_ESTATE, "the current CUDA device is not the tensors' device");
     if (g.rows == 0 || g.cols == 0) return TL_OK;
     const uint32_t P = uint32_t(std::lrint(double(g.p) * 65536.0));
     DropoutArgs a{};
@@ -349,5 +365,5 @@ extern "C" int tl_dropout(const tl_dropout_args* args, tl_stream stream) {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e = g.dtype == TL_F32 ? launch_by<float>(a, s)
                           : g.dtype == TL_BF16 ? launch_by<__nv_bfloat16>(a, s) : launch_by<__half>(a, s);
-    return e == cudaSuccess ? TL_OK : TL_ECUDA;
+    return e == cudaSuccess ? TL_OK : fail(TL_ECUDA, cudaGetErrorString(e));
 }

@@ -20,7 +20,7 @@ import torch
 
 from . import TL_OK, TLError, losses
 
-DROPOUT_EXPORTED = ("tl_dropout",)
+DROPOUT_EXPORTED = ("tl_dropout", "tl_dropout_last_error")
 
 _vp, _i64, _i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
 
@@ -47,4 +47,6 @@ def tl_dropout(x, y, p: float, key, site: int = 0, residual=None, stream=None) -
     handle = losses._raw_stream(device) if stream is None else losses._any_stream(stream).value
     rc = bind.dropout(x, y, residual, key, site, p, handle, device)
     if rc != TL_OK:
-        raise TLError("tl_dropout", rc, losses._load().tl_status_string(rc).decode())
+        last_error = losses._load().tl_dropout_last_error
+        last_error.restype, last_error.argtypes = ctypes.c_char_p, []
+        raise TLError("tl_dropout", rc, last_error().decode())

@@ -48,3 +48,16 @@ def test_more_elements_than_a_grid_takes_are_refused(lib):
         args = H._dropout_args(rows=1 << 20, cols=cols, ldx=cols + 1, ldy=cols + 1, y=H.BASE + (1 << 46))
         rc = lib.tl_dropout(ctypes.byref(args), None)
         assert rc in (tl.TL_ECUDA, tl.TL_ESTATE) if ok else rc == tl.TL_EINVAL, cols
+
+
+def test_errors_name_the_argument(lib):
+    lib.tl_dropout.restype, lib.tl_dropout.argtypes = ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]
+    lib.tl_dropout_last_error.restype, lib.tl_dropout_last_error.argtypes = ctypes.c_char_p, []
+    far = H.BASE + (1 << 30)
+    for word, kw in ((b"dtype", dict(dtype=7)), (b"p must", dict(p=2.0)), (b"rows", dict(rows=-1)), (b"key must", dict(key=None)),
+                     (b"x must", dict(ldx=99)), (b"y must", dict(y=None)), (b"residual must", dict(residual=far + 1, ldr=100)),
+                     (b"y overlaps x", dict(y=H.BASE + 2)), (b"y overlaps residual", dict(residual=far + 2, ldr=100)),
+                     (b"y overlaps key", dict(key=far + 8))):
+        assert lib.tl_dropout(ctypes.byref(H._dropout_args(**kw)), None) == tl.TL_EINVAL
+        assert word in lib.tl_dropout_last_error(), (word, lib.tl_dropout_last_error())
+    assert lib.tl_dropout(None, None) == tl.TL_EINVAL and b"args" in lib.tl_dropout_last_error()
