@@ -194,7 +194,8 @@ typedef struct {
 } tl_token_saved;
 
 /* Log-probabilities, entropies and alternatives.  Per valid row, with log q the
- * log-softmax of the logits / temperature:
+ * log-softmax of the logits / temperature (for log-probabilities alone there is
+ * tl_token_logprob, which takes about as long):
  *   logp     = log q_target
  *   entropy  = -sum_j q_j log q_j
  *   top      the k largest logits, the largest first and the lower id first among
@@ -205,7 +206,8 @@ typedef struct {
  * and its ids -1.  A target of vocab or more makes logp NaN and nothing else; a row
  * without a softmax has NaN outputs and ids of -1.  Ids and their log-probabilities
  * are what tl_distill_loss takes as a teacher's entries: a common offset of the
- * logits leaves its softmax as it is, at temperature 1 here and any there. */
+ * logits leaves its softmax as it is, at temperature 1 here and any there.  (A row
+ * without a softmax, as an ignored one, is a row without entries there: kd 0.) */
 typedef struct {
     const int64_t* target;   /* NULL: every row is valid (logp must be NULL) */
     float* logp;             /* rows floats, or NULL */

@@ -791,8 +791,9 @@ template <typename T, int B, int NT, int TV, int ST> struct TopShared {
 // then one per team.
 //
 // What bounds it: the reading warps' instructions (four such warps to a scheduler, 59 % of the issue slots busy) and
-// the second look, a tenth of whose lines have left L2.  4,096 x 128,256 bf16, all rows valid: 171 us with 1
-// alternative, 200 with 64, 357 with 256 (the rows alone 155 at the copy rate); 2,048 of fp32 186 with 64.  Measured
+// the second look, a tenth of whose lines have left L2.  4,096 x 128,256 bf16, all rows valid: 170 us with 1
+// alternative, 199 with 64, 348 with 256 (the rows alone 155 at the copy rate); 2,048 of fp32 182 with 64.  Shorter
+// rows are bound by the two teams: 4,096 x 50,001 bf16 122 with 64 (66 without alternatives), 8,192 x 32,003 195 (86).  Measured
 // against it with 64: one team of four warps 206, 512 reading threads and teams of four 222, all warps choosing
 // between rows 266; full tiles without guards 219 (more code than the instruction caches hold).
 template <typename T, int B, int SB, int NT, int TV, int ST, int PER_SM>
@@ -1013,8 +1014,10 @@ cudaError_t top_launch(const StatsArgs& a, int sms, GroupCache& cache, cudaStrea
 
 // A team of W warps per row, four warps to a CTA or (W = 8) eight, NV vectors per thread.  The row is read
 // once; the entries are chosen where it is.  What bounds it: a row's chain of latencies (load, sums, search, candidates,
-// order) with 9 to 20 rows under way per SM.  bf16, without / with 8 alternatives: 16,384 x 1,000 16 / 30 us,
-// 16,384 x 8,192 55 / 109 (40 at the copy rate).
+// order) with few rows under way: with alternatives 20 per SM at 1,000 16-bit entries (one warp, 8 vectors), 6 at 8,192
+// (two warps, 16 vectors), without them 24 and 8.  bf16, without / with 8 alternatives: 16,384 x 1,000 16 / 30 us (5 at the
+// copy rate), 16,384 x 8,192 55 / 111 (40); fp16 16 / 34 and 53 / 128: with alternatives its forms spill 100 to 500 bytes
+// per thread, of widened entries that the search among entries keeps.
 template <typename T, int W, int NV, bool TOP>
 __global__ void __launch_bounds__(W > 4 ? 32 * W : 128, W > 4 ? 2 : NV > 8 ? (TOP ? 3 : 4) : NV > 4 ? (TOP ? 5 : 6) : TOP ? 7 : 8) k_held(const StatsArgs a) {
     constexpr int N = Vec<T>::N, SB = 32 * W, TEAMS = W < 4 ? 4 / W : 1, CAP = W == 1 ? 512 : kCandidates;
@@ -1189,7 +1192,7 @@ template <typename T, bool TOP> cudaError_t held(const StatsArgs& a, int places,
 // ---------------------------------------------------------------------------
 
 // Without alternatives: a group of 2^clog CTAs takes one row at a time, each CTA a contiguous share of the
-// row's vectors.  What bounds it: memory (4,096 x 128,256 bf16: 148 us, 7.1 TB/s of reads; one row 4.7 us).
+// row's vectors.  What bounds it: memory (4,096 x 128,256 bf16: 148 us, 7.1 TB/s of reads; one row 4.9 us).
 template <typename T, int B>
 __global__ void __launch_bounds__(B, 512 / B) k_stats(const StatsArgs a, const int clog) {
     constexpr int TV = 8, ST = 3, nw = B / 32;
@@ -1263,7 +1266,7 @@ __global__ void __launch_bounds__(B, 512 / B) k_stats(const StatsArgs a, const i
 
 // With alternatives, for few rows: each CTA of the group chooses the k largest entries of its share and hands
 // them, with its sums, to the first one, which puts all of them in order.  What bounds it: latency (one row of 128,256
-// bf16 9.4 us with 20 alternatives, 4.8 without any).
+// bf16 9.2 us with 20 alternatives, 4.9 without any).
 constexpr int kJoined = 4096;   // candidates of all CTAs
 template <int B> struct SpreadShared {
     static constexpr int G = 8;      // groups of vectors per thread
@@ -1474,7 +1477,7 @@ cudaError_t stats(const StatsArgs& a, int sms, GroupCache& cache, cudaStream_t s
 // With q_j = 2^(w_j - rest) of the saved statistics,
 //   dx_j = -step q_j (ga + gb (log q_j + H)) + [j = y] step ga = 2^w_j (A + B w_j) + [j = y] step ga:
 // one exponential and four multiplications or additions per element, every element on its own.  One
-// segment of a row per CTA.  What bounds it: memory (4,096 x 128,256 bf16, one row in eight ignored: 278 us, 7.1 TB/s;
+// segment of a row per CTA.  What bounds it: memory (4,096 x 128,256 bf16, one row in eight ignored: 281 us, 7.0 TB/s;
 // 1,500 x 32,003 fp32 55 us, 6.6 TB/s).
 template <typename T, int NV, int TB>
 __global__ void __launch_bounds__(TB) k_token_grad(const TokenGradArgs a, const int segs) {
